@@ -395,6 +395,237 @@ HM_API hm_status hm_block_fwd(const hm_block_args *a, void *workspace, size_t wo
  */
 HM_API hm_status hm_step_decode_noalloc(const hm_decode_args *a, hm_stream_t stream);
 
+/*
+ * Channel-wise gated recurrence (SSM article sec. 3.2: the step size through
+ * softplus, a diagonal A; sec. 4.2: the recurrence as a composition of affine
+ * maps).  Beside the matrix-state scan above: one scalar state per channel,
+ * its decay set by that channel's own gate.  For every channel c of D:
+ *
+ *   z_t = dt_t + dt_bias,   Delta_t = softplus(z_t),   a_t = exp(-Delta_t exp(A_log))
+ *   h_t = a_t h_{t-1} + beta_t x_t,   h_{-1} = h0 (or 0),   y_t = h_t
+ *   beta_t = 1 (HM_INPUT_PLAIN), Delta_t (HM_INPUT_STEP), sqrt(1 - a_t^2) (HM_INPUT_UNIT,
+ *            which keeps the state's variance at that of x)
+ *
+ * x, dt, y, and their gradients are [B, L, D] of io_dtype with channels
+ * contiguous and the other two strides given in elements (so x and dt may be
+ * slices of one projection's output); every other array is dense fp32.
+ * Pointers of these entry points need the alignment of their element type
+ * only; rows that start on 16-byte boundaries run the wide loads.  Outputs
+ * must not overlap inputs, except where said.
+ * lengths (device int32 [B], or NULL: L each) gives the tokens of each
+ * sequence of a padded batch, read as clamped to [0, L]: rows behind a
+ * sequence's end are neither read for its result nor written, the final state
+ * is the one after its last token, and a sequence of no tokens hands h0 on.
+ */
+typedef enum { HM_INPUT_PLAIN = 0, HM_INPUT_STEP = 1, HM_INPUT_UNIT = 2 } hm_input_scale;
+
+typedef struct {
+    int64_t B, L;              /* sequences, tokens of each (L = 0 copies the state) */
+    int64_t D;                 /* channels */
+    hm_dtype io_dtype;         /* dtype of x, dt and y */
+    int input_scale;           /* hm_input_scale */
+    const void *x, *dt;        /* [B, L, D] */
+    void *y;                   /* [B, L, D] (written), or NULL when h_out or states is wanted alone */
+    int64_t x_stride_b, x_stride_t;    /* elements between sequences, between tokens (>= D) */
+    int64_t dt_stride_b, dt_stride_t;
+    int64_t y_stride_b, y_stride_t;
+    const float *A_log;        /* [D] */
+    const float *dt_bias;      /* [D] or NULL (0) */
+    const float *h0;           /* [B, D] or NULL (0) */
+    const int32_t *lengths;    /* [B] or NULL */
+    float *h_out;              /* [B, D] final state, or NULL; may alias h0 */
+    void *states;              /* what hm_gated_scan_bwd needs of this pass (hm_gated_scan_states_size
+                                  bytes, 16-byte aligned), or NULL when no backward follows */
+    size_t states_bytes;
+} hm_gated_scan_args;
+
+/* Bytes of `states` (0 on invalid sizes).  Grows with B * L * D / 32. */
+HM_API size_t hm_gated_scan_states_size(const hm_gated_scan_args *a);
+
+HM_API hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t stream);
+
+/*
+ * hm_gated_scan_bwd -- gradients of sum(dy * y) + sum(dh_out * h_out).  With
+ * g_t = dy_t + a_{t+1} g_{t+1} (dh_out entering at the last token):
+ *   dx_t = beta_t g_t,   d log a_t = g_t (a_t h_{t-1} + x_t d beta_t / d log a_t),
+ *   d Delta_t = -exp(A_log) d log a_t (+ g_t x_t with HM_INPUT_STEP),
+ *   ddt_t = d Delta_t sigmoid(z_t),   d dt_bias = sum ddt_t,
+ *   dA_log = sum d log a_t log a_t,   dh0 = a_0 g_0.
+ * h_{t-1} is recomputed from `states`, so no forward output is read.  The
+ * sums over tokens are taken in a fixed order: the same call gives the same
+ * bits.  dx and ddt rows behind a sequence's end are not written.  Where
+ * log a_t is zero the HM_INPUT_UNIT term takes its limit, zero.
+ */
+typedef struct {
+    int64_t B, L, D;
+    hm_dtype io_dtype;         /* dtype of x, dt, dy, dx and ddt */
+    int input_scale;
+    const void *x, *dt;        /* the forward's inputs */
+    const void *dy;            /* [B, L, D] */
+    void *dx, *ddt;            /* [B, L, D] (written) */
+    int64_t x_stride_b, x_stride_t;
+    int64_t dt_stride_b, dt_stride_t;
+    int64_t dy_stride_b, dy_stride_t;
+    int64_t dx_stride_b, dx_stride_t;
+    int64_t ddt_stride_b, ddt_stride_t;
+    const float *A_log, *dt_bias;
+    const int32_t *lengths;    /* as in the forward */
+    const void *states;        /* as the forward of the same inputs wrote it */
+    size_t states_bytes;
+    const float *dh_out;       /* [B, D] gradient of the final state, or NULL (0) */
+    float *dA_log;             /* [D] (written) */
+    float *d_dt_bias;          /* [D] or NULL */
+    float *dh0;                /* [B, D] or NULL; may alias dh_out */
+    void *workspace;           /* >= hm_gated_scan_bwd_workspace_size() bytes, 256-B aligned */
+    size_t workspace_bytes;
+} hm_gated_scan_bwd_args;
+
+HM_API size_t hm_gated_scan_bwd_workspace_size(const hm_gated_scan_bwd_args *a);
+
+HM_API hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_stream_t stream);
+
+/* hm_gated_scan_step -- one token of B sequences: h_out = a h + beta x, y = h_out. */
+typedef struct {
+    int64_t B, D;
+    hm_dtype io_dtype;         /* dtype of x, dt, y */
+    int input_scale;
+    const void *x, *dt;        /* [B, D], rows x_stride / dt_stride elements apart */
+    void *y;                   /* [B, D] (written) */
+    int64_t x_stride, dt_stride, y_stride;
+    const float *A_log, *dt_bias;
+    const float *h;            /* [B, D] */
+    float *h_out;              /* [B, D] (written); may alias h */
+} hm_gated_step_args;
+
+HM_API hm_status hm_gated_scan_step(const hm_gated_step_args *a, hm_stream_t stream);
+
+/*
+ * hm_norm_gate_fwd -- the seam between two blocks of a decoder stack in one
+ * pass over the rows (HedgeMamba explainer sec. 5.1, 5.2: norms around the
+ * branch, the SiLU gate after the normalised output, the residual sum):
+ *
+ *   n = post ? norm(y; post_w, post_b) : y       the branch's output, normalised
+ *   m = gate ? n * SiLU(gate) : n
+ *   r_out = r + alpha * scale * m                 scaled residual sum
+ *   xn = norm(r_out; pre_w, pre_b)                the next block's input
+ *   norm(u; w, b) = u / sqrt(mean(u^2) + eps) * w + b               (HM_NORM_RMS)
+ *                 = (u - mean(u)) / sqrt(var(u) + eps) * w + b      (HM_NORM_LAYER, population variance)
+ *
+ * y, gate, r, r_out, xn: [rows, D] of io_dtype, rows a stride (elements) apart.
+ * The parameters are fp32 [D]; a NULL weight or scale is 1, a NULL shift 0.
+ * xn is formed from the sum before it is rounded to r_out's type.  r NULL is a
+ * zero residual; r_out or xn may be NULL when the other alone is wanted;
+ * r_out may alias r, and r_out or xn may alias y or gate (same stride).
+ * Pointers need the alignment of their element type; rows on 16-byte
+ * boundaries run the wide loads.  1 <= D <= 16384.
+ */
+typedef enum { HM_NORM_RMS = 0, HM_NORM_LAYER = 1 } hm_norm;
+
+typedef struct {
+    int64_t rows, D;
+    hm_dtype io_dtype;
+    int norm;                  /* hm_norm, of both norms */
+    int post;                  /* 0: y enters without a norm */
+    float eps;                 /* > 0 */
+    float alpha;               /* residual scale common to all channels */
+    const void *y, *gate, *r;  /* gate, r nullable */
+    void *r_out, *xn;          /* one of them nullable */
+    int64_t y_stride, gate_stride, r_stride, r_out_stride, xn_stride;
+    const float *scale;        /* [D] residual scale per channel, or NULL (1) */
+    const float *post_w, *post_b, *pre_w, *pre_b;   /* [D] or NULL */
+} hm_norm_gate_args;
+
+HM_API hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t stream);
+
+/*
+ * hm_norm_gate_bwd -- gradients of sum(dr_out * r_out) + sum(dxn * xn) with
+ * respect to y, gate, r and the parameters, from y, gate and the r_out that
+ * the forward stored (statistics are recomputed).  dxn NULL: xn was not used
+ * (r_out is then not read and may be NULL); dr_out NULL: r_out was not used
+ * after xn; not both.  Parameter gradients are fp32 [D], each nullable, summed
+ * over the rows in a fixed order.  dr may alias dr_out or dxn, dy may alias y,
+ * dgate may alias gate (same strides).
+ */
+typedef struct {
+    int64_t rows, D;
+    hm_dtype io_dtype;
+    int norm, post;
+    float eps, alpha;
+    const void *y, *gate, *r_out, *dr_out, *dxn;
+    void *dy, *dgate, *dr;     /* dy required; dgate required with gate; dr nullable */
+    int64_t y_stride, gate_stride, r_out_stride, dr_out_stride, dxn_stride;
+    int64_t dy_stride, dgate_stride, dr_stride;
+    const float *scale;
+    const float *post_w, *post_b, *pre_w;
+    float *dscale, *dpost_w, *dpost_b, *dpre_w, *dpre_b;
+    void *workspace;           /* >= hm_norm_gate_bwd_workspace_size() bytes, 256-B aligned */
+    size_t workspace_bytes;
+} hm_norm_gate_bwd_args;
+
+HM_API size_t hm_norm_gate_bwd_workspace_size(const hm_norm_gate_bwd_args *a);
+
+HM_API hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_t stream);
+
+/*
+ * hm_rotary -- rotary positions on queries and keys in one pass (HedgeMamba
+ * explainer sec. 5.1, 5.2: the GPT-NeoX / Pythia blocks the pages distil from
+ * rotate the first part of each head; HM_FLAG_ROPE above rotates the mixer's
+ * features).  For pair i < rot / 2 of a head, at angle phi = pos * theta_i:
+ *
+ *   (u, v) <- mscale * (u cos phi - v sin phi, u sin phi + v cos phi)
+ *   HM_ROTARY_HALF         pairs (i, i + rot / 2)
+ *   HM_ROTARY_INTERLEAVED  pairs (2 i, 2 i + 1)
+ *   theta_i = base^(-2 i / rot), then by `scaling`, for contexts `factor` times
+ *   as long as the model's own orig_len:
+ *   HM_ROTARY_PLAIN     theta_i
+ *   HM_ROTARY_LINEAR    theta_i / factor
+ *   HM_ROTARY_NTK       base * factor^(rot / (rot - 2)) in place of base (rot > 2)
+ *   HM_ROTARY_BY_PARTS  theta_i ((1 - w_i) / factor + w_i), w_i = (n_i - beta_slow) /
+ *                       (beta_fast - beta_slow) clamped to [0, 1], n_i = orig_len theta_i / (2 pi)
+ *                       the turns of pair i over orig_len
+ *
+ * The elements of a head behind rot are copied unchanged (left alone where
+ * the output is the input).  transpose != 0 applies the transposed matrix
+ * instead (angle -phi, same mscale): the gradient of the inputs from that of
+ * the outputs.  Angles are reduced modulo a full turn in 64-bit integers, so
+ * far positions keep their precision (any int64 position, negative ones too;
+ * the angle is off by at most |pos| theta_i 2^-48 plus 2^-26 of a turn).
+ * q [B, L, Hq, d] and k [B, L, Hk, d] of io_dtype, heads' elements contiguous,
+ * other strides in elements; Hk = 0 leaves k out.  positions: device int64,
+ * that of (b, t) at positions[b * pos_stride_b + t * pos_stride_t]; NULL:
+ * pos0 + t.  q_out / k_out may be q / k (same strides) and must not overlap
+ * them otherwise.  rot even, 2 <= rot <= d <= 1024.
+ */
+typedef enum { HM_ROTARY_HALF = 0, HM_ROTARY_INTERLEAVED = 1 } hm_rotary_layout;
+typedef enum {
+    HM_ROTARY_PLAIN = 0,
+    HM_ROTARY_LINEAR = 1,
+    HM_ROTARY_NTK = 2,
+    HM_ROTARY_BY_PARTS = 3
+} hm_rotary_scaling;
+
+typedef struct {
+    int64_t B, L;
+    int Hq, Hk, d, rot;
+    hm_dtype io_dtype;
+    int layout, scaling, transpose;
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_stride_b, q_stride_t, q_stride_h;
+    int64_t k_stride_b, k_stride_t, k_stride_h;
+    int64_t q_out_stride_b, q_out_stride_t, q_out_stride_h;
+    int64_t k_out_stride_b, k_out_stride_t, k_out_stride_h;
+    const int64_t *positions;  /* or NULL */
+    int64_t pos_stride_b, pos_stride_t;
+    int64_t pos0;              /* used without positions */
+    double base;               /* > 0 */
+    double factor;             /* > 0 (unused by HM_ROTARY_PLAIN) */
+    double orig_len, beta_slow, beta_fast;   /* HM_ROTARY_BY_PARTS: orig_len > 0, beta_fast > beta_slow */
+    double mscale;             /* finite */
+} hm_rotary_args;
+
+HM_API hm_status hm_rotary(const hm_rotary_args *a, hm_stream_t stream);
+
 /* Number of kernels this library has enqueued in this process so far (all
  * devices, all threads).  A diagnostic for launch accounting. */
 HM_API uint64_t hm_launch_count(void);

@@ -18,6 +18,10 @@ LIB_PATH = os.path.join(_HERE, "libhm.so")
 HM_OK, HM_ERR_INVALID_ARG, HM_ERR_UNSUPPORTED, HM_ERR_CUDA, HM_ERR_TIMEOUT, HM_ERR_DEVICE = range(6)
 HM_F32, HM_BF16 = 0, 1
 HM_FLAG_DT_SCALED_INPUT, HM_FLAG_PER_FEATURE_DECAY, HM_FLAG_ROPE = 1, 2, 4
+HM_INPUT_PLAIN, HM_INPUT_STEP, HM_INPUT_UNIT = 0, 1, 2
+HM_NORM_RMS, HM_NORM_LAYER = 0, 1
+HM_ROTARY_HALF, HM_ROTARY_INTERLEAVED = 0, 1
+HM_ROTARY_PLAIN, HM_ROTARY_LINEAR, HM_ROTARY_NTK, HM_ROTARY_BY_PARTS = 0, 1, 2, 3
 
 if not os.path.exists(LIB_PATH):
     raise ImportError("libhm.so is not built (%s); run __graft_entry__.build() or "
@@ -81,6 +85,64 @@ class BlockArgs(ctypes.Structure):
                 ("b_fc2", _P)]
 
 
+class GatedScanArgs(ctypes.Structure):
+    """Mirror of hm_gated_scan_args."""
+    _fields_ = [("B", _I64), ("L", _I64), ("D", _I64), ("io_dtype", _I), ("input_scale", _I), ("x", _P), ("dt", _P),
+                ("y", _P), ("x_stride_b", _I64), ("x_stride_t", _I64), ("dt_stride_b", _I64), ("dt_stride_t", _I64),
+                ("y_stride_b", _I64), ("y_stride_t", _I64), ("A_log", _P), ("dt_bias", _P), ("h0", _P),
+                ("lengths", _P), ("h_out", _P), ("states", _P), ("states_bytes", _SZ)]
+
+
+class GatedScanBwdArgs(ctypes.Structure):
+    """Mirror of hm_gated_scan_bwd_args."""
+    _fields_ = [("B", _I64), ("L", _I64), ("D", _I64), ("io_dtype", _I), ("input_scale", _I), ("x", _P), ("dt", _P),
+                ("dy", _P), ("dx", _P), ("ddt", _P), ("x_stride_b", _I64), ("x_stride_t", _I64),
+                ("dt_stride_b", _I64), ("dt_stride_t", _I64), ("dy_stride_b", _I64), ("dy_stride_t", _I64),
+                ("dx_stride_b", _I64), ("dx_stride_t", _I64), ("ddt_stride_b", _I64), ("ddt_stride_t", _I64),
+                ("A_log", _P), ("dt_bias", _P), ("lengths", _P), ("states", _P), ("states_bytes", _SZ),
+                ("dh_out", _P), ("dA_log", _P), ("d_dt_bias", _P), ("dh0", _P), ("workspace", _P),
+                ("workspace_bytes", _SZ)]
+
+
+class GatedStepArgs(ctypes.Structure):
+    """Mirror of hm_gated_step_args."""
+    _fields_ = [("B", _I64), ("D", _I64), ("io_dtype", _I), ("input_scale", _I), ("x", _P), ("dt", _P), ("y", _P),
+                ("x_stride", _I64), ("dt_stride", _I64), ("y_stride", _I64), ("A_log", _P), ("dt_bias", _P),
+                ("h", _P), ("h_out", _P)]
+
+
+class NormGateArgs(ctypes.Structure):
+    """Mirror of hm_norm_gate_args."""
+    _fields_ = [("rows", _I64), ("D", _I64), ("io_dtype", _I), ("norm", _I), ("post", _I), ("eps", ctypes.c_float),
+                ("alpha", ctypes.c_float), ("y", _P), ("gate", _P), ("r", _P), ("r_out", _P), ("xn", _P),
+                ("y_stride", _I64), ("gate_stride", _I64), ("r_stride", _I64), ("r_out_stride", _I64),
+                ("xn_stride", _I64), ("scale", _P), ("post_w", _P), ("post_b", _P), ("pre_w", _P), ("pre_b", _P)]
+
+
+class NormGateBwdArgs(ctypes.Structure):
+    """Mirror of hm_norm_gate_bwd_args."""
+    _fields_ = [("rows", _I64), ("D", _I64), ("io_dtype", _I), ("norm", _I), ("post", _I), ("eps", ctypes.c_float),
+                ("alpha", ctypes.c_float), ("y", _P), ("gate", _P), ("r_out", _P), ("dr_out", _P), ("dxn", _P),
+                ("dy", _P), ("dgate", _P), ("dr", _P), ("y_stride", _I64), ("gate_stride", _I64),
+                ("r_out_stride", _I64), ("dr_out_stride", _I64), ("dxn_stride", _I64), ("dy_stride", _I64),
+                ("dgate_stride", _I64), ("dr_stride", _I64), ("scale", _P), ("post_w", _P), ("post_b", _P),
+                ("pre_w", _P), ("dscale", _P), ("dpost_w", _P), ("dpost_b", _P), ("dpre_w", _P), ("dpre_b", _P),
+                ("workspace", _P), ("workspace_bytes", _SZ)]
+
+
+class RotaryArgs(ctypes.Structure):
+    """Mirror of hm_rotary_args."""
+    _fields_ = [("B", _I64), ("L", _I64), ("Hq", _I), ("Hk", _I), ("d", _I), ("rot", _I), ("io_dtype", _I),
+                ("layout", _I), ("scaling", _I), ("transpose", _I), ("q", _P), ("k", _P), ("q_out", _P),
+                ("k_out", _P), ("q_stride_b", _I64), ("q_stride_t", _I64), ("q_stride_h", _I64),
+                ("k_stride_b", _I64), ("k_stride_t", _I64), ("k_stride_h", _I64), ("q_out_stride_b", _I64),
+                ("q_out_stride_t", _I64), ("q_out_stride_h", _I64), ("k_out_stride_b", _I64),
+                ("k_out_stride_t", _I64), ("k_out_stride_h", _I64), ("positions", _P), ("pos_stride_b", _I64),
+                ("pos_stride_t", _I64), ("pos0", _I64), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_double), ("beta_slow", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("mscale", ctypes.c_double)]
+
+
 lib.hm_status_string.restype = ctypes.c_char_p
 lib.hm_status_string.argtypes = [_I]
 lib.hm_last_error_detail.restype = ctypes.c_char_p
@@ -112,6 +174,16 @@ lib.hm_scan_bwd.restype = _I
 lib.hm_scan_bwd.argtypes = [ctypes.POINTER(ScanBwdArgs), _P]
 lib.hm_scan_combine.restype = _I
 lib.hm_scan_combine.argtypes = [ctypes.POINTER(CombineArgs), _P]
+for _name, _cls in (("hm_gated_scan_fwd", GatedScanArgs), ("hm_gated_scan_bwd", GatedScanBwdArgs),
+                    ("hm_gated_scan_step", GatedStepArgs), ("hm_norm_gate_fwd", NormGateArgs),
+                    ("hm_norm_gate_bwd", NormGateBwdArgs), ("hm_rotary", RotaryArgs)):
+    getattr(lib, _name).restype = _I
+    getattr(lib, _name).argtypes = [ctypes.POINTER(_cls), _P]
+for _name, _cls in (("hm_gated_scan_states_size", GatedScanArgs),
+                    ("hm_gated_scan_bwd_workspace_size", GatedScanBwdArgs),
+                    ("hm_norm_gate_bwd_workspace_size", NormGateBwdArgs)):
+    getattr(lib, _name).restype = _SZ
+    getattr(lib, _name).argtypes = [ctypes.POINTER(_cls)]
 lib.hm_launch_count.restype = ctypes.c_uint64
 lib.hm_launch_count.argtypes = []
 lib.hm_get_device_error.restype = _I
@@ -123,7 +195,10 @@ EXPORTED = ("hm_status_string", "hm_last_error_detail", "hm_version", "hm_featma
             "hm_scan_workspace_size", "hm_scan_chunked_fwd", "hm_decode_workspace_size",
             "hm_step_decode", "hm_mixer_workspace_size", "hm_mixer_fwd", "hm_get_device_error",
             "hm_launch_count", "hm_step_decode_noalloc", "hm_selftest_wait_timeout", "hm_scan_combine",
-            "hm_scan_bwd_workspace_size", "hm_scan_bwd", "hm_block_workspace_size", "hm_block_fwd")
+            "hm_scan_bwd_workspace_size", "hm_scan_bwd", "hm_block_workspace_size", "hm_block_fwd",
+            "hm_gated_scan_states_size", "hm_gated_scan_fwd", "hm_gated_scan_bwd_workspace_size",
+            "hm_gated_scan_bwd", "hm_gated_scan_step", "hm_norm_gate_fwd", "hm_norm_gate_bwd_workspace_size",
+            "hm_norm_gate_bwd", "hm_rotary")
 
 
 class HMError(RuntimeError):
@@ -373,6 +448,232 @@ def hm_block_workspace_size(args: BlockArgs) -> int:
 def hm_block_fwd(args: BlockArgs, workspace, stream=None) -> None:
     nbytes = workspace.numel() * workspace.element_size()
     _check(lib.hm_block_fwd(ctypes.byref(args), _ptr(workspace), nbytes, _stream(stream)), "hm_block_fwd")
+
+
+# ---- the operators around the mixer: gated recurrence, seam between blocks, rotary positions.
+# Their helpers check what the C side cannot see (shapes, dtypes, devices) and raise ValueError.
+
+def _io(who: str, shape, like, **ts):
+    """Each given tensor has `like`'s dtype, this shape and contiguous elements in its last axis."""
+    for name, t in ts.items():
+        if t is None:
+            continue
+        if t.shape != shape:
+            raise ValueError("%s: %s has shape %s, not %s" % (who, name, tuple(t.shape), tuple(shape)))
+        if t.dtype != like.dtype:
+            raise ValueError("%s: %s is %s, not %s" % (who, name, t.dtype, like.dtype))
+        if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel() > 0:
+            raise ValueError("%s: the last axis of %s is not contiguous" % (who, name))
+
+
+def _dense(who: str, shape, dtype, **ts):
+    """Each given tensor is dense, of this shape and dtype."""
+    for name, t in ts.items():
+        if t is None:
+            continue
+        if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError("%s: %s must be a contiguous %s tensor of shape %s, got %s %s" % (
+                who, name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+
+
+def _one_device(who: str, *ts) -> None:
+    """All tensors on the current CUDA device: the kernels run there, on its stream."""
+    import torch
+    dev = -1
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("libhm works on device memory; got a CPU tensor")
+        if dev < 0:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError("%s: a tensor is on cuda:%d, the current device is cuda:%d" % (who, t.get_device(), dev))
+
+
+def gated_scan_args(x, dt, y, A_log, dt_bias=None, h0=None, h_out=None, lengths=None, input_scale: int = 0,
+                    states=None) -> GatedScanArgs:
+    """Fill an hm_gated_scan_args (x, dt, y: [B, L, D], channels contiguous; h0,
+    h_out: [B, D] fp32; lengths: [B] int32; A_log, dt_bias: [D] fp32)."""
+    import torch
+    who = "gated_scan_args"
+    B, L, D = x.shape
+    _io(who, x.shape, x, x=x, dt=dt, y=y)
+    _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias)
+    _dense(who, (B, D), torch.float32, h0=h0, h_out=h_out)
+    _dense(who, (B,), torch.int32, lengths=lengths)
+    _one_device(who, x, dt, y, A_log, dt_bias, h0, h_out, lengths, states)
+    ys = y.stride() if y is not None else (0, 0, 1)
+    xs, ds = x.stride(), dt.stride()
+    a = GatedScanArgs(B, L, D, _dtype_code(x), int(input_scale), _ptr(x), _ptr(dt), _ptr(y), xs[0], xs[1], ds[0],
+                      ds[1], ys[0], ys[1], _ptr(A_log), _ptr(dt_bias), _ptr(h0), _ptr(lengths), _ptr(h_out),
+                      _ptr(states), states.numel() * states.element_size() if states is not None else 0)
+    a._refs = (x, dt, y, A_log, dt_bias, h0, h_out, lengths, states)
+    return a
+
+
+def hm_gated_scan_states_size(args: GatedScanArgs) -> int:
+    return int(lib.hm_gated_scan_states_size(ctypes.byref(args)))
+
+
+def hm_gated_scan_fwd(args: GatedScanArgs, stream=None) -> None:
+    _check(lib.hm_gated_scan_fwd(ctypes.byref(args), _stream(stream)), "hm_gated_scan_fwd")
+
+
+def gated_scan_bwd_args(x, dt, dy, dx, ddt, A_log, dA_log, states, dt_bias=None, d_dt_bias=None, dh_out=None,
+                        dh0=None, lengths=None, input_scale: int = 0, workspace=None) -> GatedScanBwdArgs:
+    """Fill an hm_gated_scan_bwd_args (the forward's inputs and its `states`;
+    dy, dx, ddt: [B, L, D]; dh_out, dh0: [B, D] fp32; dA_log, d_dt_bias: [D] fp32)."""
+    import torch
+    who = "gated_scan_bwd_args"
+    B, L, D = x.shape
+    _io(who, x.shape, x, x=x, dt=dt, dy=dy, dx=dx, ddt=ddt)
+    _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias, dA_log=dA_log, d_dt_bias=d_dt_bias)
+    _dense(who, (B, D), torch.float32, dh_out=dh_out, dh0=dh0)
+    _dense(who, (B,), torch.int32, lengths=lengths)
+    _one_device(who, x, dt, dy, dx, ddt, A_log, dA_log, dt_bias, d_dt_bias, dh_out, dh0, lengths, states, workspace)
+    s = [v for t in (x, dt, dy, dx, ddt) for v in t.stride()[:2]]
+    a = GatedScanBwdArgs(B, L, D, _dtype_code(x), int(input_scale), _ptr(x), _ptr(dt), _ptr(dy), _ptr(dx), _ptr(ddt),
+                         *s, _ptr(A_log), _ptr(dt_bias), _ptr(lengths), _ptr(states),
+                         states.numel() * states.element_size() if states is not None else 0, _ptr(dh_out),
+                         _ptr(dA_log), _ptr(d_dt_bias), _ptr(dh0), _ptr(workspace),
+                         workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    a._refs = (x, dt, dy, dx, ddt, A_log, dA_log, states, dt_bias, d_dt_bias, dh_out, dh0, lengths, workspace)
+    return a
+
+
+def hm_gated_scan_bwd_workspace_size(args: GatedScanBwdArgs) -> int:
+    return int(lib.hm_gated_scan_bwd_workspace_size(ctypes.byref(args)))
+
+
+def hm_gated_scan_bwd(args: GatedScanBwdArgs, stream=None) -> None:
+    _check(lib.hm_gated_scan_bwd(ctypes.byref(args), _stream(stream)), "hm_gated_scan_bwd")
+
+
+def gated_step_args(x, dt, y, h, h_out, A_log, dt_bias=None, input_scale: int = 0) -> GatedStepArgs:
+    """Fill an hm_gated_step_args (x, dt, y: [B, D]; h, h_out: [B, D] fp32, may be one tensor)."""
+    import torch
+    who = "gated_step_args"
+    B, D = x.shape
+    _io(who, x.shape, x, x=x, dt=dt, y=y)
+    _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias)
+    _dense(who, (B, D), torch.float32, h=h, h_out=h_out)
+    _one_device(who, x, dt, y, h, h_out, A_log, dt_bias)
+    a = GatedStepArgs(B, D, _dtype_code(x), int(input_scale), _ptr(x), _ptr(dt), _ptr(y), x.stride(0), dt.stride(0),
+                      y.stride(0), _ptr(A_log), _ptr(dt_bias), _ptr(h), _ptr(h_out))
+    a._refs = (x, dt, y, h, h_out, A_log, dt_bias)
+    return a
+
+
+def hm_gated_scan_step(args: GatedStepArgs, stream=None) -> None:
+    _check(lib.hm_gated_scan_step(ctypes.byref(args), _stream(stream)), "hm_gated_scan_step")
+
+
+def _row_stride(t) -> int:
+    """Elements between the rows of [..., D], whose leading axes must be dense over one another."""
+    if t is None:
+        return 0
+    step = want = 0
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if not step:
+            step = want = st
+        elif st != want:
+            raise ValueError("rows of a tensor with strides %s are not equally spaced" % (tuple(t.stride()),))
+        want *= n
+    return step or t.shape[-1]
+
+
+def norm_gate_args(y, r, r_out, xn, gate=None, norm: int = 0, post: bool = True, eps: float = 1e-5,
+                   alpha: float = 1.0, scale=None, post_w=None, post_b=None, pre_w=None, pre_b=None) -> NormGateArgs:
+    """Fill an hm_norm_gate_args (y, gate, r, r_out, xn: [..., D]; parameters: [D] fp32)."""
+    import torch
+    who = "norm_gate_args"
+    D = y.shape[-1]
+    _io(who, y.shape, y, y=y, gate=gate, r=r, r_out=r_out, xn=xn)
+    _dense(who, (D,), torch.float32, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, pre_b=pre_b)
+    _one_device(who, y, gate, r, r_out, xn, scale, post_w, post_b, pre_w, pre_b)
+    a = NormGateArgs(y.numel() // D if D else 0, D, _dtype_code(y), int(norm), int(post), eps, alpha, _ptr(y),
+                     _ptr(gate), _ptr(r), _ptr(r_out), _ptr(xn), _row_stride(y), _row_stride(gate), _row_stride(r),
+                     _row_stride(r_out), _row_stride(xn), _ptr(scale), _ptr(post_w), _ptr(post_b), _ptr(pre_w),
+                     _ptr(pre_b))
+    a._refs = (y, gate, r, r_out, xn, scale, post_w, post_b, pre_w, pre_b)
+    return a
+
+
+def hm_norm_gate_fwd(args: NormGateArgs, stream=None) -> None:
+    _check(lib.hm_norm_gate_fwd(ctypes.byref(args), _stream(stream)), "hm_norm_gate_fwd")
+
+
+def norm_gate_bwd_args(y, r_out, dr_out, dxn, dy, dr, gate=None, dgate=None, norm: int = 0, post: bool = True,
+                       eps: float = 1e-5, alpha: float = 1.0, scale=None, post_w=None, post_b=None, pre_w=None,
+                       dscale=None, dpost_w=None, dpost_b=None, dpre_w=None, dpre_b=None,
+                       workspace=None) -> NormGateBwdArgs:
+    """Fill an hm_norm_gate_bwd_args (y, gate and the forward's r_out, the gradients of its
+    outputs, the gradient buffers; rows [..., D] of one dtype, parameters and theirs [D] fp32)."""
+    import torch
+    who = "norm_gate_bwd_args"
+    D = y.shape[-1]
+    _io(who, y.shape, y, y=y, gate=gate, r_out=r_out, dr_out=dr_out, dxn=dxn, dy=dy, dgate=dgate, dr=dr)
+    _dense(who, (D,), torch.float32, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, dscale=dscale,
+           dpost_w=dpost_w, dpost_b=dpost_b, dpre_w=dpre_w, dpre_b=dpre_b)
+    _one_device(who, y, gate, r_out, dr_out, dxn, dy, dgate, dr, scale, post_w, post_b, pre_w, dscale, dpost_w,
+                dpost_b, dpre_w, dpre_b, workspace)
+    a = NormGateBwdArgs(y.numel() // D if D else 0, D, _dtype_code(y), int(norm), int(post), eps, alpha, _ptr(y),
+                        _ptr(gate), _ptr(r_out), _ptr(dr_out), _ptr(dxn), _ptr(dy), _ptr(dgate), _ptr(dr),
+                        _row_stride(y), _row_stride(gate), _row_stride(r_out), _row_stride(dr_out), _row_stride(dxn),
+                        _row_stride(dy), _row_stride(dgate), _row_stride(dr), _ptr(scale), _ptr(post_w),
+                        _ptr(post_b), _ptr(pre_w), _ptr(dscale), _ptr(dpost_w), _ptr(dpost_b), _ptr(dpre_w),
+                        _ptr(dpre_b), _ptr(workspace),
+                        workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    a._refs = (y, r_out, dr_out, dxn, dy, dr, gate, dgate, scale, post_w, post_b, pre_w, dscale, dpost_w, dpost_b,
+               dpre_w, dpre_b, workspace)
+    return a
+
+
+def hm_norm_gate_bwd_workspace_size(args: NormGateBwdArgs) -> int:
+    return int(lib.hm_norm_gate_bwd_workspace_size(ctypes.byref(args)))
+
+
+def hm_norm_gate_bwd(args: NormGateBwdArgs, stream=None) -> None:
+    _check(lib.hm_norm_gate_bwd(ctypes.byref(args), _stream(stream)), "hm_norm_gate_bwd")
+
+
+def rotary_args(q, k, q_out, k_out, rot: int = 0, base: float = 10000.0, layout: int = 0, scaling: int = 0,
+                factor: float = 1.0, orig_len: float = 0.0, beta_slow: float = 1.0, beta_fast: float = 32.0,
+                mscale: float = 1.0, transpose: bool = False, positions=None, pos0: int = 0) -> RotaryArgs:
+    """Fill an hm_rotary_args (q, q_out: [B, L, Hq, d]; k, k_out: [B, L, Hk, d] or None; rot = 0
+    turns whole heads; positions: int64 [B, L], or [1, L] / [B, 1] shared along an axis of their own)."""
+    import torch
+    who = "rotary_args"
+    B, L, Hq, d = q.shape
+    Hk = 0
+    _io(who, q.shape, q, q=q, q_out=q_out)
+    qs, os = q.stride(), q_out.stride()
+    ks = ko = (0, 0, 0)
+    if k is not None:
+        Hk = k.shape[2]
+        _io(who, (B, L, Hk, d), q, k=k, k_out=k_out)
+        ks, ko = k.stride(), k_out.stride()
+    pb = pt = 0
+    if positions is not None:
+        if positions.dtype != torch.int64 or positions.dim() != 2 or positions.shape[0] not in (1, B) \
+                or positions.shape[1] not in (1, L):
+            raise ValueError("%s: positions must be int64 [B or 1, L or 1]" % who)
+        pb = positions.stride(0) if positions.shape[0] > 1 else 0
+        pt = positions.stride(1) if positions.shape[1] > 1 else 0
+    _one_device(who, q, k, q_out, k_out, positions)
+    a = RotaryArgs(B, L, Hq, Hk, d, int(rot) or d, _dtype_code(q), int(layout), int(scaling), int(transpose), _ptr(q),
+                   _ptr(k), _ptr(q_out), _ptr(k_out), qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], os[0], os[1], os[2],
+                   ko[0], ko[1], ko[2], _ptr(positions), pb, pt, int(pos0), base, factor, orig_len, beta_slow,
+                   beta_fast, mscale)
+    a._refs = (q, k, q_out, k_out, positions)
+    return a
+
+
+def hm_rotary(args: RotaryArgs, stream=None) -> None:
+    _check(lib.hm_rotary(ctypes.byref(args), _stream(stream)), "hm_rotary")
 
 
 def hm_launch_count() -> int:

@@ -50,6 +50,14 @@ hm_status fail(hm_status s, const char *fmt, ...) {
 
 void set_error_detail(const char *msg) { snprintf(g_detail, sizeof(g_detail), "%s", msg ? msg : ""); }
 
+hm_status fail_args(hm_status s, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_detail, sizeof(g_detail), fmt, ap);
+    va_end(ap);
+    return s;
+}
+
 namespace {
 
 hm_status cuda_fail(cudaError_t e, const char *what) {

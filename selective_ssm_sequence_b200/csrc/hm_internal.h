@@ -38,6 +38,8 @@ void count_launches(unsigned int n);
 
 // Sets the text hm_last_error_detail() returns on this host thread.
 void set_error_detail(const char *msg);
+// The same with a printf format; returns `s` (for `return fail_args(...)`).
+hm_status fail_args(hm_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 
 // ---------------------------------------------------------------- device helpers
 
