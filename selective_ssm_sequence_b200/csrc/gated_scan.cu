@@ -4,19 +4,27 @@
 //   z = dt + bias, Delta = softplus(z), a = exp(-Delta exp(A_log))
 //   h_t = a_t h_{t-1} + beta_t x_t
 //
-// A thread per (sequence, channel) walks the tokens.  The forward stores the
-// state in front of every 64th token; the backward walks the chunks from the
-// end, recomputes the 64 states of each from there and runs the adjoint
-// g_t = dy_t + a_{t+1} g_{t+1} back through them.
+// A run of tokens acts on the state as h -> A h + B with A the product of its
+// decays, and runs compose: (A2, B2) o (A1, B1) = (A2 A1, A2 B1 + B2).  A warp
+// takes 64 channels (two per lane) and a run of consecutive tokens, whose
+// decays and inputs stay in registers; the block's warps stand one behind the
+// other in time, the blocks of a cluster likewise, and the cluster walks the
+// sequence a window at a time.  In a window each warp forms its run's (A, B),
+// the block composes them through shared memory and hands its own to every
+// block of the cluster (st.async into their shared memory, counted by an
+// mbarrier there), and each warp, now knowing its entering state, runs its
+// tokens once more out of registers.  So each input is read once from HBM,
+// there is one launch and no scratch, and every sum has a fixed order.
 #include <type_traits>
 
-#include "hm_internal.h"
+#include "tc_common.cuh"
 
 namespace hm {
 
 namespace {
 
 constexpr int kChunk = 64;   // tokens between two stored states
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Gate {
     float z, step, la, a, beta;
@@ -39,26 +47,325 @@ __device__ __forceinline__ int64_t clamped_len(const int32_t *lengths, int64_t b
     return n < 0 ? 0 : n > L ? L : n;
 }
 
-template <typename T, int SCALE>
-__global__ void __launch_bounds__(128) gated_fwd_kernel(hm_gated_scan_args p) {
-    const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= p.D) return;
-    const float rate = expf(p.A_log[c]), bias = p.dt_bias ? p.dt_bias[c] : 0.f;
-    const int64_t nchunk = (p.L + kChunk - 1) / kChunk;
-    for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
-        const int64_t n = clamped_len(p.lengths, b, p.L);
-        const T *x = (const T *)p.x + b * p.x_stride_b + c;
-        const T *dt = (const T *)p.dt + b * p.dt_stride_b + c;
-        T *y = (T *)p.y + b * p.y_stride_b + c;
-        float h = p.h0 ? p.h0[b * p.D + c] : 0.f;
-        for (int64_t t = 0; t < n; ++t) {
-            if (p.states && t % kChunk == 0) ((float *)p.states)[(b * nchunk + t / kChunk) * p.D + c] = h;
-            const Gate g = gate_of<SCALE>(hm_ld(dt, t * p.dt_stride_t), bias, rate);
-            h = fmaf(g.a, h, g.beta * hm_ld(x, t * p.x_stride_t));
-            if (p.y) hm_st(y, t * p.y_stride_t, h);
-        }
-        if (p.h_out) p.h_out[b * p.D + c] = h;
+
+// ------------------------------------------------------------------ gates
+
+// A thread's two channels.  Fp32 data: the library's exp and log1p (the gates
+// are then good to a few units of the last place, and bandwidth still bounds
+// the kernel).  Bf16 data: the special-function unit limits the pass, so the
+// gates are formed in the log2 domain with three of its instructions per
+// element and packed fp32 arithmetic, keeping a relative error near 2^-22.
+struct Gate2 {
+    float2 a, beta, step, la, e;   // step and la in units of `unit` (1, or ln 2 for bf16); e = e^z (clamped)
+};
+
+struct ChanParams {
+    float2 bias, rate;             // bf16: bias / ln 2
+};
+
+template <typename T>
+__device__ __forceinline__ ChanParams chan_params(const float *A_log, const float *dt_bias, int64_t c, int64_t D) {
+    ChanParams p;
+    const int64_t c1 = c + 1 < D ? c + 1 : c;
+    p.rate = c < D ? make_float2(expf(A_log[c]), expf(A_log[c1])) : make_float2(0.f, 0.f);
+    p.bias = dt_bias && c < D ? make_float2(dt_bias[c], dt_bias[c1]) : make_float2(0.f, 0.f);
+    if (sizeof(T) == 2) p.bias = tc::mul2(p.bias, make_float2(kLog2e, kLog2e));
+    return p;
+}
+
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
+// minimum and maximum that hand a NaN on
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float rsq(float x) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// log2(1 + e) for 0 <= e <= 1/4: e times the degree-5 polynomial of least
+// maximal relative error (9e-9; fitted to log1p(e) / (e ln 2) there).
+__device__ __forceinline__ float2 log2_1p_small(float2 e) {
+    float2 p = tc::fma2(splat(-0.13323059678077698f), e, splat(0.26215097308158875f));
+    p = tc::fma2(p, e, splat(-0.3574727177619934f));
+    p = tc::fma2(p, e, splat(0.48071789741516113f));
+    p = tc::fma2(p, e, splat(-0.7213437557220459f));
+    p = tc::fma2(p, e, splat(1.4426950216293335f));
+    return tc::mul2(p, e);
+}
+
+// 1 - 2^w for -1/2 <= w <= 0: -w times a degree-4 polynomial fitted to
+// (2^w - 1) / w (relative error 1.3e-8).
+__device__ __forceinline__ float2 one_minus_exp2_small(float2 w) {
+    float2 p = tc::fma2(splat(0.0011544522130861878f), w, splat(0.009541281498968601f));
+    p = tc::fma2(p, w, splat(0.0554904080927372f));
+    p = tc::fma2(p, w, splat(0.2402256429195404f));
+    p = tc::fma2(p, w, splat(0.6931471824645996f));
+    return tc::mul2(p, make_float2(-w.x, -w.y));
+}
+
+// beta^2 = 1 - a^2, from the exponent where a is near one
+__device__ __forceinline__ float2 unit_sq(float2 la, float2 a) {
+    const float2 w = tc::add2(la, la);
+    const float2 s = one_minus_exp2_small(w);
+    return make_float2(w.x > -0.5f ? s.x : fmaf(-a.x, a.x, 1.f), w.y > -0.5f ? s.y : fmaf(-a.y, a.y, 1.f));
+}
+
+template <int SCALE>
+__device__ __forceinline__ Gate2 gates2(__nv_bfloat16, float2 dt, const ChanParams &p) {
+    Gate2 g;
+    const float2 z = tc::fma2(dt, splat(kLog2e), p.bias);       // z / ln 2
+    g.e = make_float2(tc::ex2_approx(min_nan(z.x, 120.f)), tc::ex2_approx(min_nan(z.y, 120.f)));
+    const float2 s = tc::add2(g.e, splat(1.f));
+    const float2 small = log2_1p_small(g.e);
+    // softplus(z) >= z, which takes over where e is clamped
+    g.step = make_float2(g.e.x < 0.25f ? small.x : max_nan(tc::lg2_approx(s.x), z.x),
+                         g.e.y < 0.25f ? small.y : max_nan(tc::lg2_approx(s.y), z.y));
+    g.la = tc::mul2(g.step, make_float2(-p.rate.x, -p.rate.y));
+    g.a = make_float2(tc::ex2_approx(g.la.x), tc::ex2_approx(g.la.y));
+    if (SCALE == HM_INPUT_STEP) g.beta = tc::mul2(g.step, splat(kLn2));
+    if (SCALE == HM_INPUT_UNIT) {
+        const float2 q = unit_sq(g.la, g.a);
+        // q = 0: the smallest normal number in its place under the root, so beta = 0
+        g.beta = make_float2(q.x * rsq(fmaxf(q.x, 1.1754944e-38f)), q.y * rsq(fmaxf(q.y, 1.1754944e-38f)));
     }
+    return g;
+}
+
+template <int SCALE>
+__device__ __forceinline__ Gate2 gates2(float, float2 dt, const ChanParams &p) {
+    const Gate x = gate_of<SCALE>(dt.x, p.bias.x, p.rate.x), y = gate_of<SCALE>(dt.y, p.bias.y, p.rate.y);
+    Gate2 g;
+    g.a = make_float2(x.a, y.a);
+    g.beta = make_float2(x.beta, y.beta);
+    g.step = make_float2(x.step, y.step);
+    g.la = make_float2(x.la, y.la);
+    g.e = make_float2(x.z, y.z);      // z itself: the backward takes its sigmoid
+    return g;
+}
+
+__device__ __forceinline__ float2 ld_pair(const __nv_bfloat16 *p) {
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ float2 ld_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ void st_pair(__nv_bfloat16 *p, float2 v) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
+}
+__device__ __forceinline__ void st_pair(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
+
+// ------------------------------------------------------------------ exchange
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes into block `rank`'s shared memory (at this block's address `dst`),
+// counted by that block's mbarrier `bar`
+__device__ __forceinline__ void st_async16(uint32_t dst, uint32_t bar, uint32_t rank, float4 v) {
+    asm volatile(
+        "{\n\t.reg .b32 d, b;\n\t"
+        "mapa.shared::cluster.u32 d, %0, %2;\n\t"
+        "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [d], {%3, %4, %5, %6}, [b];\n\t}" ::"r"(dst),
+        "r"(bar), "r"(rank), "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)),
+        "r"(__float_as_uint(v.w))
+        : "memory");
+}
+
+// Bounded wait of every thread of the block.  After a timeout the kernel keeps
+// its control flow (its loops are bounded and every block of a cluster must
+// reach the barriers), with short waits that let its own copies land.
+__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, DevErr err,
+                                         unsigned site) {
+    const uint32_t polls = *abort_flag ? 1u << 10 : tc::kWaitPolls;
+    for (uint32_t i = 0; i < polls; ++i)
+        if (tc::mbar_try_wait(bar, parity)) return;
+    *abort_flag = 1;
+    report_error(err, HM_ERR_TIMEOUT, KID_GATED_SCAN, site);
+}
+
+__device__ __forceinline__ float2 apply(const float4 &ab, float2 h) {   // (A, B, A, B) of two channels
+    return tc::fma2(make_float2(ab.x, ab.z), h, make_float2(ab.y, ab.w));
+}
+
+// ------------------------------------------------------------------ forward
+
+constexpr int kR = 16;        // tokens of a warp's run
+constexpr int kCols = 64;     // channels of a warp
+constexpr int kMaxWarps = 16;
+constexpr int kMaxCluster = 16;
+constexpr int kStages = 2;
+
+struct FwdArgs {
+    hm_gated_scan_args p;
+    int64_t groups;           // column groups of a sequence
+    int64_t nchunk;
+};
+
+// blockIdx.x = (sequence, column group, rank in cluster).  WIDE: tiles come by
+// TMA (two stages, the next window's in flight while this one is computed) and
+// rows leave as pairs; else element loads and stores.
+template <typename T, int SCALE, bool WIDE>
+__global__ void __launch_bounds__(kMaxWarps * 32)
+gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_constant__ CUtensorMap map_x, FwdArgs f,
+                 int cluster, DevErr err) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full[kStages], xbar[2];
+    __shared__ int abort_flag;
+    const hm_gated_scan_args &p = f.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int T_cta = nw * kR;
+    const int rank = cluster > 1 ? (int)cluster_rank() : 0;
+    const int64_t unit = blockIdx.x / cluster, b = unit / f.groups;
+    const int64_t c0 = (unit - b * f.groups) * kCols, c = c0 + 2 * lane;
+    const bool in0 = c < p.D, in1 = c + 1 < p.D;
+    const int64_t n = clamped_len(p.lengths, b, p.L);
+    const int64_t window = (int64_t)cluster * T_cta;
+    const int iters = (int)((n + window - 1) / window);
+    const int tile = T_cta * kCols;                // elements of one stage's tile
+    const uint32_t tile_bytes = (uint32_t)(tile * sizeof(T));
+    T *stage0 = reinterpret_cast<T *>(smem);
+    // by parity of the window: the warps' (A, B) per lane, then those of the cluster's blocks
+    float4 *agg0 = reinterpret_cast<float4 *>(smem + (WIDE ? kStages * 2 * tile_bytes : 0));
+    float4 *ctas0 = agg0 + 2 * nw * 32;
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < kStages; ++s) tc::mbar_init(&full[s], 1);
+        tc::mbar_init(&xbar[0], 1);
+        tc::mbar_init(&xbar[1], 1);
+        tc::mbar_fence_init();
+    }
+    auto fetch = [&](int it) {
+        const int s = it % kStages;
+        const int t = (int)((int64_t)it * window + (int64_t)rank * T_cta);
+        T *dst = stage0 + (int64_t)s * 2 * tile;
+        tc::mbar_arrive_expect_tx(&full[s], 2 * tile_bytes);
+        tc::tma_load_3d(dst, &map_dt, &full[s], (int)c0, t, (int)b);
+        tc::tma_load_3d(dst + tile, &map_x, &full[s], (int)c0, t, (int)b);
+    };
+    if (cluster > 1) cluster_sync();
+    else __syncthreads();
+    if (WIDE && threadIdx.x == 0)
+        for (int s = 0; s < kStages && s < iters; ++s) fetch(s);
+
+    const ChanParams par = chan_params<T>(p.A_log, p.dt_bias, c, p.D);
+    float2 h = make_float2(0.f, 0.f);              // state entering the window, the same in every warp
+    if (p.h0) {
+        if (in0) h.x = p.h0[b * p.D + c];
+        if (in1) h.y = p.h0[b * p.D + c + 1];
+    }
+    const T *dtp = (const T *)p.dt + b * p.dt_stride_b + c, *xp = (const T *)p.x + b * p.x_stride_b + c;
+    T *yp = (T *)p.y + b * p.y_stride_b + c;
+
+    for (int it = 0; it < iters; ++it) {
+        const int64_t t0 = (int64_t)it * window + (int64_t)rank * T_cta + warp * kR;
+        const int m = n - t0 >= kR ? kR : n > t0 ? (int)(n - t0) : 0;   // tokens of this run
+        float2 a[kR], u[kR];
+        float2 A = splat(1.f), B = splat(0.f);
+        if (WIDE) wait_bar(&full[it % kStages], (it / kStages) & 1, &abort_flag, err, 0);
+        if (m > 0) {
+            const T *sdt = stage0 + (int64_t)(it % kStages) * 2 * tile + (warp * kR) * kCols + 2 * lane;
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                float2 dv = splat(0.f), xv = splat(0.f);
+                if (WIDE) {
+                    dv = ld_pair(sdt + i * kCols);
+                    xv = ld_pair(sdt + tile + i * kCols);
+                } else if (i < m) {
+                    const int64_t od = (t0 + i) * p.dt_stride_t, ox = (t0 + i) * p.x_stride_t;
+                    if (in0) dv.x = hm_ld(dtp, od), xv.x = hm_ld(xp, ox);
+                    if (in1) dv.y = hm_ld(dtp, od + 1), xv.y = hm_ld(xp, ox + 1);
+                }
+                const Gate2 g = gates2<SCALE>(T(), dv, par);
+                a[i] = g.a;
+                u[i] = SCALE == HM_INPUT_PLAIN ? xv : tc::mul2(xv, g.beta);
+            }
+            if (m < kR) {                          // tokens behind the end change nothing
+#pragma unroll
+                for (int i = 0; i < kR; ++i)
+                    if (i >= m) a[i] = splat(1.f), u[i] = splat(0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {
+                A = tc::mul2(A, a[i]);
+                B = tc::fma2(a[i], B, u[i]);
+            }
+        }
+        float4 *agg = agg0 + (it & 1) * nw * 32 + lane, *ctas = ctas0 + (it & 1) * cluster * 32 + lane;
+        agg[warp * 32] = make_float4(A.x, B.x, A.y, B.y);
+        __syncthreads();                           // aggregates written; this window's tiles read
+        if (WIDE && threadIdx.x == 0 && it + kStages < iters) fetch(it + kStages);
+        float2 pa = splat(1.f), pb = splat(0.f);   // the block's runs in front of this warp's
+        float2 ba, bb;                             // all the block's runs
+        {
+            float2 qa = splat(1.f), qb = splat(0.f);
+            for (int w = 0; w < nw; ++w) {
+                if (w == warp) pa = qa, pb = qb;
+                const float4 v = agg[w * 32];
+                qb = apply(v, qb);
+                qa = tc::mul2(qa, make_float2(v.x, v.z));
+            }
+            ba = qa;
+            bb = qb;
+        }
+        float2 hin = h;
+        if (cluster > 1) {
+            if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&xbar[it & 1], (uint32_t)cluster * 512u);
+            for (int r = warp; r < cluster; r += nw)
+                st_async16(tc::smem_u32(ctas + rank * 32), tc::smem_u32(&xbar[it & 1]), (uint32_t)r,
+                           make_float4(ba.x, bb.x, ba.y, bb.y));
+            wait_bar(&xbar[it & 1], (it >> 1) & 1, &abort_flag, err, 1);
+            for (int r = 0; r < cluster; ++r) {
+                if (r == rank) hin = h;
+                h = apply(ctas[r * 32], h);
+            }
+        } else {
+            h = tc::fma2(ba, h, bb);
+        }
+        hin = tc::fma2(pa, hin, pb);
+        if (m > 0) {
+            if (p.states && t0 % kChunk == 0 && in0) {
+                float *st = (float *)p.states + (b * f.nchunk + t0 / kChunk) * p.D + c;
+                st[0] = hin.x;
+                if (in1) st[1] = hin.y;
+            }
+            if (p.y) {
+                T *yr = yp + t0 * p.y_stride_t;
+#pragma unroll
+                for (int i = 0; i < kR; ++i) {
+                    hin = tc::fma2(a[i], hin, u[i]);
+                    if (i < m) {
+                        if (WIDE) {
+                            if (in0) st_pair(yr, hin);
+                        } else {
+                            if (in0) hm_st(yr, 0, hin.x);
+                            if (in1) hm_st(yr, 1, hin.y);
+                        }
+                    }
+                    yr += p.y_stride_t;
+                }
+            }
+        }
+    }
+    if (p.h_out && rank == 0 && warp == 0) {
+        if (in0) p.h_out[b * p.D + c] = h.x;
+        if (in1) p.h_out[b * p.D + c + 1] = h.y;
+    }
+    if (cluster > 1) cluster_sync();               // no block leaves while others may still write to it
 }
 
 // partial sums of dA_log and d_dt_bias: part[(b * 2 + k) * D + c]
@@ -149,8 +456,8 @@ hm_status check_common(const char *who, int64_t B, int64_t L, int64_t D, hm_dtyp
     if (B < 0 || L < 0 || D < 1)
         return fail_args(HM_ERR_INVALID_ARG, "%s: bad sizes B=%lld L=%lld D=%lld", who, (long long)B, (long long)L,
                          (long long)D);
-    if (B > (1LL << 31) || L > (1LL << 31) || D > (1LL << 24) || B * L > (1LL << 40))
-        return fail_args(HM_ERR_UNSUPPORTED, "%s: need B, L <= 2^31, B L <= 2^40 and D <= 2^24", who);
+    if (B > (1LL << 30) || L > (1LL << 30) || D > (1LL << 24) || B * L > (1LL << 40))
+        return fail_args(HM_ERR_UNSUPPORTED, "%s: need B, L <= 2^30, B L <= 2^40 and D <= 2^24", who);
     return HM_OK;
 }
 
@@ -269,16 +576,101 @@ extern "C" size_t hm_gated_scan_states_size(const hm_gated_scan_args *a) {
     return states_bytes(a->B, a->L, a->D);
 }
 
+namespace hm {
+namespace {
+
+// [B, L, D] as (channel, token, sequence), tiles of 64 channels x `rows` tokens
+bool tile_map(CUtensorMap *m, hm_dtype t, const void *base, int64_t B, int64_t L, int64_t D, int64_t sb, int64_t st,
+              int rows) {
+    const size_t es = esize(t);
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)L, (uint64_t)B};
+    const uint64_t strides[2] = {(uint64_t)(L > 1 ? st : (D + 7) / 8 * 8) * es, (uint64_t)(B > 1 ? sb : (D + 7) / 8 * 8) * es};
+    const uint32_t box[3] = {kCols, (uint32_t)rows, 1};
+    return tc::make_tmap(m, t == HM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, 3,
+                         dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// rows that TMA can fetch: 16-byte aligned base and strides
+bool tma_rows(const void *p, size_t es, int64_t B, int64_t L, int64_t sb, int64_t st) {
+    return aligned_to(p, 16) && (L <= 1 || st * (int64_t)es % 16 == 0) && (B <= 1 || sb * (int64_t)es % 16 == 0);
+}
+// rows that can be read or written as channel pairs
+bool pair_rows(const void *p, size_t es, int64_t B, int64_t L, int64_t sb, int64_t st) {
+    return aligned_to(p, 2 * es) && (L <= 1 || st % 2 == 0) && (B <= 1 || sb % 2 == 0);
+}
+
+struct Split {
+    int warps, cluster;
+};
+
+// The tokens are split over blocks of a cluster until about four blocks of
+// four warps stand on each SM, then over more warps per block.
+Split split_of(int64_t units, int64_t L, size_t es) {
+    const int64_t runs = (L + kR - 1) / kR;
+    Split s{4, 1};
+    while (s.warps > 1 && s.warps / 2 >= runs) s.warps /= 2;
+    while (s.cluster < kMaxCluster && units * s.cluster * 2 <= 148 * 4 && (int64_t)s.warps * s.cluster < runs)
+        s.cluster *= 2;
+    const int most = es == 4 ? kMaxWarps / 2 : kMaxWarps;      // two stages of a window's tiles in shared memory
+    while (s.warps < most && units * s.cluster * s.warps * 2 <= 148 * 16 && (int64_t)s.warps * s.cluster < runs)
+        s.warps *= 2;
+    return s;
+}
+
+template <typename K, typename... A>
+cudaError_t launch_cluster(K kernel, int64_t units, Split sp, size_t smem, cudaStream_t s, A... args) {
+    cudaError_t e = tc::ensure_smem_limit(kernel, (int)smem);
+    if (e != cudaSuccess) return e;
+    if (sp.cluster > 8) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(units * sp.cluster));
+    cfg.blockDim = dim3(sp.warps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = sp.cluster;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+}  // namespace
+}  // namespace hm
+
 extern "C" hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t stream) {
     set_error_detail("");
     HM_TRY(check_fwd(a));
     if (a->B == 0) return HM_OK;
-    const dim3 grid((unsigned)((a->D + 127) / 128), grid_y(a->B));
+    FwdArgs f{*a, (a->D + kCols - 1) / kCols, (a->L + kChunk - 1) / kChunk};
+    const int64_t units = a->B * f.groups;
+    const size_t es = esize(a->io_dtype);
+    const Split sp = split_of(units, a->L, es);
+    if (units * sp.cluster > 0x7fffffffLL)
+        return fail_args(HM_ERR_UNSUPPORTED, "gated_scan_fwd: B * D / 64 is too large");
+    CUtensorMap mdt{}, mx{};
+    const int rows = sp.warps * kR;
+    const bool wide = a->L > 0 && a->D % 2 == 0 && tma_rows(a->x, es, a->B, a->L, a->x_stride_b, a->x_stride_t) &&
+                      tma_rows(a->dt, es, a->B, a->L, a->dt_stride_b, a->dt_stride_t) &&
+                      (!a->y || pair_rows(a->y, es, a->B, a->L, a->y_stride_b, a->y_stride_t)) &&
+                      tile_map(&mdt, a->io_dtype, a->dt, a->B, a->L, a->D, a->dt_stride_b, a->dt_stride_t, rows) &&
+                      tile_map(&mx, a->io_dtype, a->x, a->B, a->L, a->D, a->x_stride_b, a->x_stride_t, rows);
+    const DevErr err{device_error_word()};
     const cudaError_t e = by_type(a->io_dtype, a->input_scale, [&](auto *t, auto sc) {
         using T = std::remove_pointer_t<decltype(t)>;
-        gated_fwd_kernel<T, decltype(sc)::value><<<grid, 128, 0, (cudaStream_t)stream>>>(*a);
-        count_launches(1);
-        return cudaGetLastError();
+        constexpr int S = decltype(sc)::value;
+        const size_t tiles = (size_t)kStages * 2 * rows * kCols * sizeof(T);
+        const size_t swap = (size_t)2 * (sp.warps + sp.cluster) * 512;
+        return wide ? launch_cluster(gated_fwd_kernel<T, S, true>, units, sp, tiles + swap, (cudaStream_t)stream, mdt,
+                                     mx, f, sp.cluster, err)
+                    : launch_cluster(gated_fwd_kernel<T, S, false>, units, sp, swap, (cudaStream_t)stream, mdt, mx, f,
+                                     sp.cluster, err);
     });
     return e == cudaSuccess ? HM_OK : fail_args(HM_ERR_CUDA, "gated_scan_fwd launch: %s", cudaGetErrorString(e));
 }

@@ -29,6 +29,7 @@ enum KernelId : unsigned int {
     KID_CONV = 9,
     KID_SELFTEST = 10,
     KID_BWD_DW_TC = 11,
+    KID_GATED_SCAN = 12,
 };
 
 unsigned int *device_error_word();  // address of this device's error word (host)
