@@ -50,117 +50,145 @@ __device__ __forceinline__ int64_t clamped_len(const int32_t *lengths, int64_t b
 
 // ------------------------------------------------------------------ gates
 
-// A thread's two channels.  Fp32 data: the library's exp and log1p (the gates
-// are then good to a few units of the last place, and bandwidth still bounds
-// the kernel).  Bf16 data: the special-function unit limits the pass, so the
-// gates are formed in the log2 domain with three of its instructions per
-// element and packed fp32 arithmetic, keeping a relative error near 2^-22.
-struct Gate2 {
-    float2 a, beta, step, la, e;   // step and la in units of `unit` (1, or ln 2 for bf16); e = e^z (clamped)
+// A thread's two channels as one packed register pair.  Held as 64 bits from
+// the load on, so that the packed instructions find their operands in place.
+struct F2 {
+    unsigned long long v;
 };
-
-struct ChanParams {
-    float2 bias, rate;             // bf16: bias / ln 2
-};
-
-template <typename T>
-__device__ __forceinline__ ChanParams chan_params(const float *A_log, const float *dt_bias, int64_t c, int64_t D) {
-    ChanParams p;
-    const int64_t c1 = c + 1 < D ? c + 1 : c;
-    p.rate = c < D ? make_float2(expf(A_log[c]), expf(A_log[c1])) : make_float2(0.f, 0.f);
-    p.bias = dt_bias && c < D ? make_float2(dt_bias[c], dt_bias[c1]) : make_float2(0.f, 0.f);
-    if (sizeof(T) == 2) p.bias = tc::mul2(p.bias, make_float2(kLog2e, kLog2e));
-    return p;
-}
-
-__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
-// minimum and maximum that hand a NaN on
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+__device__ __forceinline__ F2 pk(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
     return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+__device__ __forceinline__ float2 un(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
     return r;
+}
+__device__ __forceinline__ F2 splat(float v) { return pk(v, v); }
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 ex2(F2 a) {
+    const float2 u = un(a);
+    return pk(tc::ex2_approx(u.x), tc::ex2_approx(u.y));
 }
 __device__ __forceinline__ float rsq(float x) {
     float r;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-
-// log2(1 + e) for 0 <= e <= 1/4: e times the degree-5 polynomial of least
-// maximal relative error (9e-9; fitted to log1p(e) / (e ln 2) there).
-__device__ __forceinline__ float2 log2_1p_small(float2 e) {
-    float2 p = tc::fma2(splat(-0.13323059678077698f), e, splat(0.26215097308158875f));
-    p = tc::fma2(p, e, splat(-0.3574727177619934f));
-    p = tc::fma2(p, e, splat(0.48071789741516113f));
-    p = tc::fma2(p, e, splat(-0.7213437557220459f));
-    p = tc::fma2(p, e, splat(1.4426950216293335f));
-    return tc::mul2(p, e);
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-// 1 - 2^w for -1/2 <= w <= 0: -w times a degree-4 polynomial fitted to
-// (2^w - 1) / w (relative error 1.3e-8).
-__device__ __forceinline__ float2 one_minus_exp2_small(float2 w) {
-    float2 p = tc::fma2(splat(0.0011544522130861878f), w, splat(0.009541281498968601f));
-    p = tc::fma2(p, w, splat(0.0554904080927372f));
-    p = tc::fma2(p, w, splat(0.2402256429195404f));
-    p = tc::fma2(p, w, splat(0.6931471824645996f));
-    return tc::mul2(p, make_float2(-w.x, -w.y));
+// The issue slots and the special-function unit bound this pass as much as
+// HBM does, so the gates are formed in the log2 domain with two
+// special-function instructions per element (three with HM_INPUT_UNIT) and
+// packed fp32 arithmetic:
+//   e = 2^-|z'|, z' = z / ln 2;   softplus(z) / ln 2 = max(z', 0) + log2(1 + e)
+// with log2(1 + e) = e P(e) a polynomial on the whole [0, 1], which keeps its
+// relative precision where e (and the decay's distance from one) is tiny.  No
+// input overflows: an infinite z gives e = 0, and a NaN goes through e.
+struct ChanParams {
+    F2 bias, nrate;                   // bias / ln 2; -exp(A_log)
+};
+struct Gate2 {
+    F2 z, e, step, la, a;             // z, step and la divided by ln 2
+};
+
+__device__ __forceinline__ ChanParams chan_params(const float *A_log, const float *dt_bias, int64_t c, int64_t D) {
+    const int64_t c1 = c + 1 < D ? c + 1 : c;
+    ChanParams p;
+    float r0 = c < D ? expf(A_log[c]) : 0.f, r1 = c < D ? expf(A_log[c1]) : 0.f;
+    if (r0 > 3e38f) r0 = 3e38f;       // finite, so that a step of zero decays nothing
+    if (r1 > 3e38f) r1 = 3e38f;
+    p.nrate = pk(-r0, -r1);
+    p.bias = (dt_bias && c < D ? pk(dt_bias[c], dt_bias[c1]) : splat(0.f)) * splat(kLog2e);
+    return p;
 }
 
-// beta^2 = 1 - a^2, from the exponent where a is near one
-__device__ __forceinline__ float2 unit_sq(float2 la, float2 a) {
-    const float2 w = tc::add2(la, la);
-    const float2 s = one_minus_exp2_small(w);
-    return make_float2(w.x > -0.5f ? s.x : fmaf(-a.x, a.x, 1.f), w.y > -0.5f ? s.y : fmaf(-a.y, a.y, 1.f));
+// log2(1 + e) / e for 0 <= e <= 1: the degree-7 polynomial of least maximal
+// relative error (2e-7; fitted to log1p(e) / (e ln 2)).
+__device__ __forceinline__ F2 log2_1p_over(F2 e) {
+    F2 p = fma(splat(-0.012319470755755901f), e, splat(0.06360787898302078f));
+    p = fma(p, e, splat(-0.15535186231136322f));
+    p = fma(p, e, splat(0.25600969791412354f));
+    p = fma(p, e, splat(-0.35339483618736267f));
+    p = fma(p, e, splat(0.48006370663642883f));
+    p = fma(p, e, splat(-0.7213100790977478f));
+    return fma(p, e, splat(1.4426947832107544f));
 }
 
-template <int SCALE>
-__device__ __forceinline__ Gate2 gates2(__nv_bfloat16, float2 dt, const ChanParams &p) {
+__device__ __forceinline__ Gate2 gates2(F2 dt, const ChanParams &p) {
     Gate2 g;
-    const float2 z = tc::fma2(dt, splat(kLog2e), p.bias);       // z / ln 2
-    g.e = make_float2(tc::ex2_approx(min_nan(z.x, 120.f)), tc::ex2_approx(min_nan(z.y, 120.f)));
-    const float2 s = tc::add2(g.e, splat(1.f));
-    const float2 small = log2_1p_small(g.e);
-    // softplus(z) >= z, which takes over where e is clamped
-    g.step = make_float2(g.e.x < 0.25f ? small.x : max_nan(tc::lg2_approx(s.x), z.x),
-                         g.e.y < 0.25f ? small.y : max_nan(tc::lg2_approx(s.y), z.y));
-    g.la = tc::mul2(g.step, make_float2(-p.rate.x, -p.rate.y));
-    g.a = make_float2(tc::ex2_approx(g.la.x), tc::ex2_approx(g.la.y));
-    if (SCALE == HM_INPUT_STEP) g.beta = tc::mul2(g.step, splat(kLn2));
-    if (SCALE == HM_INPUT_UNIT) {
-        const float2 q = unit_sq(g.la, g.a);
-        // q = 0: the smallest normal number in its place under the root, so beta = 0
-        g.beta = make_float2(q.x * rsq(fmaxf(q.x, 1.1754944e-38f)), q.y * rsq(fmaxf(q.y, 1.1754944e-38f)));
-    }
+    g.z = fma(dt, splat(kLog2e), p.bias);
+    const float2 z = un(g.z);
+    g.e = pk(tc::ex2_approx(-fabsf(z.x)), tc::ex2_approx(-fabsf(z.y)));
+    g.step = fma(log2_1p_over(g.e), g.e, pk(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+    g.la = g.step * p.nrate;
+    g.a = ex2(g.la);
     return g;
 }
 
-template <int SCALE>
-__device__ __forceinline__ Gate2 gates2(float, float2 dt, const ChanParams &p) {
-    const Gate x = gate_of<SCALE>(dt.x, p.bias.x, p.rate.x), y = gate_of<SCALE>(dt.y, p.bias.y, p.rate.y);
-    Gate2 g;
-    g.a = make_float2(x.a, y.a);
-    g.beta = make_float2(x.beta, y.beta);
-    g.step = make_float2(x.step, y.step);
-    g.la = make_float2(x.la, y.la);
-    g.e = make_float2(x.z, y.z);      // z itself: the backward takes its sigmoid
-    return g;
+// beta^2 = 1 - a^2 = 1 - 2^w, w = 2 la.  Above -1/2 it is -w times a degree-4
+// polynomial fitted to (2^w - 1) / w (relative error 1.3e-8), since the
+// difference would lose the bits of a step that hardly decays.
+__device__ __forceinline__ F2 unit_sq(const Gate2 &g) {
+    const F2 w = g.la + g.la;
+    F2 p = fma(splat(-0.0011544522130861878f), w, splat(-0.009541281498968601f));
+    p = fma(p, w, splat(-0.0554904080927372f));
+    p = fma(p, w, splat(-0.2402256429195404f));
+    p = fma(p, w, splat(-0.6931471824645996f));
+    const float2 s = un(p * w), u = un(w), a = un(g.a);
+    return pk(u.x > -0.5f ? s.x : fmaf(-a.x, a.x, 1.f), u.y > -0.5f ? s.y : fmaf(-a.y, a.y, 1.f));
 }
 
-__device__ __forceinline__ float2 ld_pair(const __nv_bfloat16 *p) {
-    const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+// beta x
+template <int SCALE>
+__device__ __forceinline__ F2 input2(const Gate2 &g, F2 x) {
+    if (SCALE == HM_INPUT_PLAIN) return x;
+    if (SCALE == HM_INPUT_STEP) return x * (g.step * splat(kLn2));
+    const float2 q = un(unit_sq(g));
+    return x * pk(sqrt_approx(q.x), sqrt_approx(q.y));
 }
-__device__ __forceinline__ float2 ld_pair(const float *p) { return *reinterpret_cast<const float2 *>(p); }
-__device__ __forceinline__ void st_pair(__nv_bfloat16 *p, float2 v) {
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y);
+
+// two channels of a row as loaded: one word of bf16, two of fp32
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint32_t *>(p); }
+    __device__ __forceinline__ void set(float x, float y) { w = tc::pack_bf16x2(x, y); }
+    __device__ __forceinline__ F2 pair() const { return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+};
+template <>
+struct Raw<float> {
+    float2 w;
+    __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const float2 *>(p); }
+    __device__ __forceinline__ void set(float x, float y) { w = make_float2(x, y); }
+    __device__ __forceinline__ F2 pair() const { return pk(w.x, w.y); }
+};
+__device__ __forceinline__ void st_pair(__nv_bfloat16 *p, F2 v) {
+    const float2 u = un(v);
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(u.x, u.y);
 }
-__device__ __forceinline__ void st_pair(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
+__device__ __forceinline__ void st_pair(float *p, F2 v) { *reinterpret_cast<float2 *>(p) = un(v); }
 
 // ------------------------------------------------------------------ exchange
 
@@ -174,31 +202,40 @@ __device__ __forceinline__ void cluster_sync() {
 }
 // 16 bytes into block `rank`'s shared memory (at this block's address `dst`),
 // counted by that block's mbarrier `bar`
-__device__ __forceinline__ void st_async16(uint32_t dst, uint32_t bar, uint32_t rank, float4 v) {
+// a run's (A, B), 16 bytes per lane
+struct __align__(16) Map2 {
+    F2 A, B;
+};
+__device__ __forceinline__ F2 apply(const Map2 &m, F2 h) { return fma(m.A, h, m.B); }
+// m, then n
+__device__ __forceinline__ Map2 then(const Map2 &m, const Map2 &n) { return {m.A * n.A, fma(n.A, m.B, n.B)}; }
+
+// 16 bytes into block `rank`'s shared memory (at this block's address `dst`),
+// counted by that block's mbarrier `bar`
+__device__ __forceinline__ void st_async16(uint32_t dst, uint32_t bar, uint32_t rank, const Map2 &m) {
     asm volatile(
         "{\n\t.reg .b32 d, b;\n\t"
         "mapa.shared::cluster.u32 d, %0, %2;\n\t"
         "mapa.shared::cluster.u32 b, %1, %2;\n\t"
-        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [d], {%3, %4, %5, %6}, [b];\n\t}" ::"r"(dst),
-        "r"(bar), "r"(rank), "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)),
-        "r"(__float_as_uint(v.w))
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [d], {%3, %4}, [b];\n\t}" ::"r"(dst),
+        "r"(bar), "r"(rank), "l"(m.A.v), "l"(m.B.v)
         : "memory");
 }
 
 // Bounded wait of every thread of the block.  After a timeout the kernel keeps
 // its control flow (its loops are bounded and every block of a cluster must
 // reach the barriers), with short waits that let its own copies land.
-__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, DevErr err,
-                                         unsigned site) {
+__device__ __noinline__ void wait_bar_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, DevErr err,
+                                           unsigned site) {
     const uint32_t polls = *abort_flag ? 1u << 10 : tc::kWaitPolls;
     for (uint32_t i = 0; i < polls; ++i)
         if (tc::mbar_try_wait(bar, parity)) return;
     *abort_flag = 1;
     report_error(err, HM_ERR_TIMEOUT, KID_GATED_SCAN, site);
 }
-
-__device__ __forceinline__ float2 apply(const float4 &ab, float2 h) {   // (A, B, A, B) of two channels
-    return tc::fma2(make_float2(ab.x, ab.z), h, make_float2(ab.y, ab.w));
+__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, DevErr err,
+                                         unsigned site) {
+    if (!tc::mbar_try_wait(bar, parity)) wait_bar_slow(bar, parity, abort_flag, err, site);
 }
 
 // ------------------------------------------------------------------ forward
@@ -215,13 +252,16 @@ struct FwdArgs {
     int64_t nchunk;
 };
 
-// blockIdx.x = (sequence, column group, rank in cluster).  WIDE: tiles come by
-// TMA (two stages, the next window's in flight while this one is computed) and
-// rows leave as pairs; else element loads and stores.
+// blockIdx.x = (sequence, column group, rank in cluster).  WIDE: tiles come
+// and go by TMA (two stages, so the window after the next is on its way while
+// one is computed; results leave through two staging tiles), except the
+// window in which a sequence ends; else element loads and stores.
+//
+// 128 threads and about 125 registers: four blocks on an SM.
 template <typename T, int SCALE, bool WIDE>
 __global__ void __launch_bounds__(kMaxWarps * 32)
-gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_constant__ CUtensorMap map_x, FwdArgs f,
-                 int cluster, DevErr err) {
+gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_constant__ CUtensorMap map_x,
+                 const __grid_constant__ CUtensorMap map_y, FwdArgs f, int cluster, DevErr err) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[kStages], xbar[2];
     __shared__ int abort_flag;
@@ -232,15 +272,15 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     const int64_t unit = blockIdx.x / cluster, b = unit / f.groups;
     const int64_t c0 = (unit - b * f.groups) * kCols, c = c0 + 2 * lane;
     const bool in0 = c < p.D, in1 = c + 1 < p.D;
-    const int64_t n = clamped_len(p.lengths, b, p.L);
-    const int64_t window = (int64_t)cluster * T_cta;
-    const int iters = (int)((n + window - 1) / window);
-    const int tile = T_cta * kCols;                // elements of one stage's tile
+    const int n = (int)clamped_len(p.lengths, b, p.L);          // L is at most 2^30
+    const int window = cluster * T_cta;
+    const int iters = (int)(((unsigned)n + (unsigned)window - 1u) / (unsigned)window);
+    const int tile = T_cta * kCols;                // elements of a tile
     const uint32_t tile_bytes = (uint32_t)(tile * sizeof(T));
-    T *stage0 = reinterpret_cast<T *>(smem);
-    // by parity of the window: the warps' (A, B) per lane, then those of the cluster's blocks
-    float4 *agg0 = reinterpret_cast<float4 *>(smem + (WIDE ? kStages * 2 * tile_bytes : 0));
-    float4 *ctas0 = agg0 + 2 * nw * 32;
+    T *stage0 = reinterpret_cast<T *>(smem), *out0 = stage0 + 2 * kStages * tile;
+    // by parity of the window: the warps' maps per lane, then those of the cluster's blocks
+    Map2 *agg0 = reinterpret_cast<Map2 *>(smem + (WIDE ? (2 * kStages + 2) * tile_bytes : 0));
+    Map2 *ctas0 = agg0 + 2 * nw * 32;
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -249,112 +289,126 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         tc::mbar_init(&xbar[1], 1);
         tc::mbar_fence_init();
     }
+    auto tile_start = [&](int it) { return it * window + rank * T_cta; };
     auto fetch = [&](int it) {
         const int s = it % kStages;
-        const int t = (int)((int64_t)it * window + (int64_t)rank * T_cta);
-        T *dst = stage0 + (int64_t)s * 2 * tile;
+        T *dst = stage0 + s * 2 * tile;
         tc::mbar_arrive_expect_tx(&full[s], 2 * tile_bytes);
-        tc::tma_load_3d(dst, &map_dt, &full[s], (int)c0, t, (int)b);
-        tc::tma_load_3d(dst + tile, &map_x, &full[s], (int)c0, t, (int)b);
+        tc::tma_load_3d(dst, &map_dt, &full[s], (int)c0, tile_start(it), (int)b);
+        tc::tma_load_3d(dst + tile, &map_x, &full[s], (int)c0, tile_start(it), (int)b);
+    };
+    // a tile that lies whole in front of the sequence's end leaves by TMA
+    auto whole = [&](int it) { return WIDE && p.y && tile_start(it) + T_cta <= n; };
+    auto send = [&](int it) {
+        tc::tma_store_3d(&map_y, out0 + (it & 1) * tile, (int)c0, tile_start(it), (int)b);
+        tc::bulk_commit();
     };
     if (cluster > 1) cluster_sync();
     else __syncthreads();
     if (WIDE && threadIdx.x == 0)
         for (int s = 0; s < kStages && s < iters; ++s) fetch(s);
 
-    const ChanParams par = chan_params<T>(p.A_log, p.dt_bias, c, p.D);
-    float2 h = make_float2(0.f, 0.f);              // state entering the window, the same in every warp
-    if (p.h0) {
-        if (in0) h.x = p.h0[b * p.D + c];
-        if (in1) h.y = p.h0[b * p.D + c + 1];
-    }
+    const ChanParams par = chan_params(p.A_log, p.dt_bias, c, p.D);
+    F2 h = splat(0.f);                             // state entering the window, the same in every warp
+    if (p.h0) h = pk(in0 ? p.h0[b * p.D + c] : 0.f, in1 ? p.h0[b * p.D + c + 1] : 0.f);
     const T *dtp = (const T *)p.dt + b * p.dt_stride_b + c, *xp = (const T *)p.x + b * p.x_stride_b + c;
     T *yp = (T *)p.y + b * p.y_stride_b + c;
 
     for (int it = 0; it < iters; ++it) {
-        const int64_t t0 = (int64_t)it * window + (int64_t)rank * T_cta + warp * kR;
-        const int m = n - t0 >= kR ? kR : n > t0 ? (int)(n - t0) : 0;   // tokens of this run
-        float2 a[kR], u[kR];
-        float2 A = splat(1.f), B = splat(0.f);
+        const int t0 = tile_start(it) + warp * kR;
+        const int m = min(max(n - t0, 0), kR);     // tokens of this run
+        Map2 run[kR];                              // the run's composition up to each token
+        Map2 all = {splat(1.f), splat(0.f)};
         if (WIDE) wait_bar(&full[it % kStages], (it / kStages) & 1, &abort_flag, err, 0);
         if (m > 0) {
-            const T *sdt = stage0 + (int64_t)(it % kStages) * 2 * tile + (warp * kR) * kCols + 2 * lane;
+            Raw<T> dv[kR], xv[kR];
+            const T *sdt = stage0 + (it % kStages) * 2 * tile + (warp * kR) * kCols + 2 * lane;
+            if (WIDE) {
 #pragma unroll
-            for (int i = 0; i < kR; ++i) {
-                float2 dv = splat(0.f), xv = splat(0.f);
-                if (WIDE) {
-                    dv = ld_pair(sdt + i * kCols);
-                    xv = ld_pair(sdt + tile + i * kCols);
-                } else if (i < m) {
-                    const int64_t od = (t0 + i) * p.dt_stride_t, ox = (t0 + i) * p.x_stride_t;
-                    if (in0) dv.x = hm_ld(dtp, od), xv.x = hm_ld(xp, ox);
-                    if (in1) dv.y = hm_ld(dtp, od + 1), xv.y = hm_ld(xp, ox + 1);
+                for (int i = 0; i < kR; ++i) {
+                    dv[i].load(sdt + i * kCols);
+                    xv[i].load(sdt + tile + i * kCols);
                 }
-                const Gate2 g = gates2<SCALE>(T(), dv, par);
-                a[i] = g.a;
-                u[i] = SCALE == HM_INPUT_PLAIN ? xv : tc::mul2(xv, g.beta);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kR; ++i) {
+                    float d0 = 0.f, d1 = 0.f, x0 = 0.f, x1 = 0.f;
+                    if (i < m) {
+                        const int64_t od = (int64_t)(t0 + i) * p.dt_stride_t, ox = (int64_t)(t0 + i) * p.x_stride_t;
+                        if (in0) d0 = hm_ld(dtp, od), x0 = hm_ld(xp, ox);
+                        if (in1) d1 = hm_ld(dtp, od + 1), x1 = hm_ld(xp, ox + 1);
+                    }
+                    dv[i].set(d0, d1);
+                    xv[i].set(x0, x1);
+                }
             }
-            if (m < kR) {                          // tokens behind the end change nothing
+            if (m < kR) {        // tokens behind the end change nothing: a step of zero, no input
 #pragma unroll
                 for (int i = 0; i < kR; ++i)
-                    if (i >= m) a[i] = splat(1.f), u[i] = splat(0.f);
+                    if (i >= m) dv[i].set(-INFINITY, -INFINITY), xv[i].set(0.f, 0.f);
             }
+            F2 sum = splat(0.f);
 #pragma unroll
             for (int i = 0; i < kR; ++i) {
-                A = tc::mul2(A, a[i]);
-                B = tc::fma2(a[i], B, u[i]);
+                const Gate2 g = gates2(dv[i].pair(), par);
+                sum = sum + g.la;
+                all.B = fma(g.a, all.B, input2<SCALE>(g, xv[i].pair()));
+                all.A = all.A * g.a;
+                run[i] = all;
             }
+            // the whole run's decay from the sum of the exponents: the rounding of the
+            // single decays then does not build up over more than a run
+            all.A = ex2(sum);
         }
-        float4 *agg = agg0 + (it & 1) * nw * 32 + lane, *ctas = ctas0 + (it & 1) * cluster * 32 + lane;
-        agg[warp * 32] = make_float4(A.x, B.x, A.y, B.y);
-        __syncthreads();                           // aggregates written; this window's tiles read
-        if (WIDE && threadIdx.x == 0 && it + kStages < iters) fetch(it + kStages);
-        float2 pa = splat(1.f), pb = splat(0.f);   // the block's runs in front of this warp's
-        float2 ba, bb;                             // all the block's runs
-        {
-            float2 qa = splat(1.f), qb = splat(0.f);
-            for (int w = 0; w < nw; ++w) {
-                if (w == warp) pa = qa, pb = qb;
-                const float4 v = agg[w * 32];
-                qb = apply(v, qb);
-                qa = tc::mul2(qa, make_float2(v.x, v.z));
-            }
-            ba = qa;
-            bb = qb;
+        Map2 *agg = agg0 + (it & 1) * nw * 32 + lane, *ctas = ctas0 + (it & 1) * cluster * 32 + lane;
+        agg[warp * 32] = all;
+        if (WIDE && threadIdx.x == 0) tc::bulk_wait_read_all();   // the staging tile of two windows ago has left
+        __syncthreads();                           // aggregates written; this window's tiles read; the last's staged
+        if (WIDE && threadIdx.x == 0) {
+            if (it > 0 && whole(it - 1)) send(it - 1);
+            if (it + kStages < iters) fetch(it + kStages);
         }
-        float2 hin = h;
+        // the block's runs in front of this warp's, then all of them
+        Map2 q = {splat(1.f), splat(0.f)};
+        int w = 0;
+        for (; w < warp; ++w) q = then(q, agg[w * 32]);
+        const Map2 before = q;
+        for (; w < nw; ++w) q = then(q, agg[w * 32]);
+        F2 hin = h;
         if (cluster > 1) {
             if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&xbar[it & 1], (uint32_t)cluster * 512u);
             for (int r = warp; r < cluster; r += nw)
-                st_async16(tc::smem_u32(ctas + rank * 32), tc::smem_u32(&xbar[it & 1]), (uint32_t)r,
-                           make_float4(ba.x, bb.x, ba.y, bb.y));
+                st_async16(tc::smem_u32(ctas + rank * 32), tc::smem_u32(&xbar[it & 1]), (uint32_t)r, q);
             wait_bar(&xbar[it & 1], (it >> 1) & 1, &abort_flag, err, 1);
-            for (int r = 0; r < cluster; ++r) {
-                if (r == rank) hin = h;
-                h = apply(ctas[r * 32], h);
-            }
+            int r = 0;
+            for (; r < rank; ++r) h = apply(ctas[r * 32], h);
+            hin = h;
+            for (; r < cluster; ++r) h = apply(ctas[r * 32], h);
         } else {
-            h = tc::fma2(ba, h, bb);
+            h = apply(q, h);
         }
-        hin = tc::fma2(pa, hin, pb);
+        hin = apply(before, hin);
         if (m > 0) {
             if (p.states && t0 % kChunk == 0 && in0) {
                 float *st = (float *)p.states + (b * f.nchunk + t0 / kChunk) * p.D + c;
-                st[0] = hin.x;
-                if (in1) st[1] = hin.y;
+                st[0] = un(hin).x;
+                if (in1) st[1] = un(hin).y;
             }
-            if (p.y) {
+            if (whole(it)) {
+                T *so = out0 + (it & 1) * tile + (warp * kR) * kCols + 2 * lane;
+#pragma unroll
+                for (int i = 0; i < kR; ++i) {
+                    st_pair(so + i * kCols, apply(run[i], hin));
+                }
+                tc::fence_proxy_async_smem();
+            } else if (p.y) {
                 T *yr = yp + t0 * p.y_stride_t;
 #pragma unroll
                 for (int i = 0; i < kR; ++i) {
-                    hin = tc::fma2(a[i], hin, u[i]);
                     if (i < m) {
-                        if (WIDE) {
-                            if (in0) st_pair(yr, hin);
-                        } else {
-                            if (in0) hm_st(yr, 0, hin.x);
-                            if (in1) hm_st(yr, 1, hin.y);
-                        }
+                        const float2 v = un(apply(run[i], hin));
+                        if (in0) hm_st(yr, 0, v.x);
+                        if (in1) hm_st(yr, 1, v.y);
                     }
                     yr += p.y_stride_t;
                 }
@@ -362,8 +416,15 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         }
     }
     if (p.h_out && rank == 0 && warp == 0) {
-        if (in0) p.h_out[b * p.D + c] = h.x;
-        if (in1) p.h_out[b * p.D + c + 1] = h.y;
+        if (in0) p.h_out[b * p.D + c] = un(h).x;
+        if (in1) p.h_out[b * p.D + c + 1] = un(h).y;
+    }
+    if (WIDE) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            if (iters > 0 && whole(iters - 1)) send(iters - 1);
+            tc::bulk_wait_all();
+        }
     }
     if (cluster > 1) cluster_sync();               // no block leaves while others may still write to it
 }
@@ -594,10 +655,6 @@ bool tile_map(CUtensorMap *m, hm_dtype t, const void *base, int64_t B, int64_t L
 bool tma_rows(const void *p, size_t es, int64_t B, int64_t L, int64_t sb, int64_t st) {
     return aligned_to(p, 16) && (L <= 1 || st * (int64_t)es % 16 == 0) && (B <= 1 || sb * (int64_t)es % 16 == 0);
 }
-// rows that can be read or written as channel pairs
-bool pair_rows(const void *p, size_t es, int64_t B, int64_t L, int64_t sb, int64_t st) {
-    return aligned_to(p, 2 * es) && (L <= 1 || st % 2 == 0) && (B <= 1 || sb % 2 == 0);
-}
 
 struct Split {
     int warps, cluster;
@@ -654,23 +711,24 @@ extern "C" hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t 
     const Split sp = split_of(units, a->L, es);
     if (units * sp.cluster > 0x7fffffffLL)
         return fail_args(HM_ERR_UNSUPPORTED, "gated_scan_fwd: B * D / 64 is too large");
-    CUtensorMap mdt{}, mx{};
+    CUtensorMap mdt{}, mx{}, my{};
     const int rows = sp.warps * kR;
-    const bool wide = a->L > 0 && a->D % 2 == 0 && tma_rows(a->x, es, a->B, a->L, a->x_stride_b, a->x_stride_t) &&
+    const bool wide = a->L > 0 && tma_rows(a->x, es, a->B, a->L, a->x_stride_b, a->x_stride_t) &&
                       tma_rows(a->dt, es, a->B, a->L, a->dt_stride_b, a->dt_stride_t) &&
-                      (!a->y || pair_rows(a->y, es, a->B, a->L, a->y_stride_b, a->y_stride_t)) &&
+                      (!a->y || (tma_rows(a->y, es, a->B, a->L, a->y_stride_b, a->y_stride_t) &&
+                                 tile_map(&my, a->io_dtype, a->y, a->B, a->L, a->D, a->y_stride_b, a->y_stride_t, rows))) &&
                       tile_map(&mdt, a->io_dtype, a->dt, a->B, a->L, a->D, a->dt_stride_b, a->dt_stride_t, rows) &&
                       tile_map(&mx, a->io_dtype, a->x, a->B, a->L, a->D, a->x_stride_b, a->x_stride_t, rows);
     const DevErr err{device_error_word()};
     const cudaError_t e = by_type(a->io_dtype, a->input_scale, [&](auto *t, auto sc) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int S = decltype(sc)::value;
-        const size_t tiles = (size_t)kStages * 2 * rows * kCols * sizeof(T);
+        const size_t tiles = (size_t)(2 * kStages + 2) * rows * kCols * sizeof(T);
         const size_t swap = (size_t)2 * (sp.warps + sp.cluster) * 512;
         return wide ? launch_cluster(gated_fwd_kernel<T, S, true>, units, sp, tiles + swap, (cudaStream_t)stream, mdt,
-                                     mx, f, sp.cluster, err)
-                    : launch_cluster(gated_fwd_kernel<T, S, false>, units, sp, swap, (cudaStream_t)stream, mdt, mx, f,
-                                     sp.cluster, err);
+                                     mx, my, f, sp.cluster, err)
+                    : launch_cluster(gated_fwd_kernel<T, S, false>, units, sp, swap, (cudaStream_t)stream, mdt, mx, my,
+                                     f, sp.cluster, err);
     });
     return e == cudaSuccess ? HM_OK : fail_args(HM_ERR_CUDA, "gated_scan_fwd launch: %s", cudaGetErrorString(e));
 }
