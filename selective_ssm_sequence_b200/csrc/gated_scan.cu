@@ -222,6 +222,35 @@ __device__ __forceinline__ void st_async16(uint32_t dst, uint32_t bar, uint32_t 
         : "memory");
 }
 
+// ------------------------------------------------------------------ time split
+
+// A sequence is walked in windows of `cluster` x W runs, W the warps of a
+// block; block `rank` of the cluster takes its W runs of each.  What a block
+// needs of a window are the maps of the blocks in front of it, and of the
+// window before those of all others, so two mbarriers count the arrivals: `low`
+// from the blocks in front (waited for in the same window), `high` from this
+// block and those behind (waited for one window later, when they have long
+// arrived).  No block waits for one behind it in the same window, so a
+// block's latency to the others is hidden as long as they lag less than a
+// window.
+//
+// Two slots per sender are enough: a block passes on its map of window i + 2
+// only after it has seen all maps of window i + 1, and each block hands its own
+// on only after all its warps have read everything of window i.
+struct Exchange {
+    Map2 *agg;                // [2][W][32] by parity of the window: the block's warps
+    Map2 *ctas;               // [2][cluster][32]: the cluster's blocks
+    uint64_t *low, *high;     // [2] each
+    int rank, cluster;
+    volatile int *abort_flag;
+    DevErr err;
+};
+
+constexpr int kR = 16;        // tokens of a warp's run
+constexpr int kCols = 64;     // channels of a warp
+constexpr int kMaxCluster = 16;
+constexpr int kStages = 2;
+
 // Bounded wait of every thread of the block.  After a timeout the kernel keeps
 // its control flow (its loops are bounded and every block of a cluster must
 // reach the barriers), with short waits that let its own copies land.
@@ -238,13 +267,56 @@ __device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatil
     if (!tc::mbar_try_wait(bar, parity)) wait_bar_slow(bar, parity, abort_flag, err, site);
 }
 
-// ------------------------------------------------------------------ forward
+// State at the start of window `it` from that at this block's runs of the
+// window before (`hb`); it > 0, cluster > 1.
+__device__ __forceinline__ F2 finish_window(const Exchange &x, int it, F2 hb) {
+    const int i = it - 1;
+    wait_bar(&x.high[i & 1], (i >> 1) & 1, x.abort_flag, x.err, 1);
+    const Map2 *m = x.ctas + ((i & 1) * x.cluster + x.rank) * 32 + (threadIdx.x & 31);
+#pragma unroll 4
+    for (int r = x.rank; r < x.cluster; ++r, m += 32) hb = apply(*m, hb);
+    return hb;
+}
 
-constexpr int kR = 16;        // tokens of a warp's run
-constexpr int kCols = 64;     // channels of a warp
-constexpr int kMaxWarps = 16;
-constexpr int kMaxCluster = 16;
-constexpr int kStages = 2;
+// After the block barrier of window `it` (all warps' maps in agg): the state
+// entering this warp's run, from `h`, the state at the start of the window.
+// h becomes the state at the block's runs (cluster > 1) or behind the window.
+template <int W>
+__device__ __forceinline__ F2 enter_run(const Exchange &x, int it, int warp, F2 &h) {
+    const int lane = threadIdx.x & 31;
+    const Map2 *agg = x.agg + (it & 1) * W * 32 + lane;
+    if (x.cluster == 1) {
+        F2 hin = h;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w == warp) hin = h;
+            h = apply(agg[w * 32], h);
+        }
+        return hin;
+    }
+    Map2 before = {splat(1.f), splat(0.f)}, q = agg[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+        if (w == warp) before = q;
+        q = then(q, agg[w * 32]);
+    }
+    const uint32_t slot = tc::smem_u32(x.ctas + ((it & 1) * x.cluster + x.rank) * 32 + lane);
+    const uint32_t lo = tc::smem_u32(&x.low[it & 1]), hi = tc::smem_u32(&x.high[it & 1]);
+    if (threadIdx.x == 0) {
+        tc::mbar_arrive_expect_tx(&x.high[it & 1], (uint32_t)(x.cluster - x.rank) * 512u);
+        if (x.rank) tc::mbar_arrive_expect_tx(&x.low[it & 1], (uint32_t)x.rank * 512u);
+    }
+    for (int r = warp; r < x.cluster; r += W) st_async16(slot, x.rank < r ? lo : hi, (uint32_t)r, q);
+    if (x.rank) {
+        wait_bar(&x.low[it & 1], (it >> 1) & 1, x.abort_flag, x.err, 2);
+        const Map2 *m = x.ctas + (it & 1) * x.cluster * 32 + lane;
+#pragma unroll 4
+        for (int r = 0; r < x.rank; ++r, m += 32) h = apply(*m, h);
+    }
+    return warp ? apply(before, h) : h;
+}
+
+// ------------------------------------------------------------------ forward
 
 struct FwdArgs {
     hm_gated_scan_args p;
@@ -252,56 +324,55 @@ struct FwdArgs {
     int64_t nchunk;
 };
 
-// blockIdx.x = (sequence, column group, rank in cluster).  WIDE: tiles come
-// and go by TMA (two stages, so the window after the next is on its way while
-// one is computed; results leave through two staging tiles), except the
-// window in which a sequence ends; else element loads and stores.
+// blockIdx.x = (sequence, column group, rank in cluster).  WIDE: tiles come by
+// TMA (two stages, so the window after the next is on its way while one is
+// computed) and each warp sends its run's results by TMA from a staging tile of
+// its own, except the run in which a sequence ends; else element loads and
+// stores.
 //
-// 128 threads and about 125 registers: four blocks on an SM.
-template <typename T, int SCALE, bool WIDE>
-__global__ void __launch_bounds__(kMaxWarps * 32)
+// The run's composed maps live in registers (64 of them): 16 warps on an SM.
+template <typename T, int SCALE, bool WIDE, int W>
+__global__ void __launch_bounds__(W * 32, 16 / W)
 gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_constant__ CUtensorMap map_x,
                  const __grid_constant__ CUtensorMap map_y, FwdArgs f, int cluster, DevErr err) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t full[kStages], xbar[2];
+    __shared__ uint64_t full[kStages], low[2], high[2];
     __shared__ int abort_flag;
+    constexpr int kRows = W * kR;                  // tokens of a block's window
+    constexpr int kTile = kRows * kCols;           // elements of a tile
+    constexpr uint32_t kBytes = kTile * sizeof(T);
     const hm_gated_scan_args &p = f.p;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    const int T_cta = nw * kR;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int64_t unit = blockIdx.x / cluster, b = unit / f.groups;
     const int64_t c0 = (unit - b * f.groups) * kCols, c = c0 + 2 * lane;
     const bool in0 = c < p.D, in1 = c + 1 < p.D;
     const int n = (int)clamped_len(p.lengths, b, p.L);          // L is at most 2^30
-    const int window = cluster * T_cta;
+    const int window = cluster * kRows;
     const int iters = (int)(((unsigned)n + (unsigned)window - 1u) / (unsigned)window);
-    const int tile = T_cta * kCols;                // elements of a tile
-    const uint32_t tile_bytes = (uint32_t)(tile * sizeof(T));
-    T *stage0 = reinterpret_cast<T *>(smem), *out0 = stage0 + 2 * kStages * tile;
-    // by parity of the window: the warps' maps per lane, then those of the cluster's blocks
-    Map2 *agg0 = reinterpret_cast<Map2 *>(smem + (WIDE ? (2 * kStages + 2) * tile_bytes : 0));
-    Map2 *ctas0 = agg0 + 2 * nw * 32;
+    T *stage0 = reinterpret_cast<T *>(smem), *out = stage0 + 2 * kStages * kTile + warp * kR * kCols;
+    Exchange x;
+    x.agg = reinterpret_cast<Map2 *>(smem + (WIDE ? (2 * kStages + 1) * kBytes : 0));
+    x.ctas = x.agg + 2 * W * 32;
+    x.low = low;
+    x.high = high;
+    x.rank = rank;
+    x.cluster = cluster;
+    x.abort_flag = &abort_flag;
+    x.err = err;
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int s = 0; s < kStages; ++s) tc::mbar_init(&full[s], 1);
-        tc::mbar_init(&xbar[0], 1);
-        tc::mbar_init(&xbar[1], 1);
+        for (int s = 0; s < 2; ++s) tc::mbar_init(&low[s], 1), tc::mbar_init(&high[s], 1);
         tc::mbar_fence_init();
     }
-    auto tile_start = [&](int it) { return it * window + rank * T_cta; };
     auto fetch = [&](int it) {
-        const int s = it % kStages;
-        T *dst = stage0 + s * 2 * tile;
-        tc::mbar_arrive_expect_tx(&full[s], 2 * tile_bytes);
-        tc::tma_load_3d(dst, &map_dt, &full[s], (int)c0, tile_start(it), (int)b);
-        tc::tma_load_3d(dst + tile, &map_x, &full[s], (int)c0, tile_start(it), (int)b);
-    };
-    // a tile that lies whole in front of the sequence's end leaves by TMA
-    auto whole = [&](int it) { return WIDE && p.y && tile_start(it) + T_cta <= n; };
-    auto send = [&](int it) {
-        tc::tma_store_3d(&map_y, out0 + (it & 1) * tile, (int)c0, tile_start(it), (int)b);
-        tc::bulk_commit();
+        const int s = it % kStages, t = it * window + rank * kRows;
+        T *dst = stage0 + s * 2 * kTile;
+        tc::mbar_arrive_expect_tx(&full[s], 2 * kBytes);
+        tc::tma_load_3d(dst, &map_dt, &full[s], (int)c0, t, (int)b);
+        tc::tma_load_3d(dst + kTile, &map_x, &full[s], (int)c0, t, (int)b);
     };
     if (cluster > 1) cluster_sync();
     else __syncthreads();
@@ -309,25 +380,26 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         for (int s = 0; s < kStages && s < iters; ++s) fetch(s);
 
     const ChanParams par = chan_params(p.A_log, p.dt_bias, c, p.D);
-    F2 h = splat(0.f);                             // state entering the window, the same in every warp
+    // the state at the start of the window; between windows of a cluster that at this block's runs
+    F2 h = splat(0.f);
     if (p.h0) h = pk(in0 ? p.h0[b * p.D + c] : 0.f, in1 ? p.h0[b * p.D + c + 1] : 0.f);
     const T *dtp = (const T *)p.dt + b * p.dt_stride_b + c, *xp = (const T *)p.x + b * p.x_stride_b + c;
     T *yp = (T *)p.y + b * p.y_stride_b + c;
 
-    for (int it = 0; it < iters; ++it) {
-        const int t0 = tile_start(it) + warp * kR;
+    int t0 = rank * kRows + warp * kR;             // the run's first token
+    for (int it = 0; it < iters; ++it, t0 += window) {
         const int m = min(max(n - t0, 0), kR);     // tokens of this run
         Map2 run[kR];                              // the run's composition up to each token
         Map2 all = {splat(1.f), splat(0.f)};
         if (WIDE) wait_bar(&full[it % kStages], (it / kStages) & 1, &abort_flag, err, 0);
         if (m > 0) {
             Raw<T> dv[kR], xv[kR];
-            const T *sdt = stage0 + (it % kStages) * 2 * tile + (warp * kR) * kCols + 2 * lane;
+            const T *sdt = stage0 + (it % kStages) * 2 * kTile + (warp * kR) * kCols + 2 * lane;
             if (WIDE) {
 #pragma unroll
                 for (int i = 0; i < kR; ++i) {
                     dv[i].load(sdt + i * kCols);
-                    xv[i].load(sdt + tile + i * kCols);
+                    xv[i].load(sdt + kTile + i * kCols);
                 }
             } else {
 #pragma unroll
@@ -360,47 +432,29 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
             // single decays then does not build up over more than a run
             all.A = ex2(sum);
         }
-        Map2 *agg = agg0 + (it & 1) * nw * 32 + lane, *ctas = ctas0 + (it & 1) * cluster * 32 + lane;
-        agg[warp * 32] = all;
-        if (WIDE && threadIdx.x == 0) tc::bulk_wait_read_all();   // the staging tile of two windows ago has left
-        __syncthreads();                           // aggregates written; this window's tiles read; the last's staged
-        if (WIDE && threadIdx.x == 0) {
-            if (it > 0 && whole(it - 1)) send(it - 1);
-            if (it + kStages < iters) fetch(it + kStages);
-        }
-        // the block's runs in front of this warp's, then all of them
-        Map2 q = {splat(1.f), splat(0.f)};
-        int w = 0;
-        for (; w < warp; ++w) q = then(q, agg[w * 32]);
-        const Map2 before = q;
-        for (; w < nw; ++w) q = then(q, agg[w * 32]);
-        F2 hin = h;
-        if (cluster > 1) {
-            if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&xbar[it & 1], (uint32_t)cluster * 512u);
-            for (int r = warp; r < cluster; r += nw)
-                st_async16(tc::smem_u32(ctas + rank * 32), tc::smem_u32(&xbar[it & 1]), (uint32_t)r, q);
-            wait_bar(&xbar[it & 1], (it >> 1) & 1, &abort_flag, err, 1);
-            int r = 0;
-            for (; r < rank; ++r) h = apply(ctas[r * 32], h);
-            hin = h;
-            for (; r < cluster; ++r) h = apply(ctas[r * 32], h);
-        } else {
-            h = apply(q, h);
-        }
-        hin = apply(before, hin);
+        x.agg[((it & 1) * W + warp) * 32 + lane] = all;
+        if (cluster > 1 && it > 0) h = finish_window(x, it, h);
+        __syncthreads();         // maps written; this window's tiles, and the window before's maps, read
+        if (WIDE && threadIdx.x == 0 && it + kStages < iters) fetch(it + kStages);
+        const F2 hin = enter_run<W>(x, it, warp, h);
         if (m > 0) {
             if (p.states && t0 % kChunk == 0 && in0) {
                 float *st = (float *)p.states + (b * f.nchunk + t0 / kChunk) * p.D + c;
                 st[0] = un(hin).x;
                 if (in1) st[1] = un(hin).y;
             }
-            if (whole(it)) {
-                T *so = out0 + (it & 1) * tile + (warp * kR) * kCols + 2 * lane;
+            if (WIDE && p.y && m == kR) {
+                if (lane == 0) tc::bulk_wait_read_all();         // the last run's results have left
+                __syncwarp();
+                T *so = out + 2 * lane;
 #pragma unroll
-                for (int i = 0; i < kR; ++i) {
-                    st_pair(so + i * kCols, apply(run[i], hin));
-                }
+                for (int i = 0; i < kR; ++i) st_pair(so + i * kCols, apply(run[i], hin));
                 tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::tma_store_3d(&map_y, out, (int)c0, t0, (int)b);
+                    tc::bulk_commit();
+                }
             } else if (p.y) {
                 T *yr = yp + t0 * p.y_stride_t;
 #pragma unroll
@@ -415,17 +469,12 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
             }
         }
     }
+    if (cluster > 1 && iters > 0) h = finish_window(x, iters, h);
     if (p.h_out && rank == 0 && warp == 0) {
         if (in0) p.h_out[b * p.D + c] = un(h).x;
         if (in1) p.h_out[b * p.D + c + 1] = un(h).y;
     }
-    if (WIDE) {
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            if (iters > 0 && whole(iters - 1)) send(iters - 1);
-            tc::bulk_wait_all();
-        }
-    }
+    if (WIDE && lane == 0) tc::bulk_wait_all();
     if (cluster > 1) cluster_sync();               // no block leaves while others may still write to it
 }
 
@@ -657,20 +706,16 @@ bool tma_rows(const void *p, size_t es, int64_t B, int64_t L, int64_t sb, int64_
 }
 
 struct Split {
-    int warps, cluster;
+    int warps, cluster;       // of a block; blocks of a cluster
 };
 
-// The tokens are split over blocks of a cluster until about four blocks of
-// four warps stand on each SM, then over more warps per block.
-Split split_of(int64_t units, int64_t L, size_t es) {
+// The tokens are split over warps and blocks until about 14 warps stand on
+// each SM, or the sequence is.
+Split split_of(int64_t units, int64_t L) {
     const int64_t runs = (L + kR - 1) / kR;
-    Split s{4, 1};
-    while (s.warps > 1 && s.warps / 2 >= runs) s.warps /= 2;
-    while (s.cluster < kMaxCluster && units * s.cluster * 2 <= 148 * 4 && (int64_t)s.warps * s.cluster < runs)
+    Split s{runs > 4 ? 8 : 4, 1};
+    while (s.cluster < kMaxCluster && units * s.cluster * s.warps * 2 <= 148 * 16 && (int64_t)s.warps * s.cluster < runs)
         s.cluster *= 2;
-    const int most = es == 4 ? kMaxWarps / 2 : kMaxWarps;      // two stages of a window's tiles in shared memory
-    while (s.warps < most && units * s.cluster * s.warps * 2 <= 148 * 16 && (int64_t)s.warps * s.cluster < runs)
-        s.warps *= 2;
     return s;
 }
 
@@ -708,7 +753,7 @@ extern "C" hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t 
     FwdArgs f{*a, (a->D + kCols - 1) / kCols, (a->L + kChunk - 1) / kChunk};
     const int64_t units = a->B * f.groups;
     const size_t es = esize(a->io_dtype);
-    const Split sp = split_of(units, a->L, es);
+    const Split sp = split_of(units, a->L);
     if (units * sp.cluster > 0x7fffffffLL)
         return fail_args(HM_ERR_UNSUPPORTED, "gated_scan_fwd: B * D / 64 is too large");
     CUtensorMap mdt{}, mx{}, my{};
@@ -716,19 +761,20 @@ extern "C" hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t 
     const bool wide = a->L > 0 && tma_rows(a->x, es, a->B, a->L, a->x_stride_b, a->x_stride_t) &&
                       tma_rows(a->dt, es, a->B, a->L, a->dt_stride_b, a->dt_stride_t) &&
                       (!a->y || (tma_rows(a->y, es, a->B, a->L, a->y_stride_b, a->y_stride_t) &&
-                                 tile_map(&my, a->io_dtype, a->y, a->B, a->L, a->D, a->y_stride_b, a->y_stride_t, rows))) &&
+                                 tile_map(&my, a->io_dtype, a->y, a->B, a->L, a->D, a->y_stride_b, a->y_stride_t, kR))) &&
                       tile_map(&mdt, a->io_dtype, a->dt, a->B, a->L, a->D, a->dt_stride_b, a->dt_stride_t, rows) &&
                       tile_map(&mx, a->io_dtype, a->x, a->B, a->L, a->D, a->x_stride_b, a->x_stride_t, rows);
     const DevErr err{device_error_word()};
     const cudaError_t e = by_type(a->io_dtype, a->input_scale, [&](auto *t, auto sc) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int S = decltype(sc)::value;
-        const size_t tiles = (size_t)(2 * kStages + 2) * rows * kCols * sizeof(T);
-        const size_t swap = (size_t)2 * (sp.warps + sp.cluster) * 512;
-        return wide ? launch_cluster(gated_fwd_kernel<T, S, true>, units, sp, tiles + swap, (cudaStream_t)stream, mdt,
-                                     mx, my, f, sp.cluster, err)
-                    : launch_cluster(gated_fwd_kernel<T, S, false>, units, sp, swap, (cudaStream_t)stream, mdt, mx, my,
-                                     f, sp.cluster, err);
+        const size_t smem = (wide ? (size_t)(2 * kStages + 1) * rows * kCols * sizeof(T) : 0) +
+                            (size_t)2 * (sp.warps + sp.cluster) * 32 * sizeof(Map2);
+        auto go = [&](auto kernel) {
+            return launch_cluster(kernel, units, sp, smem, (cudaStream_t)stream, mdt, mx, my, f, sp.cluster, err);
+        };
+        if (sp.warps == 8) return wide ? go(gated_fwd_kernel<T, S, true, 8>) : go(gated_fwd_kernel<T, S, false, 8>);
+        return wide ? go(gated_fwd_kernel<T, S, true, 4>) : go(gated_fwd_kernel<T, S, false, 4>);
     });
     return e == cudaSuccess ? HM_OK : fail_args(HM_ERR_CUDA, "gated_scan_fwd launch: %s", cudaGetErrorString(e));
 }
