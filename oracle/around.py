@@ -8,7 +8,8 @@ the result's own sum with every term replaced by its absolute value (and, for
 the recurrences, with the error that a relative perturbation of every factor
 would build up).  A result computed with relative errors of at most delta per
 factor and term is within delta times that magnitude of the exact one, to
-first order.
+first order; a decay a = exp(la) counts 1 + |la| times, since a relative error
+delta of its exponent is one of |la| delta of itself.
 """
 from __future__ import annotations
 
@@ -44,7 +45,7 @@ def gated_scan(x, dt, A_log, dt_bias=None, h0=None, lengths=None, scale=PLAIN):
     """(y, h_out, magnitude of y): y rows behind a sequence's end are zero."""
     x = np.asarray(x, np.float64)
     B, L, D = x.shape
-    _, _, _, a, beta = gates(dt, A_log, dt_bias, scale)
+    _, _, la, a, beta = gates(dt, A_log, dt_bias, scale)
     _, on = _lengths(lengths, B, L)
     h = np.zeros((B, D)) if h0 is None else np.asarray(h0, np.float64).copy()
     m, e = np.abs(h), np.zeros((B, D))
@@ -53,7 +54,7 @@ def gated_scan(x, dt, A_log, dt_bias=None, h0=None, lengths=None, scale=PLAIN):
         live = on[:, t, None]
         u = beta[:, t] * x[:, t]
         m2 = a[:, t] * m + np.abs(u)
-        e = np.where(live, a[:, t] * e + m2, e)
+        e = np.where(live, a[:, t] * (e + m * (1 - la[:, t])) + np.abs(u), e)
         h = np.where(live, a[:, t] * h + u, h)
         m = np.where(live, m2, m)
         y[:, t], mag[:, t] = np.where(live, h, 0.0), np.where(live, e, 0.0)
@@ -76,7 +77,7 @@ def gated_scan_bwd(x, dt, dy, A_log, dt_bias=None, h0=None, lengths=None, scale=
         hb[:, t], mb[:, t], eb[:, t] = h, m, e
         u = beta[:, t] * x[:, t]
         m2 = a[:, t] * m + np.abs(u)
-        e = np.where(live, a[:, t] * e + m2, e)
+        e = np.where(live, a[:, t] * (e + m * (1 - la[:, t])) + np.abs(u), e)
         h = np.where(live, a[:, t] * h + u, h)
         m = np.where(live, m2, m)
     c = np.zeros((B, D)) if dh_out is None else np.asarray(dh_out, np.float64).copy()
@@ -87,11 +88,12 @@ def gated_scan_bwd(x, dt, dy, A_log, dt_bias=None, h0=None, lengths=None, scale=
         gt, gmt = dy[:, t] + c, np.abs(dy[:, t]) + cm
         get = ce + gmt
         g[:, t], gm[:, t], ge[:, t] = (np.where(live, v, 0.0) for v in (gt, gmt, get))
-        c, cm, ce = (np.where(live, a[:, t] * v, w) for v, w in ((gt, c), (gmt, cm), (get, ce)))
-    dla, dlam = g * a * hb, a * (ge * mb + gm * eb)
+        c, cm = (np.where(live, a[:, t] * v, w) for v, w in ((gt, c), (gmt, cm)))
+        ce = np.where(live, a[:, t] * (get + gmt * (1 - la[:, t])), ce)
+    dla, dlam = g * a * hb, a * (ge * mb + gm * eb + gm * mb * (1 - la))
     if scale == UNIT:
         k = np.where(beta > 0, a * a / np.where(beta > 0, beta, 1.0), 0.0)
-        dla, dlam = dla - g * x * k, dlam + ge * np.abs(x) * k
+        dla, dlam = dla - g * x * k, dlam + (ge + gm * (1 - la)) * np.abs(x) * k
     dd, ddm = -rate * dla, rate * dlam
     if scale == STEP:
         dd, ddm = dd + g * x, ddm + ge * np.abs(x)

@@ -85,11 +85,6 @@ __device__ __forceinline__ F2 ex2(F2 a) {
     const float2 u = un(a);
     return pk(tc::ex2_approx(u.x), tc::ex2_approx(u.y));
 }
-__device__ __forceinline__ float rsq(float x) {
-    float r;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ float sqrt_approx(float x) {
     float r;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -174,6 +169,7 @@ template <>
 struct Raw<__nv_bfloat16> {
     uint32_t w;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint32_t *>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint32_t *>(p) = w; }
     __device__ __forceinline__ void set(float x, float y) { w = tc::pack_bf16x2(x, y); }
     __device__ __forceinline__ F2 pair() const { return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
 };
@@ -181,6 +177,7 @@ template <>
 struct Raw<float> {
     float2 w;
     __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const float2 *>(p); }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float2 *>(p) = w; }
     __device__ __forceinline__ void set(float x, float y) { w = make_float2(x, y); }
     __device__ __forceinline__ F2 pair() const { return pk(w.x, w.y); }
 };
@@ -478,68 +475,270 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     if (cluster > 1) cluster_sync();               // no block leaves while others may still write to it
 }
 
-// partial sums of dA_log and d_dt_bias: part[(b * 2 + k) * D + c]
-template <typename T, int SCALE>
-__global__ void __launch_bounds__(128) gated_bwd_kernel(hm_gated_scan_bwd_args p, float *part) {
-    const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= p.D) return;
-    const float rate = expf(p.A_log[c]), bias = p.dt_bias ? p.dt_bias[c] : 0.f;
-    const int64_t nchunk = (p.L + kChunk - 1) / kChunk;
-    for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
-        const int64_t n = clamped_len(p.lengths, b, p.L);
-        const T *x = (const T *)p.x + b * p.x_stride_b + c;
-        const T *dt = (const T *)p.dt + b * p.dt_stride_b + c;
-        const T *dy = (const T *)p.dy + b * p.dy_stride_b + c;
-        T *dx = (T *)p.dx + b * p.dx_stride_b + c;
-        T *ddt = (T *)p.ddt + b * p.ddt_stride_b + c;
-        float carry = p.dh_out ? p.dh_out[b * p.D + c] : 0.f, sA = 0.f, sb = 0.f;
-        float hs[kChunk];
-        for (int64_t k = (n + kChunk - 1) / kChunk - 1; k >= 0; --k) {
-            const int64_t t0 = k * kChunk;
-            const int m = (int)(n - t0 < kChunk ? n - t0 : kChunk);
-            float h = ((const float *)p.states)[(b * nchunk + k) * p.D + c];
-            for (int i = 0; i < m; ++i) {
-                hs[i] = h;
-                const Gate g = gate_of<SCALE>(hm_ld(dt, (t0 + i) * p.dt_stride_t), bias, rate);
-                h = fmaf(g.a, h, g.beta * hm_ld(x, (t0 + i) * p.x_stride_t));
-            }
-            float cA = 0.f, cb = 0.f;
-            for (int i = m - 1; i >= 0; --i) {
-                const int64_t t = t0 + i;
-                const Gate q = gate_of<SCALE>(hm_ld(dt, t * p.dt_stride_t), bias, rate);
-                const float xv = hm_ld(x, t * p.x_stride_t);
-                const float g = hm_ld(dy, t * p.dy_stride_t) + carry;
-                carry = q.a * g;
-                float dla = carry * hs[i];
-                if (SCALE == HM_INPUT_UNIT && q.beta > 0.f) dla -= g * xv * q.a * q.a / q.beta;
-                float dstep = -rate * dla;
-                if (SCALE == HM_INPUT_STEP) dstep += g * xv;
-                const float dz = dstep / (1.f + expf(-q.z));
-                hm_st(dx, t * p.dx_stride_t, g * q.beta);
-                hm_st(ddt, t * p.ddt_stride_t, dz);
-                cA = fmaf(dla, q.la, cA);
-                cb += dz;
-            }
-            sA += cA;
-            sb += cb;
-        }
-        part[(b * 2 + 0) * p.D + c] = sA;
-        part[(b * 2 + 1) * p.D + c] = sb;
-        if (p.dh0) p.dh0[b * p.D + c] = carry;
-    }
+// ------------------------------------------------------------------ backward
+
+constexpr int kRb = 8;             // tokens of a warp's run
+constexpr int kWb = kChunk / kRb;  // a block's window is the chunk behind one stored state
+constexpr int kBwdStages = 3;
+
+struct BwdArgs {
+    hm_gated_scan_bwd_args p;
+    int64_t groups;
+    int64_t nchunk;
+    float *part;                   // [B * cluster][2][D]: the blocks' shares of dA_log and d_dt_bias
+};
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-__global__ void __launch_bounds__(128) gated_sum_kernel(const float *part, int64_t rows, int64_t D, float *dA,
-                                                        float *db) {
-    const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= D) return;
-    float sA = 0.f, sb = 0.f;
-    for (int64_t r = 0; r < rows; ++r) {
-        sA += part[(r * 2 + 0) * D + c];
-        sb += part[(r * 2 + 1) * D + c];
+// The forward's scheme with time reversed for the adjoint: c, the gradient
+// that reaches h_t from behind token t, goes through a run as c -> A c + R.
+// A block's window is one chunk of 64 tokens, entered forward in time from the
+// state that the forward stored, so the states need no exchange between
+// blocks: the same pass over dt, x and dy gives a run's forward map (A, B) and
+// its adjoint map (A, R), both with A = 2^(sum of the exponents).  Then each
+// warp walks its run forward for the h_{t-1} and back for the gradients, which
+// leave over the tiles of x and dt they came from.
+//
+// Registers hold a, h_{t-1}, Delta, sigmoid(z) (and beta) of 8 tokens: 16
+// warps on an SM; x and dy are read again from shared memory.
+template <typename T, int SCALE, bool WIDE>
+__global__ void __launch_bounds__(kWb * 32, 2)
+gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_constant__ CUtensorMap map_x,
+                 const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_dx,
+                 const __grid_constant__ CUtensorMap map_ddt, BwdArgs f, int cluster, DevErr err) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full[kBwdStages], low[2], high[2];
+    __shared__ int abort_flag;
+    constexpr int kTile = kChunk * kCols;
+    constexpr uint32_t kBytes = kTile * sizeof(T);
+    const hm_gated_scan_bwd_args &p = f.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = cluster > 1 ? (int)cluster_rank() : 0;
+    const int64_t unit = blockIdx.x / cluster, b = unit / f.groups;
+    const int64_t c0 = (unit - b * f.groups) * kCols, c = c0 + 2 * lane;
+    const bool in0 = c < p.D, in1 = c + 1 < p.D;
+    const int n = (int)clamped_len(p.lengths, b, p.L);
+    const int chunks = (n + kChunk - 1) / kChunk, iters = (chunks + cluster - 1) / cluster;
+    T *stage0 = reinterpret_cast<T *>(smem);
+    Exchange x;
+    x.agg = reinterpret_cast<Map2 *>(smem + kBwdStages * 3 * kBytes);   // adjoint maps, last warp first
+    Map2 *fwd = x.agg + 2 * kWb * 32;                                                // forward maps
+    x.ctas = fwd + 2 * kWb * 32;
+    x.low = low;
+    x.high = high;
+    x.rank = rank;
+    x.cluster = cluster;
+    x.abort_flag = &abort_flag;
+    x.err = err;
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < kBwdStages; ++s) tc::mbar_init(&full[s], 1);
+        for (int s = 0; s < 2; ++s) tc::mbar_init(&low[s], 1), tc::mbar_init(&high[s], 1);
+        tc::mbar_fence_init();
     }
-    dA[c] = sA;
-    if (db) db[c] = sb;
+    // chunk of window `it`: from the sequence's end; negative: none
+    auto chunk_of = [&](int it) { return chunks - 1 - (it * cluster + rank); };
+    auto fetch = [&](int it) {
+        const int s = it % kBwdStages, t = chunk_of(it) * kChunk;
+        if (t < 0) return;
+        T *dst = stage0 + s * 3 * kTile;
+        tc::mbar_arrive_expect_tx(&full[s], 3 * kBytes);
+        tc::tma_load_3d(dst, &map_dt, &full[s], (int)c0, t, (int)b);
+        tc::tma_load_3d(dst + kTile, &map_x, &full[s], (int)c0, t, (int)b);
+        tc::tma_load_3d(dst + 2 * kTile, &map_dy, &full[s], (int)c0, t, (int)b);
+    };
+    if (cluster > 1) cluster_sync();
+    else __syncthreads();
+    if (WIDE && threadIdx.x == 0)
+        for (int s = 0; s < kBwdStages && s < iters; ++s) fetch(s);
+
+    const ChanParams par = chan_params(p.A_log, p.dt_bias, c, p.D);
+    F2 carry = splat(0.f);         // gradient entering the window from behind (between windows: this block's part)
+    if (p.dh_out) carry = pk(in0 ? p.dh_out[b * p.D + c] : 0.f, in1 ? p.dh_out[b * p.D + c + 1] : 0.f);
+    const T *dtp = (const T *)p.dt + b * p.dt_stride_b + c, *xp = (const T *)p.x + b * p.x_stride_b + c;
+    const T *dyp = (const T *)p.dy + b * p.dy_stride_b + c;
+    T *dxp = (T *)p.dx + b * p.dx_stride_b + c, *ddtp = (T *)p.ddt + b * p.ddt_stride_b + c;
+    F2 sumA = splat(0.f), sumb = splat(0.f);
+
+    for (int it = 0; it < iters; ++it) {
+        const int chunk = chunk_of(it), t0 = chunk * kChunk + warp * kRb;
+        const int m = chunk < 0 ? 0 : min(max(n - t0, 0), kRb);
+        T *tile = stage0 + (it % kBwdStages) * 3 * kTile + (warp * kRb) * kCols + 2 * lane;
+        F2 a[kRb], h[kRb], step[kRb], sig[kRb], beta[kRb];
+        Map2 mf = {splat(1.f), splat(0.f)}, mr = {splat(1.f), splat(0.f)};
+        F2 hin = splat(0.f);
+        if (chunk >= 0 && in0) {
+            const float *st = (const float *)p.states + (b * f.nchunk + chunk) * p.D + c;
+            hin = pk(st[0], in1 ? st[1] : 0.f);
+        }
+        if (WIDE && chunk >= 0) wait_bar(&full[it % kBwdStages], (it / kBwdStages) & 1, &abort_flag, err, 3);
+        if (m > 0) {
+            // a thread's own elements of the tile: element loads put them there, and tokens behind
+            // the end become a step of zero, no input, no gradient of their own
+            if (!WIDE || m < kRb) {
+                for (int i = WIDE ? m : 0; i < kRb; ++i) {
+                    float d0 = -INFINITY, d1 = -INFINITY, x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
+                    if (i < m) {
+                        const int64_t t = t0 + i, od = t * p.dt_stride_t, ox = t * p.x_stride_t, oy = t * p.dy_stride_t;
+                        if (in0) d0 = hm_ld(dtp, od), x0 = hm_ld(xp, ox), y0 = hm_ld(dyp, oy);
+                        if (in1) d1 = hm_ld(dtp, od + 1), x1 = hm_ld(xp, ox + 1), y1 = hm_ld(dyp, oy + 1);
+                    }
+                    Raw<T> r;
+                    r.set(d0, d1);
+                    r.store(tile + i * kCols);
+                    r.set(x0, x1);
+                    r.store(tile + kTile + i * kCols);
+                    r.set(y0, y1);
+                    r.store(tile + 2 * kTile + i * kCols);
+                }
+            }
+            Raw<T> dv[kRb], xr[kRb];
+#pragma unroll
+            for (int i = 0; i < kRb; ++i) {
+                dv[i].load(tile + i * kCols);
+                xr[i].load(tile + kTile + i * kCols);
+            }
+            F2 sum = splat(0.f);
+#pragma unroll
+            for (int i = 0; i < kRb; ++i) {
+                const Gate2 g = gates2(dv[i].pair(), par);
+                const float2 e = un(g.e), z = un(g.z);
+                const float r0 = rcp_approx(1.f + e.x), r1 = rcp_approx(1.f + e.y);
+                sig[i] = pk(z.x < 0.f ? e.x * r0 : r0, z.y < 0.f ? e.y * r1 : r1);
+                a[i] = g.a;
+                step[i] = g.step;
+                if (SCALE == HM_INPUT_UNIT) {
+                    const float2 q = un(unit_sq(g));
+                    beta[i] = pk(sqrt_approx(q.x), sqrt_approx(q.y));
+                }
+                const F2 xv = xr[i].pair();
+                const F2 u = SCALE == HM_INPUT_PLAIN ? xv
+                             : SCALE == HM_INPUT_STEP ? xv * (g.step * splat(kLn2)) : xv * beta[i];
+                sum = sum + g.la;
+                h[i] = u;
+                mf.B = fma(g.a, mf.B, u);
+            }
+#pragma unroll
+            for (int i = kRb - 1; i >= 0; --i) {
+                Raw<T> dy;
+                dy.load(tile + 2 * kTile + i * kCols);
+                mr.B = a[i] * (dy.pair() + mr.B);
+            }
+            mf.A = mr.A = ex2(sum);
+        }
+        fwd[((it & 1) * kWb + warp) * 32 + lane] = mf;
+        x.agg[((it & 1) * kWb + kWb - 1 - warp) * 32 + lane] = mr;
+        if (cluster > 1 && it > 0) carry = finish_window(x, it, carry);
+        if (WIDE && lane == 0) tc::bulk_wait_read_all();   // this warp's rows of the last window have left
+        __syncthreads();           // maps written; the last window's tiles free
+        if (WIDE && threadIdx.x == 0 && it > 0 && it - 1 + kBwdStages < iters) fetch(it - 1 + kBwdStages);
+        F2 cin = enter_run<kWb>(x, it, kWb - 1 - warp, carry);
+        if (m > 0) {
+            const Map2 *mw = fwd + (it & 1) * kWb * 32 + lane;
+            for (int w = 0; w < warp; ++w, mw += 32) hin = apply(*mw, hin);
+#pragma unroll
+            for (int i = 0; i < kRb; ++i) {                // h[i]: u_t, then h_{t-1}
+                const F2 next = fma(a[i], hin, h[i]);
+                h[i] = hin;
+                hin = next;
+            }
+            const bool whole = WIDE && m == kRb;
+#pragma unroll
+            for (int i = kRb - 1; i >= 0; --i) {
+                Raw<T> rx, rdy;
+                rx.load(tile + kTile + i * kCols);
+                rdy.load(tile + 2 * kTile + i * kCols);
+                const F2 xv = rx.pair(), g = rdy.pair() + cin;
+                cin = a[i] * g;
+                F2 dla = cin * h[i];
+                if (SCALE == HM_INPUT_UNIT) {
+                    // g x a^2 / beta; where beta is zero so is what multiplies the quotient below
+                    const float2 bt = un(beta[i]);
+                    const F2 ib = pk(-rcp_approx(fmaxf(bt.x, 1e-18f)), -rcp_approx(fmaxf(bt.y, 1e-18f)));
+                    dla = fma(cin * xv, a[i] * ib, dla);
+                }
+                F2 dz = dla * par.nrate;
+                if (SCALE == HM_INPUT_STEP) dz = fma(g, xv, dz);
+                dz = dz * sig[i];
+                sumA = fma(dla, step[i] * par.nrate, sumA);
+                sumb = sumb + dz;
+                const F2 dx = SCALE == HM_INPUT_PLAIN ? g
+                              : SCALE == HM_INPUT_STEP ? g * (step[i] * splat(kLn2)) : g * beta[i];
+                if (whole) {
+                    st_pair(tile + i * kCols, dz);
+                    st_pair(tile + kTile + i * kCols, dx);
+                } else if (i < m) {
+                    const int64_t od = (int64_t)(t0 + i) * p.ddt_stride_t, ox = (int64_t)(t0 + i) * p.dx_stride_t;
+                    const float2 vz = un(dz), vx = un(dx);
+                    if (in0) hm_st(ddtp, od, vz.x), hm_st(dxp, ox, vx.x);
+                    if (in1) hm_st(ddtp, od + 1, vz.y), hm_st(dxp, ox + 1, vx.y);
+                }
+            }
+            if (whole) {
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    T *row = tile - 2 * lane;
+                    tc::tma_store_3d(&map_ddt, row, (int)c0, t0, (int)b);
+                    tc::tma_store_3d(&map_dx, row + kTile, (int)c0, t0, (int)b);
+                    tc::bulk_commit();
+                }
+            }
+        }
+    }
+    if (cluster > 1 && iters > 0) carry = finish_window(x, iters, carry);
+    if (p.dh0 && rank == 0 && warp == 0) {
+        if (in0) p.dh0[b * p.D + c] = un(carry).x;
+        if (in1) p.dh0[b * p.D + c + 1] = un(carry).y;
+    }
+    // the block's share of the parameter gradients, its warps' in order
+    if (WIDE && lane == 0) tc::bulk_wait_all();
+    __syncthreads();
+    x.agg[warp * 32 + lane] = {sumA, sumb};
+    __syncthreads();
+    if (warp == 0) {
+        for (int w = 1; w < kWb; ++w) {
+            const Map2 v = x.agg[w * 32 + lane];
+            sumA = sumA + v.A;
+            sumb = sumb + v.B;
+        }
+        sumA = sumA * splat(kLn2);             // log a from its base-2 exponent
+        float *o = f.part + (b * cluster + rank) * 2 * p.D + c;
+        if (in0) o[0] = un(sumA).x, o[p.D] = un(sumb).x;
+        if (in1) o[1] = un(sumA).y, o[p.D + 1] = un(sumb).y;
+    }
+    if (cluster > 1) cluster_sync();
+}
+
+// the blocks' shares summed in order: 8 threads per channel, each a stride of
+// the rows, then the 8
+__global__ void __launch_bounds__(256) gated_sum_kernel(const float *part, int64_t rows, int64_t D, float *dA,
+                                                        float *db) {
+    __shared__ float s[2][8][33];
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    float sA = 0.f, sb = 0.f;
+    if (c < D)
+        for (int64_t r = threadIdx.y; r < rows; r += 8) {
+            sA += part[(r * 2 + 0) * D + c];
+            sb += part[(r * 2 + 1) * D + c];
+        }
+    s[0][threadIdx.y][threadIdx.x] = sA;
+    s[1][threadIdx.y][threadIdx.x] = sb;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < D) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            sA += s[0][i][threadIdx.x];
+            sb += s[1][i][threadIdx.x];
+        }
+        dA[c] = sA;
+        if (db) db[c] = sb;
+    }
 }
 
 template <typename T, int SCALE>
@@ -629,8 +828,31 @@ hm_status check_fwd(const hm_gated_scan_args *a) {
     return HM_OK;
 }
 
+struct Split {
+    int warps, cluster;       // of a block; blocks of a cluster
+};
+
+// The tokens are split over warps and blocks until about 14 warps stand on
+// each SM, or the sequence is.
+Split split_of(int64_t units, int64_t L) {
+    const int64_t runs = (L + kR - 1) / kR;
+    Split s{runs > 4 ? 8 : 4, 1};
+    while (s.cluster < kMaxCluster && units * s.cluster * s.warps * 2 <= 148 * 16 && (int64_t)s.warps * s.cluster < runs)
+        s.cluster *= 2;
+    return s;
+}
+
+// the same rule for the backward, whose blocks have 8 warps and 64 tokens
+Split bwd_split(int64_t units, int64_t L) {
+    const int64_t chunks = (L + kChunk - 1) / kChunk;
+    Split s{kWb, 1};
+    while (s.cluster < kMaxCluster && units * s.cluster * 2 <= 148 * 2 && s.cluster < chunks) s.cluster *= 2;
+    return s;
+}
+
 size_t bwd_workspace(const hm_gated_scan_bwd_args *a) {
-    return (size_t)(a->B * 2 * a->D) * sizeof(float);
+    const int64_t units = a->B * ((a->D + kCols - 1) / kCols);
+    return (size_t)(a->B * bwd_split(units, a->L).cluster * 2 * a->D) * sizeof(float);
 }
 
 hm_status check_bwd(const hm_gated_scan_bwd_args *a) {
@@ -673,8 +895,6 @@ cudaError_t by_type(hm_dtype t, int scale, F f) {
 #undef HM_SCALE
 }
 
-unsigned grid_y(int64_t B) { return (unsigned)(B < 65535 ? B : 65535); }
-
 }  // namespace
 
 }  // namespace hm
@@ -703,20 +923,6 @@ bool tile_map(CUtensorMap *m, hm_dtype t, const void *base, int64_t B, int64_t L
 // rows that TMA can fetch: 16-byte aligned base and strides
 bool tma_rows(const void *p, size_t es, int64_t B, int64_t L, int64_t sb, int64_t st) {
     return aligned_to(p, 16) && (L <= 1 || st * (int64_t)es % 16 == 0) && (B <= 1 || sb * (int64_t)es % 16 == 0);
-}
-
-struct Split {
-    int warps, cluster;       // of a block; blocks of a cluster
-};
-
-// The tokens are split over warps and blocks until about 14 warps stand on
-// each SM, or the sequence is.
-Split split_of(int64_t units, int64_t L) {
-    const int64_t runs = (L + kR - 1) / kR;
-    Split s{runs > 4 ? 8 : 4, 1};
-    while (s.cluster < kMaxCluster && units * s.cluster * s.warps * 2 <= 148 * 16 && (int64_t)s.warps * s.cluster < runs)
-        s.cluster *= 2;
-    return s;
 }
 
 template <typename K, typename... A>
@@ -792,18 +998,46 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
         return fail_args(HM_ERR_INVALID_ARG, "gated_scan_bwd: workspace of %zu bytes, 256-byte aligned, is needed",
                          need);
     cudaStream_t s = (cudaStream_t)stream;
-    const unsigned gx = (unsigned)((a->D + 127) / 128);
     cudaError_t e = cudaSuccess;
-    if (a->B > 0)
-        e = by_type(a->io_dtype, a->input_scale, [&](auto *t, auto sc) {
-            using T = std::remove_pointer_t<decltype(t)>;
-            gated_bwd_kernel<T, decltype(sc)::value>
-                <<<dim3(gx, grid_y(a->B)), 128, 0, s>>>(*a, (float *)a->workspace);
-            count_launches(1);
-            return cudaGetLastError();
+    int64_t shares = 0;
+    if (a->B > 0) {
+        BwdArgs f{*a, (a->D + kCols - 1) / kCols, (a->L + kChunk - 1) / kChunk, (float *)a->workspace};
+        const int64_t units = a->B * f.groups;
+        const Split sp = bwd_split(units, a->L);
+        if (units * sp.cluster > 0x7fffffffLL)
+            return fail_args(HM_ERR_UNSUPPORTED, "gated_scan_bwd: B * D / 64 is too large");
+        shares = a->B * sp.cluster;
+        const size_t es = esize(a->io_dtype);
+        struct {
+            const void *p;
+            int64_t sb, st;
+            int rows;
+            CUtensorMap map;
+        } t[5] = {{a->dt, a->dt_stride_b, a->dt_stride_t, kChunk, {}},
+                  {a->x, a->x_stride_b, a->x_stride_t, kChunk, {}},
+                  {a->dy, a->dy_stride_b, a->dy_stride_t, kChunk, {}},
+                  {a->dx, a->dx_stride_b, a->dx_stride_t, kRb, {}},
+                  {a->ddt, a->ddt_stride_b, a->ddt_stride_t, kRb, {}}};
+        bool wide = a->L > 0;
+        for (auto &r : t)
+            wide = wide && tma_rows(r.p, es, a->B, a->L, r.sb, r.st) &&
+                   tile_map(&r.map, a->io_dtype, r.p, a->B, a->L, a->D, r.sb, r.st, r.rows);
+        const DevErr err{device_error_word()};
+        e = by_type(a->io_dtype, a->input_scale, [&](auto *tp, auto sc) {
+            using T = std::remove_pointer_t<decltype(tp)>;
+            constexpr int S = decltype(sc)::value;
+            const size_t smem = (size_t)kBwdStages * 3 * kChunk * kCols * sizeof(T) +
+                                (size_t)2 * (2 * kWb + sp.cluster) * 32 * sizeof(Map2);
+            auto go = [&](auto kernel) {
+                return launch_cluster(kernel, units, sp, smem, s, t[0].map, t[1].map, t[2].map, t[3].map, t[4].map, f,
+                                      sp.cluster, err);
+            };
+            return wide ? go(gated_bwd_kernel<T, S, true>) : go(gated_bwd_kernel<T, S, false>);
         });
+    }
     if (e == cudaSuccess) {
-        gated_sum_kernel<<<gx, 128, 0, s>>>((const float *)a->workspace, a->B, a->D, a->dA_log, a->d_dt_bias);
+        gated_sum_kernel<<<(unsigned)((a->D + 31) / 32), dim3(32, 8), 0, s>>>((const float *)a->workspace, shares,
+                                                                              a->D, a->dA_log, a->d_dt_bias);
         count_launches(1);
         e = cudaGetLastError();
     }

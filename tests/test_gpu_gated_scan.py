@@ -1,15 +1,18 @@
 """The channel-wise gated recurrence on the GPU against its fp64 definition.
 
 Tolerances: an io-typed result is rounded once (half a step, eps / 2 of the
-value) on top of fp32 arithmetic.  Every decay and input factor is formed with
-a relative error of a few 2^-24 from z's own (z = dt + bias is rounded; softplus,
-exp and sqrt are good to a few units of 2^-24; log a enters the exponential with
-|log a| e^(log a) <= 1 / e): 2^-19 covers them together, and the magnitudes that
-the definition returns carry it through the recurrence and its adjoint.  Sums
+value) on top of fp32 arithmetic.  Every exponent and input factor is formed with
+a relative error of a few 2^-22 (z = dt + bias is rounded; the polynomial of
+log(1 + e), exp2 and sqrt are good to 2^-21.5 and better): 2^-19 covers them
+together.  A relative error delta of an exponent la is one of |la| delta of the
+decay e^la, so a decay counts 1 + |la| times; the magnitudes that the definition
+returns carry this through the recurrence and its adjoint.  Sums
 a rounded z shifts Delta by |z| 2^-24 of itself at most (d log softplus / dz = sigmoid(z) /
 softplus(z) <= 1), so beyond |z| = 32 that share, |z|_max 2^-24, is added to 2^-19.  A step
 below the normal fp32 range, Delta < 2^-126, may be taken as zero; with HM_INPUT_UNIT its
-sqrt(2 Delta e^A_log) reaches 2^-62.5 e^(A_log / 2), which is the absolute floor.  Sums
+sqrt(2 Delta e^A_log) reaches 2^-62.5 e^(A_log / 2), which is the absolute floor.  A
+decay below 2^-126 may be taken as zero, which shifts what it multiplies (the state or
+an adjoint, and in the gradients the rate and log a) by 2^-126 of that.  Sums
 over tokens add less than 2^-19 of their absolute sum (fp32 partial sums of at
 most a few thousand terms, relative 2^-24 each in a chain of at most 2^5 per level)."""
 import numpy as np
@@ -117,16 +120,18 @@ def _check(hm, c, io, scale, lengths=None, pad=0, backward=True):
         if k in got:
             assert np.all(got[k][~on] == 7.0), "rows of %s behind a sequence's end were written" % k
             got[k] = np.where(on[..., None], got[k], 0.0)
-    _near(got["y"], y, mag, half, "y", delta, tiny * np.abs(c["x"]).sum(1).max())
+    # the largest state, rate and log a of the case, for the decays flushed to zero
+    flush = 2.0 ** -126 * (1 + mag.max()) * (1 + np.exp(c["A_log"].max())) * (1 + z * np.exp(c["A_log"].max())) if L else 0.0
+    _near(got["y"], y, mag, half, "y", delta, tiny * np.abs(c["x"]).sum(1).max() + flush)
     last = mag.max(1) if L else np.zeros_like(h)      # a bound of the last magnitude, padded batches too
-    _near(got["h_out"], h, last + np.abs(h), 2.0 ** -24, "h_out", delta, tiny * np.abs(c["x"]).sum(1).max() if L else 0.0)
+    _near(got["h_out"], h, last + np.abs(h), 2.0 ** -24, "h_out", delta, tiny * np.abs(c["x"]).sum(1).max() + flush if L else 0.0)
     if backward:
         want = around.gated_scan_bwd(c["x"], c["dt"], c["dy"], c["A_log"], dh_out=c["dh_out"], **kw)
         # every adjoint is at most the sum of what enters it
         grad = (np.abs(c["dy"]).sum(1).max() + np.abs(c["dh_out"]).max()) * (1 + np.abs(c["x"]).max()) if L else 0.0
         for k, (v, m) in want.items():
             _near(got[k], v, m, half if k in ("dx", "ddt") else 2.0 ** -24, k, delta,
-                  tiny * grad * (B * L if k in ("dA_log", "d_dt_bias") else 1))
+                  (tiny + flush) * grad * (B * L if k in ("dA_log", "d_dt_bias") else 1))
     return got
 
 
