@@ -2,11 +2,15 @@
 // post-norm, SiLU gate, scaled residual sum and the next block's pre-norm.
 //
 // Bandwidth-bound: five row arrays forward, eight backward, each touched once.
-// A block of threads holds a row in registers: statistics come from there
-// (mean first, then the centred squares), so nothing is read twice.  In the
-// backward each thread keeps its columns' parameter gradients in registers
-// over all its rows; the blocks' shares are summed in a second, small kernel
-// in a fixed order.
+// A team of warps holds a row in registers: statistics come from there (mean
+// first, then the centred squares), so nothing is read twice.
+//
+// Forward: a warp takes up to 2048 bf16 (1024 fp32) elements of a row, so a
+// row of that width needs no barrier, its sums cost five shuffles per 64
+// elements of a lane, and all its loads are in flight at once.  Backward: each
+// thread keeps the five parameter gradients of its columns in registers over
+// all its rows (40 of them for 8 columns), so there a block shares a row; the
+// blocks' shares are summed by a second, small kernel in a fixed order.
 #include "hm_internal.h"
 
 namespace hm {
@@ -15,65 +19,98 @@ namespace {
 
 constexpr int kE = 8;   // elements of a thread per piece
 
-// Columns of thread `tid`: with VEC pieces of 8 consecutive elements, else
-// single elements a block's width apart (both coalesced).
+// Columns of thread `tid` of a team of nthr: with VEC pieces of 8 consecutive
+// elements, else single elements a team's width apart (both coalesced).
 template <bool VEC>
 __device__ __forceinline__ int col_of(int piece, int j, int tid, int nthr) {
     return VEC ? (piece * nthr + tid) * kE + j : (piece * kE + j) * nthr + tid;
 }
 
-__device__ __forceinline__ void unpack8(const __nv_bfloat16 *p, float *f) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// 8 elements as loaded
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "l"(p));
     }
-}
-__device__ __forceinline__ void unpack8(const float *p, float *f) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void pack8(__nv_bfloat16 *p, const float *f) {
-    uint32_t w[4];
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void set(const float *f) {
+        uint32_t *u = &w.x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
     }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void pack8(float *p, const float *f) {
-    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
-}
+    __device__ __forceinline__ void get(float *f) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { __stcs(reinterpret_cast<uint4 *>(p), w); }
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w)
+                     : "l"(p));
+        asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(b.x), "=f"(b.y), "=f"(b.z), "=f"(b.w)
+                     : "l"(p + 4));
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void set(const float *f) {
+        a = make_float4(f[0], f[1], f[2], f[3]);
+        b = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ void get(float *f) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    __device__ __forceinline__ void store(float *p) const {
+        __stcs(reinterpret_cast<float4 *>(p), a);
+        __stcs(reinterpret_cast<float4 *>(p + 4), b);
+    }
+};
 
+// a piece of a row; columns behind D are zero
 template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T *row, int piece, int tid, int nthr, int D, float *f) {
+__device__ __forceinline__ Raw8<T> load8(const T *row, int piece, int tid, int nthr, int D) {
+    Raw8<T> r;
     if (VEC) {
         const int c = col_of<true>(piece, 0, tid, nthr);
-        if (c < D) {
-            unpack8(row + c, f);
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < kE; ++j) f[j] = 0.f;
+        if (c < D) r.load(row + c);
+        else r.zero();
     } else {
+        float f[kE];
 #pragma unroll
         for (int j = 0; j < kE; ++j) {
             const int c = col_of<false>(piece, j, tid, nthr);
             f[j] = c < D ? hm_ld(row, c) : 0.f;
         }
+        r.set(f);
     }
+    return r;
 }
 
 template <bool VEC, typename T>
 __device__ __forceinline__ void store8(T *row, int piece, int tid, int nthr, int D, const float *f) {
     if (VEC) {
         const int c = col_of<true>(piece, 0, tid, nthr);
-        if (c < D) pack8(row + c, f);
+        if (c < D) {
+            Raw8<T> r;
+            r.set(f);
+            r.store(row + c);
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < kE; ++j) {
@@ -83,134 +120,175 @@ __device__ __forceinline__ void store8(T *row, int piece, int tid, int nthr, int
     }
 }
 
-// fp32 parameters of a thread's columns (any 4-byte alignment), or the default
+// fp32 parameters of a thread's columns, or the default.  The same for every
+// row, so they stay in L1, which the rows themselves pass by.
 template <bool VEC>
 __device__ __forceinline__ void param8(const float *p, float dflt, int piece, int tid, int nthr, int D, float *f) {
+    if (VEC) {
+        const int c = col_of<true>(piece, 0, tid, nthr);
+        if (p && c < D) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(p + c));
+            const float4 b = __ldg(reinterpret_cast<const float4 *>(p + c + 4));
+            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+            return;
+        }
 #pragma unroll
-    for (int j = 0; j < kE; ++j) {
-        const int c = col_of<VEC>(piece, j, tid, nthr);
-        f[j] = p && c < D ? p[c] : dflt;
+        for (int j = 0; j < kE; ++j) f[j] = dflt;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kE; ++j) {
+            const int c = col_of<VEC>(piece, j, tid, nthr);
+            f[j] = p && c < D ? __ldg(p + c) : dflt;
+        }
     }
 }
 
-// Sum over the block of two values; every thread gets them.  `red` holds 2 x
-// 32 floats and alternates, so one barrier per call is enough: a call's reads
-// are separated from the next-but-one call's writes by the next call's barrier.
-__device__ __forceinline__ float2 block_sum2(float a, float b, float2 (*red)[32], int &turn) {
-    a = warp_sum(a);
-    b = warp_sum(b);
+// Sum of N values over the team (a warp, or with BLOCK the whole block); every
+// thread gets them, the warps' in order.  `red` alternates between two
+// buffers, so one barrier per call is enough: a call's reads are separated
+// from the next-but-one call's writes by the next call's barrier.
+template <bool BLOCK, int N>
+__device__ __forceinline__ void team_sum(float *v, float (*red)[32][N], int &turn) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (!BLOCK) return;
+    float (*r)[N] = red[turn & 1];
+    ++turn;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[threadIdx.x >> 5][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = r[0][i];
     const int nw = blockDim.x >> 5;
-    if (nw > 1) {
-        float2 *r = red[turn & 1];
-        ++turn;
-        if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        const float2 v = (threadIdx.x & 31) < nw ? r[threadIdx.x & 31] : make_float2(0.f, 0.f);
-        a = warp_sum(v.x);
-        b = warp_sum(v.y);
-    }
-    return make_float2(a, b);
+    for (int w = 1; w < nw; ++w)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += r[w][i];
 }
 
-// mean (0 for RMS) and 1 / sqrt(mean square + eps) of up to two rows at once
-template <bool VEC, int NV>
-__device__ __forceinline__ void stats2(const float (*u)[kE], const float (*v)[kE], bool layer, int D, float eps,
-                                       float2 (*red)[32], int &turn, float2 &mean, float2 &rstd) {
-    const int tid = threadIdx.x, n = blockDim.x;
-    mean = make_float2(0.f, 0.f);
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// One row per team: a warp of four (BLOCK false), or the block.
+template <typename T, bool VEC, int NV, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 512 : 128) norm_gate_fwd_kernel(hm_norm_gate_args p) {
+    __shared__ float red[2][32][1];
+    int turn = 0;
+    const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nthr = BLOCK ? blockDim.x : 32, D = (int)p.D;
+    const float inv = 1.f / (float)D;
+    const bool layer = p.norm == HM_NORM_LAYER;
+    const int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= p.rows) return;         // whole teams
+    Raw8<T> ry[NV], rg[NV], rr[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        ry[k] = load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
+        if (p.gate) rg[k] = load8<VEC>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D);
+        if (p.r) rr[k] = load8<VEC>((const T *)p.r + row * p.r_stride, k, tid, nthr, D);
+        else rr[k].zero();
+    }
+    float mean = 0.f, rstd = 1.f;
+    if (p.post) {
+        float f[kE], v[1] = {0.f};
+        if (layer) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                ry[k].get(f);
+#pragma unroll
+                for (int j = 0; j < kE; ++j) v[0] += f[j];
+            }
+            team_sum<BLOCK, 1>(v, red, turn);
+            mean = v[0] * inv;
+            v[0] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            ry[k].get(f);
+#pragma unroll
+            for (int j = 0; j < kE; ++j) {
+                const float d = col_of<VEC>(k, j, tid, nthr) < D ? f[j] - mean : 0.f;
+                v[0] = fmaf(d, d, v[0]);
+            }
+        }
+        team_sum<BLOCK, 1>(v, red, turn);
+        rstd = rsqrtf(v[0] * inv + p.eps);
+    }
+    float r[NV][kE], v[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        float u[kE], w[kE], c[kE];
+        ry[k].get(u);
+        rr[k].get(r[k]);
+        if (p.post) {
+            param8<VEC>(p.post_w, 1.f, k, tid, nthr, D, w);
+#pragma unroll
+            for (int j = 0; j < kE; ++j) u[j] = (u[j] - mean) * rstd * w[j];
+            if (p.post_b) {
+                param8<VEC>(p.post_b, 0.f, k, tid, nthr, D, c);
+#pragma unroll
+                for (int j = 0; j < kE; ++j) u[j] += c[j];
+            }
+        }
+        if (p.gate) {
+            rg[k].get(c);
+#pragma unroll
+            for (int j = 0; j < kE; ++j) u[j] *= c[j] * sigmoid(c[j]);
+        }
+        param8<VEC>(p.scale, 1.f, k, tid, nthr, D, w);
+#pragma unroll
+        for (int j = 0; j < kE; ++j) {
+            // columns behind D hold zero, for the sums below
+            r[k][j] = col_of<VEC>(k, j, tid, nthr) < D ? fmaf(p.alpha * w[j], u[j], r[k][j]) : 0.f;
+            v[0] += layer ? r[k][j] : r[k][j] * r[k][j];
+        }
+        if (p.r_out) store8<VEC>((T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D, r[k]);
+    }
+    if (!p.xn) return;
+    team_sum<BLOCK, 1>(v, red, turn);
+    mean = 0.f;
     if (layer) {
-        float a = 0.f, b = 0.f;
+        mean = v[0] * inv;
+        v[0] = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
-                a += u[k][j];
-                if (v) b += v[k][j];
+                const float d = col_of<VEC>(k, j, tid, nthr) < D ? r[k][j] - mean : 0.f;
+                v[0] = fmaf(d, d, v[0]);
             }
-        mean = block_sum2(a, b, red, turn);
-        mean.x /= (float)D;
-        mean.y /= (float)D;
+        team_sum<BLOCK, 1>(v, red, turn);
     }
-    float a = 0.f, b = 0.f;
+    rstd = rsqrtf(v[0] * inv + p.eps);
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+        float w[kE], c[kE];
+        param8<VEC>(p.pre_w, 1.f, k, tid, nthr, D, w);
 #pragma unroll
-        for (int j = 0; j < kE; ++j)
-            if (col_of<VEC>(k, j, tid, n) < D) {
-                const float d = u[k][j] - mean.x;
-                a = fmaf(d, d, a);
-                if (v) {
-                    const float e = v[k][j] - mean.y;
-                    b = fmaf(e, e, b);
-                }
-            }
-    const float2 q = block_sum2(a, b, red, turn);
-    rstd.x = rsqrtf(q.x / (float)D + eps);
-    rstd.y = rsqrtf(q.y / (float)D + eps);
-}
-
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
-
-template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(1024) norm_gate_fwd_kernel(hm_norm_gate_args p) {
-    __shared__ float2 red[2][32];
-    int turn = 0;
-    const int tid = threadIdx.x, nthr = blockDim.x, D = (int)p.D;
-    const bool layer = p.norm == HM_NORM_LAYER;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        float u[NV][kE], r[NV][kE], g[NV][kE], w[kE], c[kE];
+        for (int j = 0; j < kE; ++j) r[k][j] = (r[k][j] - mean) * rstd * w[j];
+        if (p.pre_b) {
+            param8<VEC>(p.pre_b, 0.f, k, tid, nthr, D, c);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D, u[k]);
-            if (p.gate) load8<VEC>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D, g[k]);
-            if (p.r) load8<VEC>((const T *)p.r + row * p.r_stride, k, tid, nthr, D, r[k]);
-            else
-#pragma unroll
-                for (int j = 0; j < kE; ++j) r[k][j] = 0.f;
+            for (int j = 0; j < kE; ++j) r[k][j] += c[j];
         }
-        float2 mean, rstd;
-        if (p.post) {
-            stats2<VEC, NV>(u, nullptr, layer, D, p.eps, red, turn, mean, rstd);
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                param8<VEC>(p.post_w, 1.f, k, tid, nthr, D, w);
-                param8<VEC>(p.post_b, 0.f, k, tid, nthr, D, c);
-#pragma unroll
-                for (int j = 0; j < kE; ++j) u[k][j] = fmaf((u[k][j] - mean.x) * rstd.x, w[j], c[j]);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            param8<VEC>(p.scale, 1.f, k, tid, nthr, D, w);
-#pragma unroll
-            for (int j = 0; j < kE; ++j) {
-                const float m = p.gate ? u[k][j] * g[k][j] * sigmoid(g[k][j]) : u[k][j];
-                // columns behind D hold zero, for the sums below
-                r[k][j] = col_of<VEC>(k, j, tid, nthr) < D ? fmaf(p.alpha * w[j], m, r[k][j]) : 0.f;
-            }
-            if (p.r_out) store8<VEC>((T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D, r[k]);
-        }
-        if (p.xn) {
-            stats2<VEC, NV>(r, nullptr, layer, D, p.eps, red, turn, mean, rstd);
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                param8<VEC>(p.pre_w, 1.f, k, tid, nthr, D, w);
-                param8<VEC>(p.pre_b, 0.f, k, tid, nthr, D, c);
-#pragma unroll
-                for (int j = 0; j < kE; ++j) r[k][j] = fmaf((r[k][j] - mean.x) * rstd.x, w[j], c[j]);
-                store8<VEC>((T *)p.xn + row * p.xn_stride, k, tid, nthr, D, r[k]);
-            }
-        }
+        store8<VEC>((T *)p.xn + row * p.xn_stride, k, tid, nthr, D, r[k]);
     }
 }
 
-// part[(blockIdx.x * 5 + i) * D + c]: this block's share of dscale, dpost_w,
-// dpost_b, dpre_w, dpre_b
-template <typename T, bool VEC, int NV>
-__global__ void __launch_bounds__(512) norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
-    __shared__ float2 red[2][32];
+// A team per row (the block, or with BLOCK false each warp), rows `teams`
+// apart, the next row's loads under way while one is worked on.
+// part[(team * 5 + i) * D + c]: the team's share of dscale, dpost_w, dpost_b,
+// dpre_w, dpre_b.
+template <typename T, bool VEC, int NV, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 512 : 256, NV == 1 && !BLOCK ? 2 : 1)
+norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
+    __shared__ float red[2][32][2];
     int turn = 0;
-    const int tid = threadIdx.x, nthr = blockDim.x, D = (int)p.D;
+    const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nthr = BLOCK ? blockDim.x : 32, D = (int)p.D;
+    const float inv = 1.f / (float)D;
+    const int64_t team = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t teams = BLOCK ? (int64_t)gridDim.x : (int64_t)gridDim.x * 8;
     const bool layer = p.norm == HM_NORM_LAYER;
     float acc[5][NV][kE];
 #pragma unroll
@@ -219,53 +297,86 @@ __global__ void __launch_bounds__(512) norm_gate_bwd_kernel(hm_norm_gate_bwd_arg
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int j = 0; j < kE; ++j) acc[i][k][j] = 0.f;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    Raw8<T> ry[NV], rg[NV], rr[NV], rd[NV], re[NV];
+    auto fetch = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            ry[k] = load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
+            if (p.gate) rg[k] = load8<VEC>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D);
+            if (p.dxn) {
+                rr[k] = load8<VEC>((const T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D);
+                re[k] = load8<VEC>((const T *)p.dxn + row * p.dxn_stride, k, tid, nthr, D);
+            }
+            if (p.dr_out) rd[k] = load8<VEC>((const T *)p.dr_out + row * p.dr_out_stride, k, tid, nthr, D);
+            else rd[k].zero();
+        }
+    };
+    if (team < p.rows) fetch(team);
+    for (int64_t row = team; row < p.rows; row += teams) {
         float y[NV][kE], r[NV][kE], d[NV][kE], e[NV][kE], g[NV][kE], w[kE], c[kE];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D, y[k]);
-            if (p.gate) load8<VEC>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D, g[k]);
-            if (p.dxn) {
-                load8<VEC>((const T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D, r[k]);
-                load8<VEC>((const T *)p.dxn + row * p.dxn_stride, k, tid, nthr, D, e[k]);
-            }
-            if (p.dr_out) load8<VEC>((const T *)p.dr_out + row * p.dr_out_stride, k, tid, nthr, D, d[k]);
-            else
-#pragma unroll
-                for (int j = 0; j < kE; ++j) d[k][j] = 0.f;
+            ry[k].get(y[k]);
+            if (p.gate) rg[k].get(g[k]);
+            if (p.dxn) rr[k].get(r[k]), re[k].get(e[k]);
+            rd[k].get(d[k]);
         }
-        float2 mean = make_float2(0.f, 0.f), rstd = make_float2(1.f, 1.f);
+        if (row + teams < p.rows) fetch(row + teams);
+        // statistics of y and of r_out
+        float mean[2] = {0.f, 0.f}, v[2];
+        if (layer) {
+            v[0] = v[1] = 0.f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int j = 0; j < kE; ++j) {
+                    v[0] += y[k][j];
+                    if (p.dxn) v[1] += r[k][j];
+                }
+            team_sum<BLOCK, 2>(v, red, turn);
+            mean[0] = p.post ? v[0] * inv : 0.f;
+            mean[1] = v[1] * inv;
+        }
+        v[0] = v[1] = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < kE; ++j)
+                if (col_of<VEC>(k, j, tid, nthr) < D) {
+                    const float a = y[k][j] - mean[0];
+                    v[0] = fmaf(a, a, v[0]);
+                    if (p.dxn) {
+                        const float b = r[k][j] - mean[1];
+                        v[1] = fmaf(b, b, v[1]);
+                    }
+                }
+        team_sum<BLOCK, 2>(v, red, turn);
+        const float rsy = p.post ? rsqrtf(v[0] * inv + p.eps) : 1.f, rsr = rsqrtf(v[1] * inv + p.eps);
         if (p.dxn) {
-            stats2<VEC, NV>(r, p.post ? y : nullptr, layer, D, p.eps, red, turn, mean, rstd);
             // dr = dr_out + rstd (w e - mean(w e) - u mean(w e u)), u = (r - mean) rstd
-            float s0 = 0.f, s1 = 0.f;
+            v[0] = v[1] = 0.f;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 param8<VEC>(p.pre_w, 1.f, k, tid, nthr, D, w);
 #pragma unroll
                 for (int j = 0; j < kE; ++j) {
-                    const float u = (r[k][j] - mean.x) * rstd.x;
+                    const float u = (r[k][j] - mean[1]) * rsr;
                     acc[3][k][j] = fmaf(e[k][j], u, acc[3][k][j]);
                     acc[4][k][j] += e[k][j];
                     r[k][j] = u;
                     e[k][j] *= w[j];      // zero behind D
-                    s0 += e[k][j];
-                    s1 = fmaf(e[k][j], u, s1);
+                    v[0] += e[k][j];
+                    v[1] = fmaf(e[k][j], u, v[1]);
                 }
             }
-            const float2 s = block_sum2(s0, s1, red, turn);
-            const float m0 = layer ? s.x / (float)D : 0.f, m1 = s.y / (float)D;
+            team_sum<BLOCK, 2>(v, red, turn);
+            const float m0 = layer ? v[0] * inv : 0.f, m1 = v[1] * inv;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < kE; ++j) d[k][j] += rstd.x * (e[k][j] - m0 - r[k][j] * m1);
-        } else if (p.post) {
-            float2 m1, r1;
-            stats2<VEC, NV>(y, nullptr, layer, D, p.eps, red, turn, m1, r1);
-            mean.y = m1.x;
-            rstd.y = r1.x;
+                for (int j = 0; j < kE; ++j) d[k][j] = fmaf(rsr, e[k][j] - fmaf(r[k][j], m1, m0), d[k][j]);
         }
-        float s0 = 0.f, s1 = 0.f;
+        v[0] = v[1] = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (p.dr) store8<VEC>((T *)p.dr + row * p.dr_stride, k, tid, nthr, D, d[k]);
@@ -276,7 +387,7 @@ __global__ void __launch_bounds__(512) norm_gate_bwd_kernel(hm_norm_gate_bwd_arg
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
                 const bool in = col_of<VEC>(k, j, tid, nthr) < D;
-                const float u = p.post ? (y[k][j] - mean.y) * rstd.y : y[k][j];
+                const float u = (y[k][j] - mean[0]) * rsy;
                 const float n = p.post ? fmaf(u, pw[j], pb[j]) : u;
                 const float dm = in ? d[k][j] * (p.alpha * c[j]) : 0.f;
                 float m = n, dn = dm;
@@ -284,25 +395,25 @@ __global__ void __launch_bounds__(512) norm_gate_bwd_kernel(hm_norm_gate_bwd_arg
                     const float sg = sigmoid(g[k][j]), si = g[k][j] * sg;
                     m = n * si;
                     dn = dm * si;
-                    g[k][j] = dm * n * sg * (1.f + g[k][j] * (1.f - sg));
+                    g[k][j] = dm * n * fmaf(si, 1.f - sg, sg);
                 }
                 if (in) acc[0][k][j] = fmaf(d[k][j], p.alpha * m, acc[0][k][j]);
                 acc[1][k][j] = fmaf(dn, u, acc[1][k][j]);
                 acc[2][k][j] += dn;
                 y[k][j] = u;
                 d[k][j] = p.post ? dn * pw[j] : dn;
-                s0 += d[k][j];
-                s1 = fmaf(d[k][j], u, s1);
+                v[0] += d[k][j];
+                v[1] = fmaf(d[k][j], u, v[1]);
             }
             if (p.gate) store8<VEC>((T *)p.dgate + row * p.dgate_stride, k, tid, nthr, D, g[k]);
         }
         if (p.post) {
-            const float2 s = block_sum2(s0, s1, red, turn);
-            const float m0 = layer ? s.x / (float)D : 0.f, m1 = s.y / (float)D;
+            team_sum<BLOCK, 2>(v, red, turn);
+            const float m0 = layer ? v[0] * inv : 0.f, m1 = v[1] * inv;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < kE; ++j) d[k][j] = rstd.y * (d[k][j] - m0 - y[k][j] * m1);
+                for (int j = 0; j < kE; ++j) d[k][j] = rsy * (d[k][j] - fmaf(y[k][j], m1, m0));
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) store8<VEC>((T *)p.dy + row * p.dy_stride, k, tid, nthr, D, d[k]);
@@ -314,7 +425,7 @@ __global__ void __launch_bounds__(512) norm_gate_bwd_kernel(hm_norm_gate_bwd_arg
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
                 const int c = col_of<VEC>(k, j, tid, nthr);
-                if (c < D) part[((int64_t)blockIdx.x * 5 + i) * D + c] = acc[i][k][j];
+                if (c < D) part[(team * 5 + i) * D + c] = acc[i][k][j];
             }
 }
 
@@ -322,16 +433,18 @@ struct GradPtrs {
     float *out[5];
 };
 
-// the blocks' shares summed in block order; a block of threads per 32 columns
+// the teams' shares summed in a fixed order; a block of threads per 32 columns
 // and parameter, 8 rows of it walking the shares
-__global__ void __launch_bounds__(256) norm_gate_sum_kernel(const float *part, int blocks, int D, GradPtrs g) {
+__global__ void __launch_bounds__(256) norm_gate_sum_kernel(const float *part, int teams, int D, GradPtrs g) {
     __shared__ float s[8][33];
     float *out = g.out[blockIdx.y];
     if (!out) return;
     const int c = blockIdx.x * 32 + threadIdx.x;
     float v = 0.f;
-    if (c < D)
-        for (int b = threadIdx.y; b < blocks; b += 8) v += part[((int64_t)b * 5 + blockIdx.y) * D + c];
+    if (c < D) {
+#pragma unroll 4
+        for (int b = threadIdx.y; b < teams; b += 8) v += part[((int64_t)b * 5 + blockIdx.y) * D + c];
+    }
     s[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.y == 0 && c < D) {
@@ -351,7 +464,6 @@ struct Row {
 };
 
 constexpr int64_t kMaxD = 16384;
-constexpr int64_t kBwdBlocks = 148 * 2;
 
 size_t esize(hm_dtype t) { return t == HM_BF16 ? 2 : 4; }
 
@@ -381,18 +493,36 @@ bool wide(const Row &r, size_t es) {
     return !r.p || ((((uintptr_t)r.p) & 15) == 0 && (r.stride * (int64_t)es) % 16 == 0);
 }
 
-struct Shape {
-    int nthr, nv;
+struct Team {
+    int nthr, nv;        // threads that share a row (32: a warp), pieces of 8 columns per thread
+    int blocks;          // backward
 };
 
-// the fewest pieces per thread that 1024 threads cover the row with, then
-// the fewest whole warps
-Shape shape_of(int64_t D, int most) {
+// Forward: a warp per row up to 8 pieces a lane (4 of fp32, as many
+// registers); more warps for wider rows, and for so few rows that one warp
+// each would leave most of the GPU idle.
+Team fwd_team(int64_t rows, int64_t D, size_t es) {
+    const int pieces = (int)((D + 32 * kE - 1) / (32 * kE)), most = es == 2 ? 8 : 4;
+    int warps = 1;
+    while ((pieces + warps - 1) / warps > most) warps *= 2;
+    while (warps < 16 && (pieces + warps - 1) / warps > 1 && rows * warps * 2 <= 148 * 16) warps *= 2;
     int nv = 1;
-    while ((int64_t)nv * kE * most < D) nv *= 2;
-    const int thr = (int)((D + (int64_t)nv * kE - 1) / ((int64_t)nv * kE));
-    return {(thr + 31) / 32 * 32, nv};
+    while (nv * warps < pieces) nv *= 2;
+    return {warps * 32, nv, 0};
 }
+
+// Backward: as many threads as there are pieces in a row, up to 512; blocks
+// (or warps) to fill the SMs once at 512 threads each.
+Team bwd_team(int64_t rows, int64_t D) {
+    const int pieces = (int)((D + 32 * kE - 1) / (32 * kE));
+    int nv = 1;
+    while (nv * 16 < pieces) nv *= 2;
+    const int warps = (pieces + nv - 1) / nv;
+    const int64_t most = warps == 1 ? 148 * 2 : 148 * (16 / warps), need = warps == 1 ? (rows + 7) / 8 : rows;
+    return {warps * 32, nv, (int)(need < most ? need : most)};
+}
+
+int64_t bwd_shares(const Team &t) { return t.nthr == 32 ? t.blocks * 8LL : t.blocks; }
 
 }  // namespace
 
@@ -423,39 +553,40 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
         vec = vec && wide(r, es);
     }
     const void *params[] = {a->scale, a->post_w, a->post_b, a->pre_w, a->pre_b};
-    for (const void *q : params)
+    for (const void *q : params) {
         if (((uintptr_t)q & 3) != 0) return fail_args(HM_ERR_INVALID_ARG, "%s: misaligned parameter", w);
+        vec = vec && ((uintptr_t)q & 15) == 0;
+    }
     if (a->rows == 0) return HM_OK;
     if (!a->r_out && !a->xn) return fail_args(HM_ERR_INVALID_ARG, "%s: r_out and xn are both NULL", w);
     if (a->r_out == a->xn) return fail_args(HM_ERR_INVALID_ARG, "%s: r_out and xn are the same array", w);
-    const Shape sh = shape_of(a->D, 1024);
-    const unsigned grid = (unsigned)(a->rows < (1 << 30) ? a->rows : (1 << 30));
+    const Team t = fwd_team(a->rows, a->D, es);
+    const bool block = t.nthr > 32;
+    const int64_t blocks = block ? a->rows : (a->rows + 3) / 4;
+    if (blocks > 0x7fffffffLL) return fail_args(HM_ERR_UNSUPPORTED, "%s: too many rows", w);
     cudaStream_t s = (cudaStream_t)stream;
-#define HM_FWD(T, V, N) norm_gate_fwd_kernel<T, V, N><<<grid, sh.nthr, 0, s>>>(*a)
-#define HM_FWD_N(T, V)              \
-    do {                            \
-        if (sh.nv == 1) HM_FWD(T, V, 1); \
-        else HM_FWD(T, V, 2);       \
-    } while (0)
+#define HM_FWD(T, V, N)                                                                            \
+    (block ? norm_gate_fwd_kernel<T, V, N, true><<<(unsigned)blocks, t.nthr, 0, s>>>(*a)           \
+           : norm_gate_fwd_kernel<T, V, N, false><<<(unsigned)blocks, 128, 0, s>>>(*a))
     if (a->io_dtype == HM_BF16) {
-        if (vec) HM_FWD_N(__nv_bfloat16, true);
-        else HM_FWD_N(__nv_bfloat16, false);
+        if (t.nv == 1) vec ? HM_FWD(__nv_bfloat16, true, 1) : HM_FWD(__nv_bfloat16, false, 1);
+        else if (t.nv == 2) vec ? HM_FWD(__nv_bfloat16, true, 2) : HM_FWD(__nv_bfloat16, false, 2);
+        else if (t.nv == 4) vec ? HM_FWD(__nv_bfloat16, true, 4) : HM_FWD(__nv_bfloat16, false, 4);
+        else vec ? HM_FWD(__nv_bfloat16, true, 8) : HM_FWD(__nv_bfloat16, false, 8);
     } else {
-        if (vec) HM_FWD_N(float, true);
-        else HM_FWD_N(float, false);
+        if (t.nv == 1) vec ? HM_FWD(float, true, 1) : HM_FWD(float, false, 1);
+        else if (t.nv == 2) vec ? HM_FWD(float, true, 2) : HM_FWD(float, false, 2);
+        else vec ? HM_FWD(float, true, 4) : HM_FWD(float, false, 4);
     }
 #undef HM_FWD
-#undef HM_FWD_N
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? HM_OK : fail_args(HM_ERR_CUDA, "%s launch: %s", w, cudaGetErrorString(e));
 }
 
-static int bwd_blocks(int64_t rows) { return (int)(rows < kBwdBlocks ? rows : kBwdBlocks); }
-
 extern "C" size_t hm_norm_gate_bwd_workspace_size(const hm_norm_gate_bwd_args *a) {
     if (!a || check_seam("norm_gate_bwd", a->rows, a->D, a->io_dtype, a->norm, a->eps, a->alpha) != HM_OK) return 0;
-    return (size_t)bwd_blocks(a->rows) * 5 * a->D * sizeof(float);
+    return (size_t)bwd_shares(bwd_team(a->rows, a->D)) * 5 * a->D * sizeof(float);
 }
 
 extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_t stream) {
@@ -481,20 +612,23 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
                             a->dpre_b};
     for (const void *q : params)
         if (((uintptr_t)q & 3) != 0) return fail_args(HM_ERR_INVALID_ARG, "%s: misaligned parameter", w);
+    for (int i = 0; i < 4; ++i) vec = vec && ((uintptr_t)params[i] & 15) == 0;    // those that are read
     const size_t need = hm_norm_gate_bwd_workspace_size(a);
     if (need > 0 && (!a->workspace || a->workspace_bytes < need || ((uintptr_t)a->workspace & 255) != 0))
         return fail_args(HM_ERR_INVALID_ARG, "%s: workspace of %zu bytes, 256-byte aligned, is needed", w, need);
-    const Shape sh = shape_of(a->D, 512);
-    const int grid = bwd_blocks(a->rows);
+    const Team t = bwd_team(a->rows, a->D);
+    const bool block = t.nthr > 32;
+    const int64_t shares = bwd_shares(t);
     cudaStream_t s = (cudaStream_t)stream;
     float *part = (float *)a->workspace;
-    if (grid > 0) {
-#define HM_BWD(T, V, N) norm_gate_bwd_kernel<T, V, N><<<grid, sh.nthr, 0, s>>>(*a, part)
-#define HM_BWD_N(T, V)                        \
-    do {                                      \
-        if (sh.nv == 1) HM_BWD(T, V, 1);      \
-        else if (sh.nv == 2) HM_BWD(T, V, 2); \
-        else HM_BWD(T, V, 4);                 \
+    if (t.blocks > 0) {
+#define HM_BWD(T, V, N) norm_gate_bwd_kernel<T, V, N, true><<<t.blocks, t.nthr, 0, s>>>(*a, part)
+#define HM_BWD_N(T, V)                                                                             \
+    do {                                                                                           \
+        if (!block) norm_gate_bwd_kernel<T, V, 1, false><<<t.blocks, 256, 0, s>>>(*a, part);       \
+        else if (t.nv == 1) HM_BWD(T, V, 1);                                                       \
+        else if (t.nv == 2) HM_BWD(T, V, 2);                                                       \
+        else HM_BWD(T, V, 4);                                                                      \
     } while (0)
         if (a->io_dtype == HM_BF16) {
             if (vec) HM_BWD_N(__nv_bfloat16, true);
@@ -511,7 +645,7 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     if (e == cudaSuccess) {
         // without dxn the pre-norm's parameters had no part in the loss: their shares are zero
         const GradPtrs g = {{a->dscale, a->dpost_w, a->dpost_b, a->dpre_w, a->dpre_b}};
-        norm_gate_sum_kernel<<<dim3((unsigned)((a->D + 31) / 32), 5), dim3(32, 8), 0, s>>>(part, grid, (int)a->D, g);
+        norm_gate_sum_kernel<<<dim3((unsigned)((a->D + 31) / 32), 5), dim3(32, 8), 0, s>>>(part, (int)shares, (int)a->D, g);
         count_launches(1);
         e = cudaGetLastError();
     }

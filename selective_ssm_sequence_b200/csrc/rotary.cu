@@ -1,11 +1,16 @@
 // rotary.cu -- rotary positions on queries and keys (hm_rotary).
 //
-// A thread takes P pairs (P = 8 bf16, 4 fp32: two 16-byte loads) of one token
-// and turns them in a run of heads: the angle depends on the token and the
-// pair alone, so its sine and cosine are formed once per run.  Angles are
-// kept as fractions of a turn in 64-bit fixed point: theta / (2 pi) mod 1
-// times 2^64 is an integer, and the product with the position wraps modulo
-// 2^64, which is the reduction modulo whole turns, exactly.
+// Bandwidth-bound: every element read and written once.  A thread takes P
+// pairs (P = 8 of bf16, 4 of fp32: two 16-byte loads; fewer where strides or
+// the pair count ask for it) of one token and turns them in a run of heads, q's
+// and then k's: the angle depends on the token and the pair alone, so its sine
+// and cosine are formed once per run.  The loads of four heads are in flight
+// together.
+//
+// Angles are kept as fractions of a turn in 64-bit fixed point: theta / (2 pi)
+// mod 1 times 2^64 is an integer (formed in fp64, once per block, in shared
+// memory), and its product with the position wraps modulo 2^64, which is the
+// reduction modulo whole turns, exactly.
 #include <math.h>
 
 #include "hm_internal.h"
@@ -18,15 +23,18 @@ struct Side {             // q or k
     const void *in;
     void *out;
     int64_t in_b, in_t, in_h, out_b, out_t, out_h;
-    int H;
 };
 
 struct RotArgs {
     Side s[2];
-    int64_t B, L;
+    int Hq, H;            // q's heads, all heads
+    int hg;               // heads of a run
+    int64_t L;
+    unsigned tokens;      // B * L
     int d, rot;
-    int runs_q, runs;     // runs of kHeads heads of q, of q and k
-    bool copy_tail;
+    int ng, nt;           // groups of P pairs; groups of 2 P elements behind rot (0 when left alone)
+    int per;              // items of a token: runs * (ng + nt)
+    int tb;               // tokens of a block
     const int64_t *positions;
     int64_t pos_b, pos_t, pos0;
     double log2_base;     // of the base in use (HM_ROTARY_NTK has put its factor in)
@@ -37,7 +45,8 @@ struct RotArgs {
     float mscale, sign;
 };
 
-constexpr int kHeads = 4;   // heads a thread turns by the same angles
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;   // heads whose loads are in flight together
 
 // theta_i / (2 pi) mod 1, in units of 2^-64 of a turn
 __device__ __forceinline__ unsigned long long pair_turns(const RotArgs &a, int i) {
@@ -61,40 +70,93 @@ __device__ __forceinline__ void turn_of(const RotArgs &a, unsigned long long uni
     sn *= a.mscale * a.sign;
 }
 
+// P elements, P * sizeof(T) = 2 .. 16 bytes
+template <typename T, int P>
+struct alignas(sizeof(T) * P) Vec {
+    T v[P];
+};
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f(float &o, float v) { o = v; }
+__device__ __forceinline__ void from_f(__nv_bfloat16 &o, float v) { o = __float2bfloat16_rn(v); }
+
+// the head's rows in and out
+template <typename T>
+__device__ __forceinline__ void head_of(const RotArgs &a, int h, int64_t b, int64_t t, const T *&in, T *&out) {
+    const Side &s = h < a.Hq ? a.s[0] : a.s[1];
+    const int i = h < a.Hq ? h : h - a.Hq;
+    in = (const T *)s.in + b * s.in_b + t * s.in_t + i * s.in_h;
+    out = (T *)s.out + b * s.out_b + t * s.out_t + i * s.out_h;
+}
+
 template <typename T, int P, bool INTER>
-__global__ void __launch_bounds__(256) rotary_kernel(RotArgs a) {
-    const int half = a.rot / 2, ng = (half + P - 1) / P;            // groups of P pairs
-    const int nt = a.copy_tail ? (a.d - a.rot + 2 * P - 1) / (2 * P) : 0;   // groups behind rot
-    const int64_t per = (int64_t)a.runs * (ng + nt);
-    const int64_t n = a.B * a.L * per;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t tok = i / per;
-        const int rest = (int)(i - tok * per), run = rest / (ng + nt), grp = rest - run * (ng + nt);
-        const int64_t b = tok / a.L, t = tok - b * a.L;
-        const Side &s = run < a.runs_q ? a.s[0] : a.s[1];
-        const int h0 = (run < a.runs_q ? run : run - a.runs_q) * kHeads;
-        const T *in = (const T *)s.in + b * s.in_b + t * s.in_t;
-        T *out = (T *)s.out + b * s.out_b + t * s.out_t;
-        if (grp >= ng) {
-            const int c0 = a.rot + (grp - ng) * 2 * P;
-            for (int h = h0; h < s.H && h < h0 + kHeads; ++h)
-                for (int c = c0; c < c0 + 2 * P && c < a.d; ++c) out[h * s.out_h + c] = in[h * s.in_h + c];
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotArgs a) {
+    __shared__ unsigned long long unit[512];
+    const int half = a.rot / 2;
+    for (int i = threadIdx.x; i < half; i += kThreads) unit[i] = pair_turns(a, i);
+    __syncthreads();
+    using V = Vec<T, P>;
+    const int groups = a.ng + a.nt;
+    for (int i = threadIdx.x; i < a.tb * a.per; i += kThreads) {
+        const int local = i / a.per, rest = i - local * a.per, run = rest / groups, grp = rest - run * groups;
+        const unsigned tok = blockIdx.x * (unsigned)a.tb + local;
+        if (tok >= a.tokens) break;
+        const int64_t b = tok / (unsigned)a.L, t = tok - (unsigned)b * (unsigned)a.L;
+        const int h0 = run * a.hg, h1 = min(h0 + a.hg, a.H);
+        if (grp >= a.ng) {             // elements behind rot
+            const int c0 = a.rot + (grp - a.ng) * 2 * P;
+            for (int h = h0; h < h1; ++h) {
+                const T *in;
+                T *out;
+                head_of(a, h, b, t, in, out);
+                if (c0 + P <= a.d) *reinterpret_cast<V *>(out + c0) = *reinterpret_cast<const V *>(in + c0);
+                if (c0 + 2 * P <= a.d)
+                    *reinterpret_cast<V *>(out + c0 + P) = *reinterpret_cast<const V *>(in + c0 + P);
+            }
             continue;
         }
         const int64_t pos = a.positions ? a.positions[b * a.pos_b + t * a.pos_t] : a.pos0 + t;
         float cs[P], sn[P];
 #pragma unroll
-        for (int j = 0; j < P; ++j) turn_of(a, pair_turns(a, grp * P + j), pos, cs[j], sn[j]);
-        for (int h = h0; h < s.H && h < h0 + kHeads; ++h)
+        for (int j = 0; j < P; ++j) turn_of(a, unit[grp * P + j], pos, cs[j], sn[j]);
+        const int iu = INTER ? grp * 2 * P : grp * P, iv = INTER ? iu + P : iu + half;
+        for (int hb = h0; hb < h1; hb += kBatch) {
+            V u[kBatch], v[kBatch];
 #pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const int pr = grp * P + j;
-                if (pr >= half) break;
-                const int iu = INTER ? 2 * pr : pr, iv = INTER ? 2 * pr + 1 : pr + half;
-                const float u = hm_ld(in, h * s.in_h + iu), v = hm_ld(in, h * s.in_h + iv);
-                hm_st(out, h * s.out_h + iu, u * cs[j] - v * sn[j]);
-                hm_st(out, h * s.out_h + iv, u * sn[j] + v * cs[j]);
-            }
+            for (int k = 0; k < kBatch; ++k)
+                if (hb + k < h1) {
+                    const T *in;
+                    T *out;
+                    head_of(a, hb + k, b, t, in, out);
+                    u[k] = *reinterpret_cast<const V *>(in + iu);
+                    v[k] = *reinterpret_cast<const V *>(in + iv);
+                }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (hb + k < h1) {
+                    const T *in;
+                    T *out;
+                    head_of(a, hb + k, b, t, in, out);
+                    V x, y;
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        // interleaved: element 2 j of the 2 P is u_j, 2 j + 1 is v_j
+                        const float p = to_f(INTER ? (2 * j < P ? u[k].v[2 * j % P] : v[k].v[2 * j % P]) : u[k].v[j]);
+                        const float q = to_f(INTER ? (2 * j + 1 < P ? u[k].v[(2 * j + 1) % P] : v[k].v[(2 * j + 1) % P])
+                                                   : v[k].v[j]);
+                        const float r = p * cs[j] - q * sn[j], w = p * sn[j] + q * cs[j];
+                        if (INTER) {
+                            from_f(2 * j < P ? x.v[2 * j % P] : y.v[2 * j % P], r);
+                            from_f(2 * j + 1 < P ? x.v[(2 * j + 1) % P] : y.v[(2 * j + 1) % P], w);
+                        } else {
+                            from_f(x.v[j], r);
+                            from_f(y.v[j], w);
+                        }
+                    }
+                    *reinterpret_cast<V *>(out + iu) = x;
+                    *reinterpret_cast<V *>(out + iv) = y;
+                }
+        }
     }
 }
 
@@ -141,8 +203,8 @@ extern "C" hm_status hm_rotary(const hm_rotary_args *a, hm_stream_t stream) {
     if (a->rot < 2 || a->rot % 2 != 0 || a->rot > a->d)
         return fail_args(HM_ERR_INVALID_ARG, "rotary: rot=%d must be even, from 2 to d=%d", a->rot, a->d);
     if (a->d > 1024) return fail_args(HM_ERR_UNSUPPORTED, "rotary: d=%d > 1024", a->d);
-    if (a->B > (1LL << 31) || a->L > (1LL << 31) || a->B * a->L > (1LL << 36))
-        return fail_args(HM_ERR_UNSUPPORTED, "rotary: need B, L <= 2^31 and B L <= 2^36");
+    if (a->B > (1LL << 30) || a->L > (1LL << 30) || a->B * a->L > (1LL << 30))
+        return fail_args(HM_ERR_UNSUPPORTED, "rotary: need B L <= 2^30");
     if (!finite_positive(a->base)) return fail_args(HM_ERR_INVALID_ARG, "rotary: base must be > 0");
     if (!(a->mscale - a->mscale == 0.0)) return fail_args(HM_ERR_INVALID_ARG, "rotary: mscale must be finite");
     if (a->scaling != HM_ROTARY_PLAIN && !finite_positive(a->factor))
@@ -165,15 +227,14 @@ extern "C" hm_status hm_rotary(const hm_rotary_args *a, hm_stream_t stream) {
     if (a->B == 0 || a->L == 0 || a->Hq + a->Hk == 0) return HM_OK;
 
     RotArgs r{};
-    r.s[0] = {a->q, a->q_out, is[0][0], is[0][1], is[0][2], os[0][0], os[0][1], os[0][2], a->Hq};
-    r.s[1] = {a->k, a->k_out, is[1][0], is[1][1], is[1][2], os[1][0], os[1][1], os[1][2], a->Hk};
-    r.B = a->B;
+    r.s[0] = {a->q, a->q_out, is[0][0], is[0][1], is[0][2], os[0][0], os[0][1], os[0][2]};
+    r.s[1] = {a->k, a->k_out, is[1][0], is[1][1], is[1][2], os[1][0], os[1][1], os[1][2]};
+    r.Hq = a->Hq;
+    r.H = a->Hq + a->Hk;
     r.L = a->L;
+    r.tokens = (unsigned)(a->B * a->L);
     r.d = a->d;
     r.rot = a->rot;
-    r.runs_q = (a->Hq + kHeads - 1) / kHeads;
-    r.runs = r.runs_q + (a->Hk + kHeads - 1) / kHeads;
-    r.copy_tail = a->rot < a->d && !((a->Hq == 0 || a->q == a->q_out) && (a->Hk == 0 || a->k == a->k_out));
     r.positions = a->positions;
     r.pos_b = a->pos_stride_b;
     r.pos_t = a->pos_stride_t;
@@ -189,19 +250,43 @@ extern "C" hm_status hm_rotary(const hm_rotary_args *a, hm_stream_t stream) {
     }
     r.mscale = (float)a->mscale;
     r.sign = a->transpose ? -1.f : 1.f;
-    const int P = a->io_dtype == HM_BF16 ? 8 : 4;
-    const int64_t per = (int64_t)r.runs * ((a->rot / 2 + P - 1) / P + (r.copy_tail ? (a->d - a->rot + 2 * P - 1) / (2 * P) : 0));
-    const int64_t blocks = (a->B * a->L * per + 255) / 256;
-    const unsigned grid = (unsigned)(blocks < (1 << 30) ? blocks : (1 << 30));
+    const bool copy = a->rot < a->d && !((a->Hq == 0 || a->q == a->q_out) && (a->Hk == 0 || a->k == a->k_out));
+    // the widest pieces that the pair count, the rest of the head and every row start allow
+    int P = a->io_dtype == HM_BF16 ? 8 : 4;
+    auto fits = [&](int n) {
+        if (a->rot / 2 % n || (copy && a->d % n)) return false;
+        const void *ptr[2][2] = {{a->q, a->q_out}, {a->k, a->k_out}};
+        const int64_t cnt[3] = {a->B, a->L, 0};
+        for (int i = 0; i < 2; ++i) {
+            const int H = i ? a->Hk : a->Hq;
+            if (H == 0) continue;
+            for (int j = 0; j < 2; ++j) {
+                if ((uintptr_t)ptr[i][j] % (n * es)) return false;
+                for (int k = 0; k < 3; ++k)
+                    if ((k < 2 ? cnt[k] : H) > 1 && (j ? os : is)[i][k] % n) return false;
+            }
+        }
+        return true;
+    };
+    while (P > 1 && !fits(P)) P /= 2;
+    r.ng = a->rot / 2 / P;
+    r.nt = copy ? (a->d - a->rot + 2 * P - 1) / (2 * P) : 0;
+    // runs of all heads once that fills the GPU, shorter ones before
+    r.hg = r.H;
+    while (r.hg > kBatch && (int64_t)r.tokens * r.ng * ((r.H + r.hg - 1) / r.hg) < 148 * 1024) r.hg = (r.hg + 1) / 2;
+    const int64_t per = (int64_t)((r.H + r.hg - 1) / r.hg) * (r.ng + r.nt);
+    if (per > (1 << 24)) return fail_args(HM_ERR_UNSUPPORTED, "rotary: too many heads");
+    r.per = (int)per;
+    r.tb = r.per >= kThreads ? 1 : kThreads / r.per;
+    const unsigned grid = (r.tokens + r.tb - 1) / r.tb;
     cudaStream_t s = (cudaStream_t)stream;
     const bool inter = a->layout == HM_ROTARY_INTERLEAVED;
-    if (a->io_dtype == HM_BF16) {
-        if (inter) rotary_kernel<__nv_bfloat16, 8, true><<<grid, 256, 0, s>>>(r);
-        else rotary_kernel<__nv_bfloat16, 8, false><<<grid, 256, 0, s>>>(r);
-    } else {
-        if (inter) rotary_kernel<float, 4, true><<<grid, 256, 0, s>>>(r);
-        else rotary_kernel<float, 4, false><<<grid, 256, 0, s>>>(r);
-    }
+#define HM_ROT(T, N)                                                     \
+    (inter ? rotary_kernel<T, N, true><<<grid, kThreads, 0, s>>>(r)      \
+           : rotary_kernel<T, N, false><<<grid, kThreads, 0, s>>>(r))
+    if (a->io_dtype == HM_BF16) P == 8 ? HM_ROT(__nv_bfloat16, 8) : P == 4 ? HM_ROT(__nv_bfloat16, 4) : P == 2 ? HM_ROT(__nv_bfloat16, 2) : HM_ROT(__nv_bfloat16, 1);
+    else P == 4 ? HM_ROT(float, 4) : P == 2 ? HM_ROT(float, 2) : HM_ROT(float, 1);
+#undef HM_ROT
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? HM_OK : fail_args(HM_ERR_CUDA, "rotary launch: %s", cudaGetErrorString(e));
