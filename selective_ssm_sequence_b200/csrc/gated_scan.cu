@@ -17,6 +17,7 @@
 // there is one launch and no scratch, and every sum has a fixed order.
 #include <type_traits>
 
+#include "packed.cuh"
 #include "tc_common.cuh"
 
 namespace hm {
@@ -50,37 +51,6 @@ __device__ __forceinline__ int64_t clamped_len(const int32_t *lengths, int64_t b
 
 // ------------------------------------------------------------------ gates
 
-// A thread's two channels as one packed register pair.  Held as 64 bits from
-// the load on, so that the packed instructions find their operands in place.
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 pk(float x, float y) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 un(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 splat(float v) { return pk(v, v); }
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 __device__ __forceinline__ F2 ex2(F2 a) {
     const float2 u = un(a);
     return pk(tc::ex2_approx(u.x), tc::ex2_approx(u.y));

@@ -11,13 +11,14 @@
 // thread keeps the five parameter gradients of its columns in registers over
 // all its rows (40 of them for 8 columns), so there a block shares a row; the
 // blocks' shares are summed by a second, small kernel in a fixed order.
-#include "hm_internal.h"
+#include "packed.cuh"
 
 namespace hm {
 
 namespace {
 
-constexpr int kE = 8;   // elements of a thread per piece
+constexpr int kE = 8;       // elements of a thread per piece
+constexpr int kP = kE / 2;  // pairs
 
 // Columns of thread `tid` of a team of nthr: with VEC pieces of 8 consecutive
 // elements, else single elements a team's width apart (both coalesced).
@@ -38,21 +39,14 @@ struct Raw8<__nv_bfloat16> {
                      : "l"(p));
     }
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void set(const float *f) {
-        uint32_t *u = &w.x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
+    __device__ __forceinline__ void set(const F2 *f) {
+        w = make_uint4(bf16_of(f[0]), bf16_of(f[1]), bf16_of(f[2]), bf16_of(f[3]));
     }
-    __device__ __forceinline__ void get(float *f) const {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
+    __device__ __forceinline__ void get(F2 *f) const {
+        f[0] = pk_bf16(w.x);
+        f[1] = pk_bf16(w.y);
+        f[2] = pk_bf16(w.z);
+        f[3] = pk_bf16(w.w);
     }
     __device__ __forceinline__ void store(__nv_bfloat16 *p) const { __stcs(reinterpret_cast<uint4 *>(p), w); }
 };
@@ -68,13 +62,16 @@ struct Raw8<float> {
                      : "l"(p + 4));
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void set(const float *f) {
-        a = make_float4(f[0], f[1], f[2], f[3]);
-        b = make_float4(f[4], f[5], f[6], f[7]);
+    __device__ __forceinline__ void set(const F2 *f) {
+        const float2 u0 = un(f[0]), u1 = un(f[1]), u2 = un(f[2]), u3 = un(f[3]);
+        a = make_float4(u0.x, u0.y, u1.x, u1.y);
+        b = make_float4(u2.x, u2.y, u3.x, u3.y);
     }
-    __device__ __forceinline__ void get(float *f) const {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    __device__ __forceinline__ void get(F2 *f) const {
+        f[0] = pk(a.x, a.y);
+        f[1] = pk(a.z, a.w);
+        f[2] = pk(b.x, b.y);
+        f[3] = pk(b.z, b.w);
     }
     __device__ __forceinline__ void store(float *p) const {
         __stcs(reinterpret_cast<float4 *>(p), a);
@@ -97,13 +94,14 @@ __device__ __forceinline__ Raw8<T> load8(const T *row, int piece, int tid, int n
             const int c = col_of<false>(piece, j, tid, nthr);
             f[j] = c < D ? hm_ld(row, c) : 0.f;
         }
-        r.set(f);
+        const F2 g[kP] = {pk(f[0], f[1]), pk(f[2], f[3]), pk(f[4], f[5]), pk(f[6], f[7])};
+        r.set(g);
     }
     return r;
 }
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T *row, int piece, int tid, int nthr, int D, const float *f) {
+__device__ __forceinline__ void store8(T *row, int piece, int tid, int nthr, int D, const F2 *f) {
     if (VEC) {
         const int c = col_of<true>(piece, 0, tid, nthr);
         if (c < D) {
@@ -115,7 +113,7 @@ __device__ __forceinline__ void store8(T *row, int piece, int tid, int nthr, int
 #pragma unroll
         for (int j = 0; j < kE; ++j) {
             const int c = col_of<false>(piece, j, tid, nthr);
-            if (c < D) hm_st(row, c, f[j]);
+            if (c < D) hm_st(row, c, j & 1 ? un(f[j / 2]).y : un(f[j / 2]).x);
         }
     }
 }
@@ -123,62 +121,110 @@ __device__ __forceinline__ void store8(T *row, int piece, int tid, int nthr, int
 // fp32 parameters of a thread's columns, or the default.  The same for every
 // row, so they stay in L1, which the rows themselves pass by.
 template <bool VEC>
-__device__ __forceinline__ void param8(const float *p, float dflt, int piece, int tid, int nthr, int D, float *f) {
+__device__ __forceinline__ void param8(const float *p, float dflt, int piece, int tid, int nthr, int D, F2 *f) {
     if (VEC) {
         const int c = col_of<true>(piece, 0, tid, nthr);
         if (p && c < D) {
             const float4 a = __ldg(reinterpret_cast<const float4 *>(p + c));
             const float4 b = __ldg(reinterpret_cast<const float4 *>(p + c + 4));
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+            f[0] = pk(a.x, a.y);
+            f[1] = pk(a.z, a.w);
+            f[2] = pk(b.x, b.y);
+            f[3] = pk(b.z, b.w);
             return;
         }
 #pragma unroll
-        for (int j = 0; j < kE; ++j) f[j] = dflt;
+        for (int j = 0; j < kP; ++j) f[j] = splat(dflt);
     } else {
+        float v[kE];
 #pragma unroll
         for (int j = 0; j < kE; ++j) {
             const int c = col_of<VEC>(piece, j, tid, nthr);
-            f[j] = p && c < D ? __ldg(p + c) : dflt;
+            v[j] = p && c < D ? __ldg(p + c) : dflt;
         }
+#pragma unroll
+        for (int j = 0; j < kP; ++j) f[j] = pk(v[2 * j], v[2 * j + 1]);
     }
 }
 
-// Sum of N values over the team (a warp, or with BLOCK the whole block); every
-// thread gets them, the warps' in order.  `red` alternates between two
-// buffers, so one barrier per call is enough: a call's reads are separated
-// from the next-but-one call's writes by the next call's barrier.
-template <bool BLOCK, int N>
-__device__ __forceinline__ void team_sum(float *v, float (*red)[32][N], int &turn) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if (!BLOCK) return;
-    float (*r)[N] = red[turn & 1];
-    ++turn;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) r[threadIdx.x >> 5][i] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = r[0][i];
-    const int nw = blockDim.x >> 5;
-    for (int w = 1; w < nw; ++w)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += r[w][i];
+// whether a thread has any element of the piece; with VEC (D a multiple of 8) all or none
+template <bool VEC>
+__device__ __forceinline__ bool has(int piece, int tid, int nthr, int D) {
+    return col_of<VEC>(piece, 0, tid, nthr) < D;
+}
+// f with the elements behind D set to zero (VEC: for a piece that has(); nothing to do)
+template <bool VEC>
+__device__ __forceinline__ F2 in_row(F2 f, int piece, int j, int tid, int nthr, int D) {
+    if (VEC) return f;
+    const float2 u = un(f);
+    return pk(col_of<false>(piece, 2 * j, tid, nthr) < D ? u.x : 0.f,
+              col_of<false>(piece, 2 * j + 1, tid, nthr) < D ? u.y : 0.f);
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+__device__ __forceinline__ float sum2(F2 f) {
+    const float2 u = un(f);
+    return u.x + u.y;
+}
+
+// Sum of one or two values over the team (a warp, or with BLOCK the whole
+// block); every thread gets them, always added in the same order.  `red`
+// alternates between two buffers, so one barrier per call is enough: a call's
+// reads are separated from the next-but-one call's writes by the next call's
+// barrier.
+__device__ __forceinline__ float xor_add(float v, int o) { return v + __shfl_xor_sync(0xffffffffu, v, o); }
+
+template <bool BLOCK>
+__device__ __forceinline__ float team_sum(float v, float (*red)[32], int &turn) {
+    v = warp_sum(v);
+    if (!BLOCK) return v;
+    float *r = red[turn & 1];
+    ++turn;
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (lane == 0) r[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = (lane & 15) < nw ? r[lane & 15] : 0.f;
+    return xor_add(xor_add(xor_add(xor_add(v, 8), 4), 2), 1);
+}
+
+template <bool BLOCK>
+__device__ __forceinline__ float2 team_sum2(float a, float b, float2 (*red)[32], int &turn) {
+    const int lane = threadIdx.x & 31;
+    // the lower half warp goes on with a, the upper with b
+    const bool up = (lane & 16) != 0;
+    float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+    v = xor_add(xor_add(xor_add(xor_add(v, 8), 4), 2), 1);
+    if (!BLOCK) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, 16);
+        return up ? make_float2(o, v) : make_float2(v, o);
+    }
+    float2 *r = red[turn & 1];
+    ++turn;
+    const int nw = blockDim.x >> 5;
+    if ((lane & 15) == 0) (&r[threadIdx.x >> 5].x)[up] = v;
+    __syncthreads();
+    const float2 t = (lane & 15) < nw ? r[lane & 15] : make_float2(0.f, 0.f);
+    return make_float2(xor_add(xor_add(xor_add(xor_add(t.x, 8), 4), 2), 1),
+                       xor_add(xor_add(xor_add(xor_add(t.y, 8), 4), 2), 1));
+}
+
+// 1 / (1 + e^-x): an e^-x beyond fp32 gives zero
+__device__ __forceinline__ F2 sigmoid(F2 x) {
+    float2 z = un(x * splat(-1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(z.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(z.y));
+    z = un(pk(z.x, z.y) + splat(1.f));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(z.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(z.y));
+    return pk(z.x, z.y);
+}
 
 // One row per team: a warp of four (BLOCK false), or the block.
-template <typename T, bool VEC, int NV, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 512 : 128) norm_gate_fwd_kernel(hm_norm_gate_args p) {
-    __shared__ float red[2][32][1];
+template <typename T, bool VEC, int NV, bool BLOCK, bool LAYER>
+__global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_norm_gate_args p) {
+    __shared__ float red[2][32];
     int turn = 0;
     const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nthr = BLOCK ? blockDim.x : 32, D = (int)p.D;
     const float inv = 1.f / (float)D;
-    const bool layer = p.norm == HM_NORM_LAYER;
     const int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= p.rows) return;         // whole teams
     Raw8<T> ry[NV], rg[NV], rr[NV];
@@ -191,86 +237,94 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) norm_gate_fwd_kernel(hm_nor
     }
     float mean = 0.f, rstd = 1.f;
     if (p.post) {
-        float f[kE], v[1] = {0.f};
-        if (layer) {
+        F2 f[kP], v = splat(0.f);
+        if (LAYER) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 ry[k].get(f);
 #pragma unroll
-                for (int j = 0; j < kE; ++j) v[0] += f[j];
+                for (int j = 0; j < kP; ++j) v = v + f[j];
             }
-            team_sum<BLOCK, 1>(v, red, turn);
-            mean = v[0] * inv;
-            v[0] = 0.f;
+            mean = team_sum<BLOCK>(sum2(v), red, turn) * inv;
+            v = splat(0.f);
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            if (LAYER && !has<VEC>(k, tid, nthr, D)) break;
             ry[k].get(f);
 #pragma unroll
-            for (int j = 0; j < kE; ++j) {
-                const float d = col_of<VEC>(k, j, tid, nthr) < D ? f[j] - mean : 0.f;
-                v[0] = fmaf(d, d, v[0]);
+            for (int j = 0; j < kP; ++j) {
+                const F2 d = LAYER ? in_row<VEC>(f[j] + splat(-mean), k, j, tid, nthr, D) : f[j];
+                v = fma(d, d, v);
             }
         }
-        team_sum<BLOCK, 1>(v, red, turn);
-        rstd = rsqrtf(v[0] * inv + p.eps);
+        rstd = rsqrtf(team_sum<BLOCK>(sum2(v), red, turn) * inv + p.eps);
     }
-    float r[NV][kE], v[1] = {0.f};
+    F2 r[NV][kP], v = splat(0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        float u[kE], w[kE], c[kE];
+        if (!has<VEC>(k, tid, nthr, D)) break;
+        F2 u[kP], w[kP], c[kP];
         ry[k].get(u);
         rr[k].get(r[k]);
         if (p.post) {
-            param8<VEC>(p.post_w, 1.f, k, tid, nthr, D, w);
+            if (p.post_w) {
+                param8<VEC>(p.post_w, 1.f, k, tid, nthr, D, w);
 #pragma unroll
-            for (int j = 0; j < kE; ++j) u[j] = (u[j] - mean) * rstd * w[j];
+                for (int j = 0; j < kP; ++j) u[j] = (LAYER ? u[j] + splat(-mean) : u[j]) * (w[j] * splat(rstd));
+            } else {
+#pragma unroll
+                for (int j = 0; j < kP; ++j) u[j] = (LAYER ? u[j] + splat(-mean) : u[j]) * splat(rstd);
+            }
             if (p.post_b) {
                 param8<VEC>(p.post_b, 0.f, k, tid, nthr, D, c);
 #pragma unroll
-                for (int j = 0; j < kE; ++j) u[j] += c[j];
+                for (int j = 0; j < kP; ++j) u[j] = u[j] + c[j];
             }
         }
         if (p.gate) {
             rg[k].get(c);
 #pragma unroll
-            for (int j = 0; j < kE; ++j) u[j] *= c[j] * sigmoid(c[j]);
+            for (int j = 0; j < kP; ++j) u[j] = u[j] * (c[j] * sigmoid(c[j]));
         }
         param8<VEC>(p.scale, 1.f, k, tid, nthr, D, w);
 #pragma unroll
-        for (int j = 0; j < kE; ++j) {
+        for (int j = 0; j < kP; ++j) {
             // columns behind D hold zero, for the sums below
-            r[k][j] = col_of<VEC>(k, j, tid, nthr) < D ? fmaf(p.alpha * w[j], u[j], r[k][j]) : 0.f;
-            v[0] += layer ? r[k][j] : r[k][j] * r[k][j];
+            r[k][j] = in_row<VEC>(fma(splat(p.alpha) * w[j], u[j], r[k][j]), k, j, tid, nthr, D);
+            v = LAYER ? v + r[k][j] : fma(r[k][j], r[k][j], v);
         }
         if (p.r_out) store8<VEC>((T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D, r[k]);
     }
     if (!p.xn) return;
-    team_sum<BLOCK, 1>(v, red, turn);
+    float q = team_sum<BLOCK>(sum2(v), red, turn);
     mean = 0.f;
-    if (layer) {
-        mean = v[0] * inv;
-        v[0] = 0.f;
+    if (LAYER) {
+        mean = q * inv;
+        v = splat(0.f);
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int k = 0; k < NV; ++k) {
+            if (!has<VEC>(k, tid, nthr, D)) break;
 #pragma unroll
-            for (int j = 0; j < kE; ++j) {
-                const float d = col_of<VEC>(k, j, tid, nthr) < D ? r[k][j] - mean : 0.f;
-                v[0] = fmaf(d, d, v[0]);
+            for (int j = 0; j < kP; ++j) {
+                const F2 d = in_row<VEC>(r[k][j] + splat(-mean), k, j, tid, nthr, D);
+                v = fma(d, d, v);
             }
-        team_sum<BLOCK, 1>(v, red, turn);
+        }
+        q = team_sum<BLOCK>(sum2(v), red, turn);
     }
-    rstd = rsqrtf(v[0] * inv + p.eps);
+    rstd = rsqrtf(q * inv + p.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        float w[kE], c[kE];
+        if (!has<VEC>(k, tid, nthr, D)) break;
+        F2 w[kP], c[kP];
         param8<VEC>(p.pre_w, 1.f, k, tid, nthr, D, w);
 #pragma unroll
-        for (int j = 0; j < kE; ++j) r[k][j] = (r[k][j] - mean) * rstd * w[j];
+        for (int j = 0; j < kP; ++j) r[k][j] = (LAYER ? r[k][j] + splat(-mean) : r[k][j]) * (w[j] * splat(rstd));
         if (p.pre_b) {
             param8<VEC>(p.pre_b, 0.f, k, tid, nthr, D, c);
 #pragma unroll
-            for (int j = 0; j < kE; ++j) r[k][j] += c[j];
+            for (int j = 0; j < kP; ++j) r[k][j] = r[k][j] + c[j];
         }
         store8<VEC>((T *)p.xn + row * p.xn_stride, k, tid, nthr, D, r[k]);
     }
@@ -280,23 +334,22 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128) norm_gate_fwd_kernel(hm_nor
 // apart, the next row's loads under way while one is worked on.
 // part[(team * 5 + i) * D + c]: the team's share of dscale, dpost_w, dpost_b,
 // dpre_w, dpre_b.
-template <typename T, bool VEC, int NV, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 512 : 256, NV == 1 && !BLOCK ? 2 : 1)
+template <typename T, bool VEC, int NV, bool BLOCK, bool LAYER>
+__global__ void __launch_bounds__(BLOCK ? 512 : 256, 1)
 norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
-    __shared__ float red[2][32][2];
+    __shared__ float2 red[2][32];
     int turn = 0;
     const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nthr = BLOCK ? blockDim.x : 32, D = (int)p.D;
     const float inv = 1.f / (float)D;
     const int64_t team = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int64_t teams = BLOCK ? (int64_t)gridDim.x : (int64_t)gridDim.x * 8;
-    const bool layer = p.norm == HM_NORM_LAYER;
-    float acc[5][NV][kE];
+    F2 acc[5][NV][kP];
 #pragma unroll
     for (int i = 0; i < 5; ++i)
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int j = 0; j < kE; ++j) acc[i][k][j] = 0.f;
+            for (int j = 0; j < kP; ++j) acc[i][k][j] = splat(0.f);
     Raw8<T> ry[NV], rg[NV], rr[NV], rd[NV], re[NV];
     auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -313,7 +366,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
     };
     if (team < p.rows) fetch(team);
     for (int64_t row = team; row < p.rows; row += teams) {
-        float y[NV][kE], r[NV][kE], d[NV][kE], e[NV][kE], g[NV][kE], w[kE], c[kE];
+        F2 y[NV][kP], r[NV][kP], d[NV][kP], e[NV][kP], g[NV][kP], w[kP], c[kP];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             ry[k].get(y[k]);
@@ -322,98 +375,103 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
             rd[k].get(d[k]);
         }
         if (row + teams < p.rows) fetch(row + teams);
-        // statistics of y and of r_out
-        float mean[2] = {0.f, 0.f}, v[2];
-        if (layer) {
-            v[0] = v[1] = 0.f;
+        // statistics of y and of r_out; both rows are left centred
+        F2 v0 = splat(0.f), v1 = splat(0.f);
+        float2 v;
+        if (LAYER) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < kE; ++j) {
-                    v[0] += y[k][j];
-                    if (p.dxn) v[1] += r[k][j];
+                for (int j = 0; j < kP; ++j) {
+                    v0 = v0 + y[k][j];
+                    if (p.dxn) v1 = v1 + r[k][j];
                 }
-            team_sum<BLOCK, 2>(v, red, turn);
-            mean[0] = p.post ? v[0] * inv : 0.f;
-            mean[1] = v[1] * inv;
+            v = team_sum2<BLOCK>(sum2(v0), sum2(v1), red, turn);
+            const F2 my = splat(p.post ? -v.x * inv : 0.f), mr = splat(-v.y * inv);
+            v0 = v1 = splat(0.f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if (!has<VEC>(k, tid, nthr, D)) break;
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    y[k][j] = in_row<VEC>(y[k][j] + my, k, j, tid, nthr, D);
+                    if (p.dxn) r[k][j] = in_row<VEC>(r[k][j] + mr, k, j, tid, nthr, D);
+                }
+            }
         }
-        v[0] = v[1] = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int j = 0; j < kE; ++j)
-                if (col_of<VEC>(k, j, tid, nthr) < D) {
-                    const float a = y[k][j] - mean[0];
-                    v[0] = fmaf(a, a, v[0]);
-                    if (p.dxn) {
-                        const float b = r[k][j] - mean[1];
-                        v[1] = fmaf(b, b, v[1]);
-                    }
-                }
-        team_sum<BLOCK, 2>(v, red, turn);
-        const float rsy = p.post ? rsqrtf(v[0] * inv + p.eps) : 1.f, rsr = rsqrtf(v[1] * inv + p.eps);
+            for (int j = 0; j < kP; ++j) {
+                v0 = fma(y[k][j], y[k][j], v0);
+                if (p.dxn) v1 = fma(r[k][j], r[k][j], v1);
+            }
+        v = team_sum2<BLOCK>(sum2(v0), sum2(v1), red, turn);
+        const float rsy = p.post ? rsqrtf(v.x * inv + p.eps) : 1.f, rsr = rsqrtf(v.y * inv + p.eps);
         if (p.dxn) {
             // dr = dr_out + rstd (w e - mean(w e) - u mean(w e u)), u = (r - mean) rstd
-            v[0] = v[1] = 0.f;
+            v0 = v1 = splat(0.f);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 param8<VEC>(p.pre_w, 1.f, k, tid, nthr, D, w);
 #pragma unroll
-                for (int j = 0; j < kE; ++j) {
-                    const float u = (r[k][j] - mean[1]) * rsr;
-                    acc[3][k][j] = fmaf(e[k][j], u, acc[3][k][j]);
-                    acc[4][k][j] += e[k][j];
+                for (int j = 0; j < kP; ++j) {
+                    const F2 u = r[k][j] * splat(rsr);
+                    acc[3][k][j] = fma(e[k][j], u, acc[3][k][j]);
+                    acc[4][k][j] = acc[4][k][j] + e[k][j];
                     r[k][j] = u;
-                    e[k][j] *= w[j];      // zero behind D
-                    v[0] += e[k][j];
-                    v[1] = fmaf(e[k][j], u, v[1]);
+                    e[k][j] = e[k][j] * w[j];
+                    v0 = v0 + e[k][j];
+                    v1 = fma(e[k][j], u, v1);
                 }
             }
-            team_sum<BLOCK, 2>(v, red, turn);
-            const float m0 = layer ? v[0] * inv : 0.f, m1 = v[1] * inv;
+            v = team_sum2<BLOCK>(sum2(v0), sum2(v1), red, turn);
+            const F2 m0 = splat(LAYER ? -v.x * inv : 0.f), m1 = splat(-v.y * inv);
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < kE; ++j) d[k][j] = fmaf(rsr, e[k][j] - fmaf(r[k][j], m1, m0), d[k][j]);
+                for (int j = 0; j < kP; ++j)
+                    d[k][j] = fma(splat(rsr), e[k][j] + fma(r[k][j], m1, m0), d[k][j]);
         }
-        v[0] = v[1] = 0.f;
+        v0 = v1 = splat(0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            if (!has<VEC>(k, tid, nthr, D)) break;
             if (p.dr) store8<VEC>((T *)p.dr + row * p.dr_stride, k, tid, nthr, D, d[k]);
-            float pw[kE], pb[kE];
+            F2 pw[kP], pb[kP];
             param8<VEC>(p.scale, 1.f, k, tid, nthr, D, c);
             param8<VEC>(p.post_w, 1.f, k, tid, nthr, D, pw);
             param8<VEC>(p.post_b, 0.f, k, tid, nthr, D, pb);
 #pragma unroll
-            for (int j = 0; j < kE; ++j) {
-                const bool in = col_of<VEC>(k, j, tid, nthr) < D;
-                const float u = (y[k][j] - mean[0]) * rsy;
-                const float n = p.post ? fmaf(u, pw[j], pb[j]) : u;
-                const float dm = in ? d[k][j] * (p.alpha * c[j]) : 0.f;
-                float m = n, dn = dm;
+            for (int j = 0; j < kP; ++j) {
+                const F2 da = in_row<VEC>(d[k][j], k, j, tid, nthr, D) * splat(p.alpha), dm = da * c[j];
+                const F2 u = p.post ? y[k][j] * splat(rsy) : y[k][j];
+                const F2 n = p.post ? fma(u, pw[j], pb[j]) : u;
+                F2 m = n, dn = dm;
                 if (p.gate) {
-                    const float sg = sigmoid(g[k][j]), si = g[k][j] * sg;
+                    const F2 sg = sigmoid(g[k][j]), si = g[k][j] * sg;
                     m = n * si;
                     dn = dm * si;
-                    g[k][j] = dm * n * fmaf(si, 1.f - sg, sg);
+                    // SiLU'(g) = sg + si (1 - sg)
+                    g[k][j] = dm * n * fma(si, splat(1.f) - sg, sg);
                 }
-                if (in) acc[0][k][j] = fmaf(d[k][j], p.alpha * m, acc[0][k][j]);
-                acc[1][k][j] = fmaf(dn, u, acc[1][k][j]);
-                acc[2][k][j] += dn;
+                acc[0][k][j] = fma(da, m, acc[0][k][j]);
+                acc[1][k][j] = fma(dn, u, acc[1][k][j]);
+                acc[2][k][j] = acc[2][k][j] + dn;
                 y[k][j] = u;
                 d[k][j] = p.post ? dn * pw[j] : dn;
-                v[0] += d[k][j];
-                v[1] = fmaf(d[k][j], u, v[1]);
+                v0 = v0 + d[k][j];
+                v1 = fma(d[k][j], u, v1);
             }
             if (p.gate) store8<VEC>((T *)p.dgate + row * p.dgate_stride, k, tid, nthr, D, g[k]);
         }
         if (p.post) {
-            team_sum<BLOCK, 2>(v, red, turn);
-            const float m0 = layer ? v[0] * inv : 0.f, m1 = v[1] * inv;
+            v = team_sum2<BLOCK>(sum2(v0), sum2(v1), red, turn);
+            const F2 m0 = splat(LAYER ? -v.x * inv : 0.f), m1 = splat(-v.y * inv);
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int j = 0; j < kE; ++j) d[k][j] = rsy * (d[k][j] - fmaf(y[k][j], m1, m0));
+                for (int j = 0; j < kP; ++j) d[k][j] = splat(rsy) * (d[k][j] + fma(y[k][j], m1, m0));
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) store8<VEC>((T *)p.dy + row * p.dy_stride, k, tid, nthr, D, d[k]);
@@ -425,7 +483,8 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
                 const int c = col_of<VEC>(k, j, tid, nthr);
-                if (c < D) part[(team * 5 + i) * D + c] = acc[i][k][j];
+                const float2 u = un(acc[i][k][j / 2]);
+                if (c < D) part[(team * 5 + i) * D + c] = j & 1 ? u.y : u.x;
             }
 }
 
@@ -501,8 +560,9 @@ struct Team {
 // Forward: a warp per row up to 8 pieces a lane (4 of fp32, as many
 // registers); more warps for wider rows, and for so few rows that one warp
 // each would leave most of the GPU idle.
-Team fwd_team(int64_t rows, int64_t D, size_t es) {
-    const int pieces = (int)((D + 32 * kE - 1) / (32 * kE)), most = es == 2 ? 8 : 4;
+// Rows that are read element by element get a block with as few pieces as it can.
+Team fwd_team(int64_t rows, int64_t D, size_t es, bool vec) {
+    const int pieces = (int)((D + 32 * kE - 1) / (32 * kE)), most = !vec ? (D > 8192 ? 4 : D > 4096 ? 2 : 1) : es == 2 ? 8 : 4;
     int warps = 1;
     while ((pieces + warps - 1) / warps > most) warps *= 2;
     while (warps < 16 && (pieces + warps - 1) / warps > 1 && rows * warps * 2 <= 148 * 16) warps *= 2;
@@ -560,25 +620,31 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
     if (a->rows == 0) return HM_OK;
     if (!a->r_out && !a->xn) return fail_args(HM_ERR_INVALID_ARG, "%s: r_out and xn are both NULL", w);
     if (a->r_out == a->xn) return fail_args(HM_ERR_INVALID_ARG, "%s: r_out and xn are the same array", w);
-    const Team t = fwd_team(a->rows, a->D, es);
-    const bool block = t.nthr > 32;
+    const Team t = fwd_team(a->rows, a->D, es, vec);
+    const bool block = t.nthr > 32 || !vec;
     const int64_t blocks = block ? a->rows : (a->rows + 3) / 4;
     if (blocks > 0x7fffffffLL) return fail_args(HM_ERR_UNSUPPORTED, "%s: too many rows", w);
     cudaStream_t s = (cudaStream_t)stream;
-#define HM_FWD(T, V, N)                                                                            \
-    (block ? norm_gate_fwd_kernel<T, V, N, true><<<(unsigned)blocks, t.nthr, 0, s>>>(*a)           \
-           : norm_gate_fwd_kernel<T, V, N, false><<<(unsigned)blocks, 128, 0, s>>>(*a))
+#define HM_FWD(T, V, N, B, Y) norm_gate_fwd_kernel<T, V, N, B, Y><<<(unsigned)blocks, B ? t.nthr : 128, 0, s>>>(*a)
+#define HM_FWD_Y(T, V, N, B) (a->norm == HM_NORM_LAYER ? HM_FWD(T, V, N, B, true) : HM_FWD(T, V, N, B, false))
+#define HM_FWD_B(T, N) (block ? HM_FWD_Y(T, true, N, true) : HM_FWD_Y(T, true, N, false))
+#define HM_FWD_S(T) (t.nv == 1 ? HM_FWD_Y(T, false, 1, true) : t.nv == 2 ? HM_FWD_Y(T, false, 2, true) : HM_FWD_Y(T, false, 4, true))
     if (a->io_dtype == HM_BF16) {
-        if (t.nv == 1) vec ? HM_FWD(__nv_bfloat16, true, 1) : HM_FWD(__nv_bfloat16, false, 1);
-        else if (t.nv == 2) vec ? HM_FWD(__nv_bfloat16, true, 2) : HM_FWD(__nv_bfloat16, false, 2);
-        else if (t.nv == 4) vec ? HM_FWD(__nv_bfloat16, true, 4) : HM_FWD(__nv_bfloat16, false, 4);
-        else vec ? HM_FWD(__nv_bfloat16, true, 8) : HM_FWD(__nv_bfloat16, false, 8);
+        if (!vec) HM_FWD_S(__nv_bfloat16);
+        else if (t.nv == 1) HM_FWD_B(__nv_bfloat16, 1);
+        else if (t.nv == 2) HM_FWD_B(__nv_bfloat16, 2);
+        else if (t.nv == 4) HM_FWD_B(__nv_bfloat16, 4);
+        else HM_FWD_B(__nv_bfloat16, 8);
     } else {
-        if (t.nv == 1) vec ? HM_FWD(float, true, 1) : HM_FWD(float, false, 1);
-        else if (t.nv == 2) vec ? HM_FWD(float, true, 2) : HM_FWD(float, false, 2);
-        else vec ? HM_FWD(float, true, 4) : HM_FWD(float, false, 4);
+        if (!vec) HM_FWD_S(float);
+        else if (t.nv == 1) HM_FWD_B(float, 1);
+        else if (t.nv == 2) HM_FWD_B(float, 2);
+        else HM_FWD_B(float, 4);
     }
 #undef HM_FWD
+#undef HM_FWD_Y
+#undef HM_FWD_B
+#undef HM_FWD_S
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? HM_OK : fail_args(HM_ERR_CUDA, "%s launch: %s", w, cudaGetErrorString(e));
@@ -622,21 +688,15 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     cudaStream_t s = (cudaStream_t)stream;
     float *part = (float *)a->workspace;
     if (t.blocks > 0) {
-#define HM_BWD(T, V, N) norm_gate_bwd_kernel<T, V, N, true><<<t.blocks, t.nthr, 0, s>>>(*a, part)
-#define HM_BWD_N(T, V)                                                                             \
-    do {                                                                                           \
-        if (!block) norm_gate_bwd_kernel<T, V, 1, false><<<t.blocks, 256, 0, s>>>(*a, part);       \
-        else if (t.nv == 1) HM_BWD(T, V, 1);                                                       \
-        else if (t.nv == 2) HM_BWD(T, V, 2);                                                       \
-        else HM_BWD(T, V, 4);                                                                      \
-    } while (0)
-        if (a->io_dtype == HM_BF16) {
-            if (vec) HM_BWD_N(__nv_bfloat16, true);
-            else HM_BWD_N(__nv_bfloat16, false);
-        } else {
-            if (vec) HM_BWD_N(float, true);
-            else HM_BWD_N(float, false);
-        }
+#define HM_BWD(T, V, N, B)                                                                             \
+    (a->norm == HM_NORM_LAYER                                                                          \
+         ? norm_gate_bwd_kernel<T, V, N, B, true><<<t.blocks, B ? t.nthr : 256, 0, s>>>(*a, part)      \
+         : norm_gate_bwd_kernel<T, V, N, B, false><<<t.blocks, B ? t.nthr : 256, 0, s>>>(*a, part))
+#define HM_BWD_N(T, V)                                                                                 \
+    (!block ? HM_BWD(T, V, 1, false)                                                                   \
+            : t.nv == 1 ? HM_BWD(T, V, 1, true) : t.nv == 2 ? HM_BWD(T, V, 2, true) : HM_BWD(T, V, 4, true))
+        if (a->io_dtype == HM_BF16) vec ? HM_BWD_N(__nv_bfloat16, true) : HM_BWD_N(__nv_bfloat16, false);
+        else vec ? HM_BWD_N(float, true) : HM_BWD_N(float, false);
 #undef HM_BWD
 #undef HM_BWD_N
         count_launches(1);

@@ -2,10 +2,12 @@
 //
 // Bandwidth-bound: every element read and written once.  A thread takes P
 // pairs (P = 8 of bf16, 4 of fp32: two 16-byte loads; fewer where strides or
-// the pair count ask for it) of one token and turns them in a run of heads, q's
-// and then k's: the angle depends on the token and the pair alone, so its sine
-// and cosine are formed once per run.  The loads of four heads are in flight
-// together.
+// the pair count ask for it) of one token and turns them in up to four heads,
+// q's and then k's, whose loads are in flight together: the angle depends on
+// the token and the pair alone, so its sine and cosine are formed once for the
+// four.  Its two pieces of a head lie half of rot apart in both layouts: the
+// pairs' halves (half layout), or two times P / 2 whole pairs (interleaved), so
+// that a warp's accesses are contiguous either way.
 //
 // Angles are kept as fractions of a turn in 64-bit fixed point: theta / (2 pi)
 // mod 1 times 2^64 is an integer (formed in fp64, once per block, in shared
@@ -13,7 +15,7 @@
 // reduction modulo whole turns, exactly.
 #include <math.h>
 
-#include "hm_internal.h"
+#include "packed.cuh"
 
 namespace hm {
 
@@ -28,7 +30,6 @@ struct Side {             // q or k
 struct RotArgs {
     Side s[2];
     int Hq, H;            // q's heads, all heads
-    int hg;               // heads of a run
     int64_t L;
     unsigned tokens;      // B * L
     int d, rot;
@@ -46,7 +47,7 @@ struct RotArgs {
 };
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;   // heads whose loads are in flight together
+constexpr int kHeads = 4;   // heads of a run
 
 // theta_i / (2 pi) mod 1, in units of 2^-64 of a turn
 __device__ __forceinline__ unsigned long long pair_turns(const RotArgs &a, int i) {
@@ -61,24 +62,75 @@ __device__ __forceinline__ unsigned long long pair_turns(const RotArgs &a, int i
     return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
 }
 
+// Cosine (times mscale) and sine (times mscale and the direction) of pos times
+// the pair's frequency.  The nearest quarter turn goes into signs and an
+// exchange, the rest, x in [-pi/4, pi/4], into polynomials of least maximal
+// error fitted there: sin x = x + x^3 S(x^2) (4e-9 of it) and
+// cos x = 1 - x^2 / 2 + x^4 C(x^2) (1e-10).
 __device__ __forceinline__ void turn_of(const RotArgs &a, unsigned long long unit, int64_t pos, float &cs, float &sn) {
-    const unsigned long long ph = unit * (unsigned long long)pos;
-    // the top 32 bits as a signed fraction of a turn in [-1/2, 1/2)
-    const float half_turns = (float)(int)(ph >> 32) * 4.656612873077392578125e-10f;   // 2^-31
-    sincospif(half_turns, &sn, &cs);
-    cs *= a.mscale;
-    sn *= a.mscale * a.sign;
+    const unsigned ph = (unsigned)((unit * (unsigned long long)pos) >> 32);
+    const unsigned quarter = (ph + 0x20000000u) >> 30;
+    const float x = (float)(int)(ph - (quarter << 30)) * 1.46291807926715968e-09f;   // 2 pi / 2^32
+    const float q = x * x;
+    float s = fmaf(-1.951528392964974e-04f, q, 8.33216030150652e-03f);
+    s = fmaf(s, q, -1.6666655242443085e-01f);
+    s = fmaf(s * q, x, x);
+    float c = fmaf(2.4438451873720624e-05f, q, -1.388736767694354e-03f);
+    c = fmaf(c, q, 4.166664555668831e-02f);
+    c = fmaf(c, q, -0.5f);
+    c = fmaf(c, q, 1.f);
+    const float p = quarter & 1 ? c : s, r = quarter & 1 ? s : c;
+    sn = (quarter & 2 ? -p : p) * (a.mscale * a.sign);
+    cs = ((quarter + 1) & 2 ? -r : r) * a.mscale;
 }
 
-// P elements, P * sizeof(T) = 2 .. 16 bytes
+// P elements, P * sizeof(T) = 2 .. 16 bytes, as words (or one half word)
 template <typename T, int P>
-struct alignas(sizeof(T) * P) Vec {
-    T v[P];
+struct Vec {
+    static constexpr int N = P * (int)sizeof(T) / 4;
+    uint32_t w[N];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (N == 4) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        } else if constexpr (N == 2) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[0] = u.x, w[1] = u.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (N == 4) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (N == 2) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(p) = w[0];
+    }
+    // elements 2 j and 2 j + 1 (P > 1)
+    __device__ __forceinline__ F2 pair(int j) const {
+        if constexpr (sizeof(T) == 2) return pk_bf16(w[j]);
+        else return pk(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+    }
+    __device__ __forceinline__ void set(int j, F2 v) {
+        if constexpr (sizeof(T) == 2) {
+            w[j] = bf16_of(v);
+        } else {
+            w[2 * j] = __float_as_uint(un(v).x);
+            w[2 * j + 1] = __float_as_uint(un(v).y);
+        }
+    }
+    __device__ __forceinline__ float one() const { return __uint_as_float(w[0]); }
+    __device__ __forceinline__ void one(float v) { w[0] = __float_as_uint(v); }
 };
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void from_f(float &o, float v) { o = v; }
-__device__ __forceinline__ void from_f(__nv_bfloat16 &o, float v) { o = __float2bfloat16_rn(v); }
+template <>
+struct Vec<__nv_bfloat16, 1> {
+    __nv_bfloat16 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = *p; }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *p = v; }
+    __device__ __forceinline__ F2 pair(int) const { return splat(0.f); }
+    __device__ __forceinline__ void set(int, F2) {}
+    __device__ __forceinline__ float one() const { return __bfloat162float(v); }
+    __device__ __forceinline__ void one(float f) { v = __float2bfloat16_rn(f); }
+};
 
 // the head's rows in and out
 template <typename T>
@@ -90,74 +142,76 @@ __device__ __forceinline__ void head_of(const RotArgs &a, int h, int64_t b, int6
 }
 
 template <typename T, int P, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const __grid_constant__ RotArgs a) {
     __shared__ unsigned long long unit[512];
     const int half = a.rot / 2;
     for (int i = threadIdx.x; i < half; i += kThreads) unit[i] = pair_turns(a, i);
     __syncthreads();
     using V = Vec<T, P>;
     const int groups = a.ng + a.nt;
-    for (int i = threadIdx.x; i < a.tb * a.per; i += kThreads) {
-        const int local = i / a.per, rest = i - local * a.per, run = rest / groups, grp = rest - run * groups;
-        const unsigned tok = blockIdx.x * (unsigned)a.tb + local;
-        if (tok >= a.tokens) break;
-        const int64_t b = tok / (unsigned)a.L, t = tok - (unsigned)b * (unsigned)a.L;
-        const int h0 = run * a.hg, h1 = min(h0 + a.hg, a.H);
-        if (grp >= a.ng) {             // elements behind rot
-            const int c0 = a.rot + (grp - a.ng) * 2 * P;
-            for (int h = h0; h < h1; ++h) {
-                const T *in;
-                T *out;
-                head_of(a, h, b, t, in, out);
-                if (c0 + P <= a.d) *reinterpret_cast<V *>(out + c0) = *reinterpret_cast<const V *>(in + c0);
-                if (c0 + 2 * P <= a.d)
-                    *reinterpret_cast<V *>(out + c0 + P) = *reinterpret_cast<const V *>(in + c0 + P);
-            }
-            continue;
-        }
-        const int64_t pos = a.positions ? a.positions[b * a.pos_b + t * a.pos_t] : a.pos0 + t;
-        float cs[P], sn[P];
+    for (unsigned tok0 = blockIdx.x * (unsigned)a.tb; tok0 < a.tokens; tok0 += gridDim.x * (unsigned)a.tb)
+        for (int i = threadIdx.x; i < a.tb * a.per; i += kThreads) {
+            const int local = i / a.per, rest = i - local * a.per, run = rest / groups, grp = rest - run * groups;
+            const unsigned tok = tok0 + local;
+            if (tok >= a.tokens) break;
+            const int64_t b = tok / (unsigned)a.L, t = tok - (unsigned)b * (unsigned)a.L;
+            const int h0 = run * kHeads;
+            // columns of the two pieces: of a rotated group, or of one behind rot
+            const bool tail = grp >= a.ng;
+            const int iu = tail ? a.rot + (grp - a.ng) * 2 * P : INTER && P == 1 ? 2 * grp : grp * P;
+            const int iv = tail ? iu + P : INTER && P == 1 ? iu + 1 : iu + half;
+            const bool two = iv + P <= a.d;
+            V u[kHeads], v[kHeads];
+            T *out[kHeads];
 #pragma unroll
-        for (int j = 0; j < P; ++j) turn_of(a, unit[grp * P + j], pos, cs[j], sn[j]);
-        const int iu = INTER ? grp * 2 * P : grp * P, iv = INTER ? iu + P : iu + half;
-        for (int hb = h0; hb < h1; hb += kBatch) {
-            V u[kBatch], v[kBatch];
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (hb + k < h1) {
+            for (int k = 0; k < kHeads; ++k)
+                if (h0 + k < a.H) {
                     const T *in;
-                    T *out;
-                    head_of(a, hb + k, b, t, in, out);
-                    u[k] = *reinterpret_cast<const V *>(in + iu);
-                    v[k] = *reinterpret_cast<const V *>(in + iv);
+                    head_of(a, h0 + k, b, t, in, out[k]);
+                    u[k].load(in + iu);
+                    if (two) v[k].load(in + iv);
+                }
+            if (!tail) {
+                const int64_t pos = a.positions ? a.positions[b * a.pos_b + t * a.pos_t] : a.pos0 + t;
+                float cs[P], sn[P];
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const int pair = !INTER || P == 1 ? grp * P + j
+                                     : j < P / 2 ? grp * (P / 2) + j : (half + grp * P) / 2 + j - P / 2;
+                    turn_of(a, unit[pair], pos, cs[j], sn[j]);
                 }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-                if (hb + k < h1) {
-                    const T *in;
-                    T *out;
-                    head_of(a, hb + k, b, t, in, out);
-                    V x, y;
+                for (int k = 0; k < kHeads; ++k) {
+                    if (P == 1) {
+                        const float x = u[k].one(), y = v[k].one();
+                        u[k].one(x * cs[0] - y * sn[0]);
+                        v[k].one(x * sn[0] + y * cs[0]);
+                    } else if (INTER) {
 #pragma unroll
-                    for (int j = 0; j < P; ++j) {
-                        // interleaved: element 2 j of the 2 P is u_j, 2 j + 1 is v_j
-                        const float p = to_f(INTER ? (2 * j < P ? u[k].v[2 * j % P] : v[k].v[2 * j % P]) : u[k].v[j]);
-                        const float q = to_f(INTER ? (2 * j + 1 < P ? u[k].v[(2 * j + 1) % P] : v[k].v[(2 * j + 1) % P])
-                                                   : v[k].v[j]);
-                        const float r = p * cs[j] - q * sn[j], w = p * sn[j] + q * cs[j];
-                        if (INTER) {
-                            from_f(2 * j < P ? x.v[2 * j % P] : y.v[2 * j % P], r);
-                            from_f(2 * j + 1 < P ? x.v[(2 * j + 1) % P] : y.v[(2 * j + 1) % P], w);
-                        } else {
-                            from_f(x.v[j], r);
-                            from_f(y.v[j], w);
+                        for (int j = 0; j < P; ++j) {      // pair j is elements 2 j, 2 j + 1 of its piece
+                            V &w = j < P / 2 ? u[k] : v[k];
+                            const float2 x = un(w.pair(j % (P / 2 > 0 ? P / 2 : 1)));
+                            w.set(j % (P / 2 > 0 ? P / 2 : 1),
+                                  pk(x.x * cs[j] - x.y * sn[j], x.x * sn[j] + x.y * cs[j]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < P / 2; ++j) {  // two pairs at once
+                            const F2 x = u[k].pair(j), y = v[k].pair(j);
+                            const F2 c = pk(cs[2 * j], cs[2 * j + 1]), s = pk(sn[2 * j], sn[2 * j + 1]);
+                            u[k].set(j, fma(x, c, y * pk(-sn[2 * j], -sn[2 * j + 1])));
+                            v[k].set(j, fma(x, s, y * c));
                         }
                     }
-                    *reinterpret_cast<V *>(out + iu) = x;
-                    *reinterpret_cast<V *>(out + iv) = y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kHeads; ++k)
+                if (h0 + k < a.H) {
+                    u[k].store(out[k] + iu);
+                    if (two) v[k].store(out[k] + iv);
                 }
         }
-    }
 }
 
 size_t esize(hm_dtype t) { return t == HM_BF16 ? 2 : 4; }
@@ -271,14 +325,13 @@ extern "C" hm_status hm_rotary(const hm_rotary_args *a, hm_stream_t stream) {
     while (P > 1 && !fits(P)) P /= 2;
     r.ng = a->rot / 2 / P;
     r.nt = copy ? (a->d - a->rot + 2 * P - 1) / (2 * P) : 0;
-    // runs of all heads once that fills the GPU, shorter ones before
-    r.hg = r.H;
-    while (r.hg > kBatch && (int64_t)r.tokens * r.ng * ((r.H + r.hg - 1) / r.hg) < 148 * 1024) r.hg = (r.hg + 1) / 2;
-    const int64_t per = (int64_t)((r.H + r.hg - 1) / r.hg) * (r.ng + r.nt);
+    const int64_t per = (int64_t)((r.H + kHeads - 1) / kHeads) * (r.ng + r.nt);
     if (per > (1 << 24)) return fail_args(HM_ERR_UNSUPPORTED, "rotary: too many heads");
     r.per = (int)per;
     r.tb = r.per >= kThreads ? 1 : kThreads / r.per;
-    const unsigned grid = (r.tokens + r.tb - 1) / r.tb;
+    // blocks walk the tokens, so that the frequencies are formed once per block
+    const unsigned blocks = (r.tokens + r.tb - 1) / r.tb;
+    const unsigned grid = blocks < 148 * 6 ? blocks : 148 * 6;
     cudaStream_t s = (cudaStream_t)stream;
     const bool inter = a->layout == HM_ROTARY_INTERLEAVED;
 #define HM_ROT(T, N)                                                     \
