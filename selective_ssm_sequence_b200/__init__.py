@@ -228,17 +228,32 @@ def _ptr(t) -> Optional[int]:
 
 
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return HM_F32
-    if t.dtype == torch.bfloat16:
+    torch = _need_torch()
+    if t.dtype is torch.bfloat16:
         return HM_BF16
+    if t.dtype is torch.float32:
+        return HM_F32
     raise TypeError("unsupported dtype %s (float32 or bfloat16)" % t.dtype)
+
+
+_torch = None
+
+
+def _need_torch():
+    """The torch module, imported at the first call that handles tensors."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
+        torch = _need_torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the address without a Stream object
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -452,6 +467,17 @@ def hm_block_fwd(args: BlockArgs, workspace, stream=None) -> None:
 
 # ---- the operators around the mixer: gated recurrence, seam between blocks, rotary positions.
 # Their helpers check what the C side cannot see (shapes, dtypes, devices) and raise ValueError.
+# A decode loop calls them for every token, so each tensor is looked at once (_is); only when one
+# does not pass is it found out, by the slower checks below, what to say about which.
+
+def _is(t, shape, dtype, dev: int) -> bool:
+    return t.shape == shape and t.dtype is dtype and t.get_device() == dev
+
+
+def _current_device() -> int:
+    torch = _need_torch()
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+
 
 def _io(who: str, shape, like, **ts):
     """Each given tensor has `like`'s dtype, this shape and contiguous elements in its last axis."""
@@ -478,7 +504,7 @@ def _dense(who: str, shape, dtype, **ts):
 
 def _one_device(who: str, *ts) -> None:
     """All tensors on the current CUDA device: the kernels run there, on its stream."""
-    import torch
+    torch = _need_torch()
     dev = -1
     for t in ts:
         if t is None:
@@ -495,16 +521,24 @@ def gated_scan_args(x, dt, y, A_log, dt_bias=None, h0=None, h_out=None, lengths=
                     states=None) -> GatedScanArgs:
     """Fill an hm_gated_scan_args (x, dt, y: [B, L, D], channels contiguous; h0,
     h_out: [B, D] fp32; lengths: [B] int32; A_log, dt_bias: [D] fp32)."""
-    import torch
-    who = "gated_scan_args"
-    B, L, D = x.shape
-    _io(who, x.shape, x, x=x, dt=dt, y=y)
-    _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias)
-    _dense(who, (B, D), torch.float32, h0=h0, h_out=h_out)
-    _dense(who, (B,), torch.int32, lengths=lengths)
-    _one_device(who, x, dt, y, A_log, dt_bias, h0, h_out, lengths, states)
-    ys = y.stride() if y is not None else (0, 0, 1)
+    sh, ty, dev = x.shape, x.dtype, _current_device()
+    B, L, D = sh
+    f32 = _need_torch().float32
     xs, ds = x.stride(), dt.stride()
+    ys = y.stride() if y is not None else (0, 0, 1)
+    if not (x.get_device() == dev and _is(dt, sh, ty, dev) and xs[2] == ds[2] == ys[2] == 1
+            and (y is None or _is(y, sh, ty, dev))
+            and _is(A_log, (D,), f32, dev) and A_log.is_contiguous()
+            and (dt_bias is None or _is(dt_bias, (D,), f32, dev) and dt_bias.is_contiguous())
+            and (h0 is None or _is(h0, (B, D), f32, dev) and h0.is_contiguous())
+            and (h_out is None or _is(h_out, (B, D), f32, dev) and h_out.is_contiguous())
+            and lengths is None and states is None):
+        who = "gated_scan_args"
+        _io(who, sh, x, x=x, dt=dt, y=y)
+        _dense(who, (D,), f32, A_log=A_log, dt_bias=dt_bias)
+        _dense(who, (B, D), f32, h0=h0, h_out=h_out)
+        _dense(who, (B,), _torch.int32, lengths=lengths)
+        _one_device(who, x, dt, y, A_log, dt_bias, h0, h_out, lengths, states)
     a = GatedScanArgs(B, L, D, _dtype_code(x), int(input_scale), _ptr(x), _ptr(dt), _ptr(y), xs[0], xs[1], ds[0],
                       ds[1], ys[0], ys[1], _ptr(A_log), _ptr(dt_bias), _ptr(h0), _ptr(lengths), _ptr(h_out),
                       _ptr(states), states.numel() * states.element_size() if states is not None else 0)
@@ -524,8 +558,8 @@ def gated_scan_bwd_args(x, dt, dy, dx, ddt, A_log, dA_log, states, dt_bias=None,
                         dh0=None, lengths=None, input_scale: int = 0, workspace=None) -> GatedScanBwdArgs:
     """Fill an hm_gated_scan_bwd_args (the forward's inputs and its `states`;
     dy, dx, ddt: [B, L, D]; dh_out, dh0: [B, D] fp32; dA_log, d_dt_bias: [D] fp32)."""
-    import torch
     who = "gated_scan_bwd_args"
+    torch = _need_torch()
     B, L, D = x.shape
     _io(who, x.shape, x, x=x, dt=dt, dy=dy, dx=dx, ddt=ddt)
     _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias, dA_log=dA_log, d_dt_bias=d_dt_bias)
@@ -552,15 +586,21 @@ def hm_gated_scan_bwd(args: GatedScanBwdArgs, stream=None) -> None:
 
 def gated_step_args(x, dt, y, h, h_out, A_log, dt_bias=None, input_scale: int = 0) -> GatedStepArgs:
     """Fill an hm_gated_step_args (x, dt, y: [B, D]; h, h_out: [B, D] fp32, may be one tensor)."""
-    import torch
-    who = "gated_step_args"
-    B, D = x.shape
-    _io(who, x.shape, x, x=x, dt=dt, y=y)
-    _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias)
-    _dense(who, (B, D), torch.float32, h=h, h_out=h_out)
-    _one_device(who, x, dt, y, h, h_out, A_log, dt_bias)
-    a = GatedStepArgs(B, D, _dtype_code(x), int(input_scale), _ptr(x), _ptr(dt), _ptr(y), x.stride(0), dt.stride(0),
-                      y.stride(0), _ptr(A_log), _ptr(dt_bias), _ptr(h), _ptr(h_out))
+    sh, ty, dev = x.shape, x.dtype, _current_device()
+    B, D = sh
+    f32 = _need_torch().float32
+    xs, ds, ys = x.stride(), dt.stride(), y.stride()
+    if not (x.get_device() == dev and _is(dt, sh, ty, dev) and _is(y, sh, ty, dev) and xs[1] == ds[1] == ys[1] == 1
+            and _is(h, sh, f32, dev) and h.is_contiguous() and _is(h_out, sh, f32, dev) and h_out.is_contiguous()
+            and _is(A_log, (D,), f32, dev) and A_log.is_contiguous()
+            and (dt_bias is None or _is(dt_bias, (D,), f32, dev) and dt_bias.is_contiguous())):
+        who = "gated_step_args"
+        _io(who, sh, x, x=x, dt=dt, y=y)
+        _dense(who, (D,), f32, A_log=A_log, dt_bias=dt_bias)
+        _dense(who, (B, D), f32, h=h, h_out=h_out)
+        _one_device(who, x, dt, y, h, h_out, A_log, dt_bias)
+    a = GatedStepArgs(B, D, _dtype_code(x), int(input_scale), x.data_ptr(), dt.data_ptr(), y.data_ptr(), xs[0], ds[0],
+                      ys[0], A_log.data_ptr(), _ptr(dt_bias), h.data_ptr(), h_out.data_ptr())
     a._refs = (x, dt, y, h, h_out, A_log, dt_bias)
     return a
 
@@ -573,6 +613,8 @@ def _row_stride(t) -> int:
     """Elements between the rows of [..., D], whose leading axes must be dense over one another."""
     if t is None:
         return 0
+    if t.dim() == 2:
+        return t.stride()[0]
     step = want = 0
     for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
@@ -588,15 +630,27 @@ def _row_stride(t) -> int:
 def norm_gate_args(y, r, r_out, xn, gate=None, norm: int = 0, post: bool = True, eps: float = 1e-5,
                    alpha: float = 1.0, scale=None, post_w=None, post_b=None, pre_w=None, pre_b=None) -> NormGateArgs:
     """Fill an hm_norm_gate_args (y, gate, r, r_out, xn: [..., D]; parameters: [D] fp32)."""
-    import torch
-    who = "norm_gate_args"
-    D = y.shape[-1]
-    _io(who, y.shape, y, y=y, gate=gate, r=r, r_out=r_out, xn=xn)
-    _dense(who, (D,), torch.float32, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, pre_b=pre_b)
-    _one_device(who, y, gate, r, r_out, xn, scale, post_w, post_b, pre_w, pre_b)
+    sh, ty, dev = y.shape, y.dtype, _current_device()
+    D = sh[-1]
+    f32, vec = _need_torch().float32, (D,)
+    st, flat = [], len(sh) == 2
+    ok = y.get_device() == dev
+    for t in (y, gate, r, r_out, xn):
+        if t is None:
+            st.append(0)
+            continue
+        ts = t.stride()
+        st.append(ts[0] if flat else _row_stride(t))
+        ok = ok and ts[-1] == 1 and (t is y or _is(t, sh, ty, dev))
+    for t in (scale, post_w, post_b, pre_w, pre_b):
+        ok = ok and (t is None or _is(t, vec, f32, dev) and t.is_contiguous())
+    if not ok:
+        who = "norm_gate_args"
+        _io(who, sh, y, y=y, gate=gate, r=r, r_out=r_out, xn=xn)
+        _dense(who, vec, f32, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, pre_b=pre_b)
+        _one_device(who, y, gate, r, r_out, xn, scale, post_w, post_b, pre_w, pre_b)
     a = NormGateArgs(y.numel() // D if D else 0, D, _dtype_code(y), int(norm), int(post), eps, alpha, _ptr(y),
-                     _ptr(gate), _ptr(r), _ptr(r_out), _ptr(xn), _row_stride(y), _row_stride(gate), _row_stride(r),
-                     _row_stride(r_out), _row_stride(xn), _ptr(scale), _ptr(post_w), _ptr(post_b), _ptr(pre_w),
+                     _ptr(gate), _ptr(r), _ptr(r_out), _ptr(xn), *st, _ptr(scale), _ptr(post_w), _ptr(post_b), _ptr(pre_w),
                      _ptr(pre_b))
     a._refs = (y, gate, r, r_out, xn, scale, post_w, post_b, pre_w, pre_b)
     return a
@@ -612,7 +666,7 @@ def norm_gate_bwd_args(y, r_out, dr_out, dxn, dy, dr, gate=None, dgate=None, nor
                        workspace=None) -> NormGateBwdArgs:
     """Fill an hm_norm_gate_bwd_args (y, gate and the forward's r_out, the gradients of its
     outputs, the gradient buffers; rows [..., D] of one dtype, parameters and theirs [D] fp32)."""
-    import torch
+    torch = _need_torch()
     who = "norm_gate_bwd_args"
     D = y.shape[-1]
     _io(who, y.shape, y, y=y, gate=gate, r_out=r_out, dr_out=dr_out, dxn=dxn, dy=dy, dgate=dgate, dr=dr)
@@ -645,25 +699,34 @@ def rotary_args(q, k, q_out, k_out, rot: int = 0, base: float = 10000.0, layout:
                 mscale: float = 1.0, transpose: bool = False, positions=None, pos0: int = 0) -> RotaryArgs:
     """Fill an hm_rotary_args (q, q_out: [B, L, Hq, d]; k, k_out: [B, L, Hk, d] or None; rot = 0
     turns whole heads; positions: int64 [B, L], or [1, L] / [B, 1] shared along an axis of their own)."""
-    import torch
     who = "rotary_args"
-    B, L, Hq, d = q.shape
+    torch = _need_torch()
+    sh, ty, dev = q.shape, q.dtype, _current_device()
+    B, L, Hq, d = sh
     Hk = 0
-    _io(who, q.shape, q, q=q, q_out=q_out)
     qs, os = q.stride(), q_out.stride()
-    ks = ko = (0, 0, 0)
+    ks = ko = (0, 0, 0, 1)
+    ok = q.get_device() == dev and _is(q_out, sh, ty, dev) and qs[3] == os[3] == 1
     if k is not None:
         Hk = k.shape[2]
-        _io(who, (B, L, Hk, d), q, k=k, k_out=k_out)
         ks, ko = k.stride(), k_out.stride()
+        ok = ok and _is(k, (B, L, Hk, d), ty, dev) and _is(k_out, (B, L, Hk, d), ty, dev) and ks[3] == ko[3] == 1
     pb = pt = 0
     if positions is not None:
-        if positions.dtype != torch.int64 or positions.dim() != 2 or positions.shape[0] not in (1, B) \
+        if positions.dtype is not torch.int64 or positions.dim() != 2 or positions.shape[0] not in (1, B) \
                 or positions.shape[1] not in (1, L):
             raise ValueError("%s: positions must be int64 [B or 1, L or 1]" % who)
-        pb = positions.stride(0) if positions.shape[0] > 1 else 0
-        pt = positions.stride(1) if positions.shape[1] > 1 else 0
-    _one_device(who, q, k, q_out, k_out, positions)
+        pb, pt = positions.stride()
+        if positions.shape[0] == 1:
+            pb = 0
+        if positions.shape[1] == 1:
+            pt = 0
+        ok = ok and positions.get_device() == dev
+    if not ok:
+        _io(who, sh, q, q=q, q_out=q_out)
+        if k is not None:
+            _io(who, (B, L, Hk, d), q, k=k, k_out=k_out)
+        _one_device(who, q, k, q_out, k_out, positions)
     a = RotaryArgs(B, L, Hq, Hk, d, int(rot) or d, _dtype_code(q), int(layout), int(scaling), int(transpose), _ptr(q),
                    _ptr(k), _ptr(q_out), _ptr(k_out), qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], os[0], os[1], os[2],
                    ko[0], ko[1], ko[2], _ptr(positions), pb, pt, int(pos0), base, factor, orig_len, beta_slow,

@@ -5,9 +5,9 @@
 // A team of warps holds a row in registers: statistics come from there (mean
 // first, then the centred squares), so nothing is read twice.
 //
-// Forward: a warp takes up to 2048 bf16 (1024 fp32) elements of a row, so a
-// row of that width needs no barrier, its sums cost five shuffles per 64
-// elements of a lane, and all its loads are in flight at once.  Backward: each
+// Forward: a warp takes up to 1024 bf16 (512 fp32) elements of a row, so its
+// sums cost five shuffles per 32 elements of a lane and a barrier among few
+// warps, and all its loads are in flight at once.  Backward: each
 // thread keeps the five parameter gradients of its columns in registers over
 // all its rows (40 of them for 8 columns), so there a block shares a row; the
 // blocks' shares are summed by a second, small kernel in a fixed order.
@@ -118,33 +118,46 @@ __device__ __forceinline__ void store8(T *row, int piece, int tid, int nthr, int
     }
 }
 
-// fp32 parameters of a thread's columns, or the default.  The same for every
-// row, so they stay in L1, which the rows themselves pass by.
+// fp32 parameters of a thread's columns, of a piece that it has().  The same
+// for every row, so they stay in L1, which the rows themselves pass by.
 template <bool VEC>
-__device__ __forceinline__ void param8(const float *p, float dflt, int piece, int tid, int nthr, int D, F2 *f) {
+__device__ __forceinline__ void param8(const float *p, int piece, int tid, int nthr, int D, F2 *f) {
     if (VEC) {
         const int c = col_of<true>(piece, 0, tid, nthr);
-        if (p && c < D) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(p + c));
-            const float4 b = __ldg(reinterpret_cast<const float4 *>(p + c + 4));
-            f[0] = pk(a.x, a.y);
-            f[1] = pk(a.z, a.w);
-            f[2] = pk(b.x, b.y);
-            f[3] = pk(b.z, b.w);
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < kP; ++j) f[j] = splat(dflt);
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p + c));
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(p + c + 4));
+        f[0] = pk(a.x, a.y);
+        f[1] = pk(a.z, a.w);
+        f[2] = pk(b.x, b.y);
+        f[3] = pk(b.z, b.w);
     } else {
         float v[kE];
 #pragma unroll
         for (int j = 0; j < kE; ++j) {
             const int c = col_of<VEC>(piece, j, tid, nthr);
-            v[j] = p && c < D ? __ldg(p + c) : dflt;
+            v[j] = c < D ? __ldg(p + c) : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < kP; ++j) f[j] = pk(v[2 * j], v[2 * j + 1]);
     }
+}
+
+// u * p, u + p; a NULL p leaves u
+template <bool VEC>
+__device__ __forceinline__ void times(F2 *u, const float *p, int piece, int tid, int nthr, int D) {
+    if (!p) return;
+    F2 w[kP];
+    param8<VEC>(p, piece, tid, nthr, D, w);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) u[j] = u[j] * w[j];
+}
+template <bool VEC>
+__device__ __forceinline__ void plus(F2 *u, const float *p, int piece, int tid, int nthr, int D) {
+    if (!p) return;
+    F2 w[kP];
+    param8<VEC>(p, piece, tid, nthr, D, w);
+#pragma unroll
+    for (int j = 0; j < kP; ++j) u[j] = u[j] + w[j];
 }
 
 // whether a thread has any element of the piece; with VEC (D a multiple of 8) all or none
@@ -166,45 +179,50 @@ __device__ __forceinline__ float sum2(F2 f) {
     return u.x + u.y;
 }
 
-// Sum of one or two values over the team (a warp, or with BLOCK the whole
-// block); every thread gets them, always added in the same order.  `red`
-// alternates between two buffers, so one barrier per call is enough: a call's
-// reads are separated from the next-but-one call's writes by the next call's
-// barrier.
+// Sums over the team (a warp, or with BLOCK the whole block of up to 16
+// warps) of one or of four values; every thread gets them, always added in
+// the same order.  `red` alternates between two buffers, so one barrier per
+// call is enough: a call's reads are separated from the next-but-one call's
+// writes by the next call's barrier.
+constexpr int kMaxWarps = 16;
 __device__ __forceinline__ float xor_add(float v, int o) { return v + __shfl_xor_sync(0xffffffffu, v, o); }
 
 template <bool BLOCK>
-__device__ __forceinline__ float team_sum(float v, float (*red)[32], int &turn) {
+__device__ __forceinline__ float team_sum(float v, float (*red)[kMaxWarps][4], int &turn) {
     v = warp_sum(v);
     if (!BLOCK) return v;
-    float *r = red[turn & 1];
+    float (*r)[4] = red[turn & 1];
     ++turn;
     const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    if (lane == 0) r[threadIdx.x >> 5] = v;
+    if (lane == 0) r[threadIdx.x >> 5][0] = v;
     __syncthreads();
-    v = (lane & 15) < nw ? r[lane & 15] : 0.f;
+    v = (lane & 15) < nw ? r[lane & 15][0] : 0.f;
     return xor_add(xor_add(xor_add(xor_add(v, 8), 4), 2), 1);
 }
 
+// The four values travel together: each exchange halves what a lane carries,
+// so that a quarter of the warp ends with each sum.
 template <bool BLOCK>
-__device__ __forceinline__ float2 team_sum2(float a, float b, float2 (*red)[32], int &turn) {
+__device__ __forceinline__ float4 team_sum4(float4 q, float (*red)[kMaxWarps][4], int &turn) {
     const int lane = threadIdx.x & 31;
-    // the lower half warp goes on with a, the upper with b
-    const bool up = (lane & 16) != 0;
-    float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
-    v = xor_add(xor_add(xor_add(xor_add(v, 8), 4), 2), 1);
-    if (!BLOCK) {
-        const float o = __shfl_xor_sync(0xffffffffu, v, 16);
-        return up ? make_float2(o, v) : make_float2(v, o);
+    const bool b16 = (lane & 16) != 0, b8 = (lane & 8) != 0;
+    const float s0 = b16 ? q.x : q.z, s1 = b16 ? q.y : q.w;
+    const float k0 = (b16 ? q.z : q.x) + __shfl_xor_sync(0xffffffffu, s0, 16);
+    const float k1 = (b16 ? q.w : q.y) + __shfl_xor_sync(0xffffffffu, s1, 16);
+    float v = (b8 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, b8 ? k0 : k1, 8);
+    v = xor_add(xor_add(xor_add(v, 4), 2), 1);          // lanes 8 i .. 8 i + 7: the i-th value
+    if (BLOCK) {
+        float (*r)[4] = red[turn & 1];
+        ++turn;
+        const int nw = blockDim.x >> 5, w = lane & 7, i = lane >> 3;
+        if (w == 0) r[threadIdx.x >> 5][i] = v;
+        __syncthreads();
+        v = w < nw ? r[w][i] : 0.f;
+        if (w + 8 < nw) v += r[w + 8][i];
+        v = xor_add(xor_add(xor_add(v, 4), 2), 1);
     }
-    float2 *r = red[turn & 1];
-    ++turn;
-    const int nw = blockDim.x >> 5;
-    if ((lane & 15) == 0) (&r[threadIdx.x >> 5].x)[up] = v;
-    __syncthreads();
-    const float2 t = (lane & 15) < nw ? r[lane & 15] : make_float2(0.f, 0.f);
-    return make_float2(xor_add(xor_add(xor_add(xor_add(t.x, 8), 4), 2), 1),
-                       xor_add(xor_add(xor_add(xor_add(t.y, 8), 4), 2), 1));
+    return make_float4(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 8),
+                       __shfl_sync(0xffffffffu, v, 16), __shfl_sync(0xffffffffu, v, 24));
 }
 
 // 1 / (1 + e^-x): an e^-x beyond fp32 gives zero
@@ -221,7 +239,7 @@ __device__ __forceinline__ F2 sigmoid(F2 x) {
 // One row per team: a warp of four (BLOCK false), or the block.
 template <typename T, bool VEC, int NV, bool BLOCK, bool LAYER>
 __global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_norm_gate_args p) {
-    __shared__ float red[2][32];
+    __shared__ float red[2][kMaxWarps][4];
     int turn = 0;
     const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nthr = BLOCK ? blockDim.x : 32, D = (int)p.D;
     const float inv = 1.f / (float)D;
@@ -264,34 +282,25 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         if (!has<VEC>(k, tid, nthr, D)) break;
-        F2 u[kP], w[kP], c[kP];
+        F2 u[kP], c[kP];
         ry[k].get(u);
         rr[k].get(r[k]);
         if (p.post) {
-            if (p.post_w) {
-                param8<VEC>(p.post_w, 1.f, k, tid, nthr, D, w);
 #pragma unroll
-                for (int j = 0; j < kP; ++j) u[j] = (LAYER ? u[j] + splat(-mean) : u[j]) * (w[j] * splat(rstd));
-            } else {
-#pragma unroll
-                for (int j = 0; j < kP; ++j) u[j] = (LAYER ? u[j] + splat(-mean) : u[j]) * splat(rstd);
-            }
-            if (p.post_b) {
-                param8<VEC>(p.post_b, 0.f, k, tid, nthr, D, c);
-#pragma unroll
-                for (int j = 0; j < kP; ++j) u[j] = u[j] + c[j];
-            }
+            for (int j = 0; j < kP; ++j) u[j] = (LAYER ? u[j] + splat(-mean) : u[j]) * splat(rstd);
+            times<VEC>(u, p.post_w, k, tid, nthr, D);
+            plus<VEC>(u, p.post_b, k, tid, nthr, D);
         }
         if (p.gate) {
             rg[k].get(c);
 #pragma unroll
             for (int j = 0; j < kP; ++j) u[j] = u[j] * (c[j] * sigmoid(c[j]));
         }
-        param8<VEC>(p.scale, 1.f, k, tid, nthr, D, w);
+        times<VEC>(u, p.scale, k, tid, nthr, D);
 #pragma unroll
         for (int j = 0; j < kP; ++j) {
             // columns behind D hold zero, for the sums below
-            r[k][j] = in_row<VEC>(fma(splat(p.alpha) * w[j], u[j], r[k][j]), k, j, tid, nthr, D);
+            r[k][j] = in_row<VEC>(fma(splat(p.alpha), u[j], r[k][j]), k, j, tid, nthr, D);
             v = LAYER ? v + r[k][j] : fma(r[k][j], r[k][j], v);
         }
         if (p.r_out) store8<VEC>((T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D, r[k]);
@@ -317,28 +326,27 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         if (!has<VEC>(k, tid, nthr, D)) break;
-        F2 w[kP], c[kP];
-        param8<VEC>(p.pre_w, 1.f, k, tid, nthr, D, w);
 #pragma unroll
-        for (int j = 0; j < kP; ++j) r[k][j] = (LAYER ? r[k][j] + splat(-mean) : r[k][j]) * (w[j] * splat(rstd));
-        if (p.pre_b) {
-            param8<VEC>(p.pre_b, 0.f, k, tid, nthr, D, c);
-#pragma unroll
-            for (int j = 0; j < kP; ++j) r[k][j] = r[k][j] + c[j];
-        }
+        for (int j = 0; j < kP; ++j) r[k][j] = (LAYER ? r[k][j] + splat(-mean) : r[k][j]) * splat(rstd);
+        times<VEC>(r[k], p.pre_w, k, tid, nthr, D);
+        plus<VEC>(r[k], p.pre_b, k, tid, nthr, D);
         store8<VEC>((T *)p.xn + row * p.xn_stride, k, tid, nthr, D, r[k]);
     }
 }
 
 // A team per row (the block, or with BLOCK false each warp), rows `teams`
-// apart, the next row's loads under way while one is worked on.
+// apart.  A row stays in registers as it was loaded and is unpacked where a
+// pass needs it; what the last pass does not read is loaded for the next row
+// in front of it.  FULL: the common case that every row array is there and y
+// is normalised, known to the compiler.
 // part[(team * 5 + i) * D + c]: the team's share of dscale, dpost_w, dpost_b,
 // dpre_w, dpre_b.
-template <typename T, bool VEC, int NV, bool BLOCK, bool LAYER>
-__global__ void __launch_bounds__(BLOCK ? 512 : 256, 1)
+template <typename T, bool VEC, int NV, bool BLOCK, bool LAYER, bool FULL, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1)
 norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
-    __shared__ float2 red[2][32];
+    __shared__ float red[2][kMaxWarps][4];
     int turn = 0;
+    const bool gate = FULL || p.gate, post = FULL || p.post, pre = FULL || p.dxn;
     const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nthr = BLOCK ? blockDim.x : 32, D = (int)p.D;
     const float inv = 1.f / (float)D;
     const int64_t team = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -351,128 +359,171 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
 #pragma unroll
             for (int j = 0; j < kP; ++j) acc[i][k][j] = splat(0.f);
     Raw8<T> ry[NV], rg[NV], rr[NV], rd[NV], re[NV];
+    auto fetch_y = [&](int64_t row) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) ry[k] = load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
+    };
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            ry[k] = load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
-            if (p.gate) rg[k] = load8<VEC>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D);
-            if (p.dxn) {
+            if (gate) rg[k] = load8<VEC>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D);
+            if (pre) {
                 rr[k] = load8<VEC>((const T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D);
                 re[k] = load8<VEC>((const T *)p.dxn + row * p.dxn_stride, k, tid, nthr, D);
             }
-            if (p.dr_out) rd[k] = load8<VEC>((const T *)p.dr_out + row * p.dr_out_stride, k, tid, nthr, D);
+            if (FULL || p.dr_out) rd[k] = load8<VEC>((const T *)p.dr_out + row * p.dr_out_stride, k, tid, nthr, D);
             else rd[k].zero();
         }
     };
-    if (team < p.rows) fetch(team);
+    if (team < p.rows) {
+        fetch_y(team);
+        fetch(team);
+    }
     for (int64_t row = team; row < p.rows; row += teams) {
-        F2 y[NV][kP], r[NV][kP], d[NV][kP], e[NV][kP], g[NV][kP], w[kP], c[kP];
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            ry[k].get(y[k]);
-            if (p.gate) rg[k].get(g[k]);
-            if (p.dxn) rr[k].get(r[k]), re[k].get(e[k]);
-            rd[k].get(d[k]);
-        }
-        if (row + teams < p.rows) fetch(row + teams);
-        // statistics of y and of r_out; both rows are left centred
-        F2 v0 = splat(0.f), v1 = splat(0.f);
-        float2 v;
+        // means of y and of r_out
+        float my = 0.f, mr = 0.f;
+        F2 f[kP], v0 = splat(0.f), v1 = splat(0.f);
         if (LAYER) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int j = 0; j < kP; ++j) {
-                    v0 = v0 + y[k][j];
-                    if (p.dxn) v1 = v1 + r[k][j];
-                }
-            v = team_sum2<BLOCK>(sum2(v0), sum2(v1), red, turn);
-            const F2 my = splat(p.post ? -v.x * inv : 0.f), mr = splat(-v.y * inv);
-            v0 = v1 = splat(0.f);
-#pragma unroll
             for (int k = 0; k < NV; ++k) {
-                if (!has<VEC>(k, tid, nthr, D)) break;
+                ry[k].get(f);
 #pragma unroll
-                for (int j = 0; j < kP; ++j) {
-                    y[k][j] = in_row<VEC>(y[k][j] + my, k, j, tid, nthr, D);
-                    if (p.dxn) r[k][j] = in_row<VEC>(r[k][j] + mr, k, j, tid, nthr, D);
+                for (int j = 0; j < kP; ++j) v0 = v0 + f[j];
+                if (pre) {
+                    rr[k].get(f);
+#pragma unroll
+                    for (int j = 0; j < kP; ++j) v1 = v1 + f[j];
                 }
             }
+            const float4 v = team_sum4<BLOCK>(make_float4(sum2(v0), sum2(v1), 0.f, 0.f), red, turn);
+            my = post ? -v.x * inv : 0.f;
+            mr = -v.y * inv;
         }
+        // a row of a piece, less its mean
+        auto centred = [&](const Raw8<T> &raw, float mean, int k, F2 *o) {
+            raw.get(o);
+            if (LAYER) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int j = 0; j < kP; ++j) {
-                v0 = fma(y[k][j], y[k][j], v0);
-                if (p.dxn) v1 = fma(r[k][j], r[k][j], v1);
+                for (int j = 0; j < kP; ++j) o[j] = in_row<VEC>(o[j] + splat(mean), k, j, tid, nthr, D);
             }
-        v = team_sum2<BLOCK>(sum2(v0), sum2(v1), red, turn);
-        const float rsy = p.post ? rsqrtf(v.x * inv + p.eps) : 1.f, rsr = rsqrtf(v.y * inv + p.eps);
-        if (p.dxn) {
-            // dr = dr_out + rstd (w e - mean(w e) - u mean(w e u)), u = (r - mean) rstd
-            v0 = v1 = splat(0.f);
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                param8<VEC>(p.pre_w, 1.f, k, tid, nthr, D, w);
-#pragma unroll
-                for (int j = 0; j < kP; ++j) {
-                    const F2 u = r[k][j] * splat(rsr);
-                    acc[3][k][j] = fma(e[k][j], u, acc[3][k][j]);
-                    acc[4][k][j] = acc[4][k][j] + e[k][j];
-                    r[k][j] = u;
-                    e[k][j] = e[k][j] * w[j];
-                    v0 = v0 + e[k][j];
-                    v1 = fma(e[k][j], u, v1);
-                }
-            }
-            v = team_sum2<BLOCK>(sum2(v0), sum2(v1), red, turn);
-            const F2 m0 = splat(LAYER ? -v.x * inv : 0.f), m1 = splat(-v.y * inv);
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int j = 0; j < kP; ++j)
-                    d[k][j] = fma(splat(rsr), e[k][j] + fma(r[k][j], m1, m0), d[k][j]);
-        }
+        };
+        // dr = dr_out + rstd (w e - mean(w e) - u mean(w e u)), u = (r - mean) rstd, e = dxn: the sums
+        // over w e and w e (r - mean) go with those over the squares
+        F2 v2 = splat(0.f), v3 = splat(0.f);
         v0 = v1 = splat(0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (!has<VEC>(k, tid, nthr, D)) break;
-            if (p.dr) store8<VEC>((T *)p.dr + row * p.dr_stride, k, tid, nthr, D, d[k]);
-            F2 pw[kP], pb[kP];
-            param8<VEC>(p.scale, 1.f, k, tid, nthr, D, c);
-            param8<VEC>(p.post_w, 1.f, k, tid, nthr, D, pw);
-            param8<VEC>(p.post_b, 0.f, k, tid, nthr, D, pb);
+            if (pre) {
+                F2 we[kP];
+                re[k].get(we);
+                times<VEC>(we, p.pre_w, k, tid, nthr, D);        // zero behind D
+                centred(rr[k], mr, k, f);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    v1 = fma(f[j], f[j], v1);
+                    if (LAYER) v2 = v2 + we[j];
+                    v3 = fma(we[j], f[j], v3);
+                }
+            }
+            centred(ry[k], my, k, f);
+#pragma unroll
+            for (int j = 0; j < kP; ++j) v0 = fma(f[j], f[j], v0);
+        }
+        const float4 v = team_sum4<BLOCK>(make_float4(sum2(v0), sum2(v1), sum2(v2), sum2(v3)), red, turn);
+        const float rsy = post ? rsqrtf(v.x * inv + p.eps) : 1.f, rsr = rsqrtf(v.y * inv + p.eps);
+        const float r0 = -rsr * (v.z * inv), r1 = -rsr * (rsr * (v.w * inv));
+        F2 d[NV][kP];
+        v0 = v1 = splat(0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (!has<VEC>(k, tid, nthr, D)) break;
+            rd[k].get(d[k]);
+            if (pre) {
+                F2 e[kP];
+                re[k].get(e);
+                centred(rr[k], mr, k, f);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    const F2 u = f[j] * splat(rsr);
+                    acc[3][k][j] = fma(e[j], u, acc[3][k][j]);
+                    acc[4][k][j] = acc[4][k][j] + e[j];
+                    d[k][j] = fma(u, splat(r1), LAYER ? d[k][j] + splat(r0) : d[k][j]);
+                }
+                times<VEC>(e, p.pre_w, k, tid, nthr, D);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) d[k][j] = fma(e[j], splat(rsr), d[k][j]);
+            }
+            if (FULL || p.dr) store8<VEC>((T *)p.dr + row * p.dr_stride, k, tid, nthr, D, d[k]);
+            F2 n[kP], dm[kP], u[kP];
+            centred(ry[k], my, k, u);
 #pragma unroll
             for (int j = 0; j < kP; ++j) {
-                const F2 da = in_row<VEC>(d[k][j], k, j, tid, nthr, D) * splat(p.alpha), dm = da * c[j];
-                const F2 u = p.post ? y[k][j] * splat(rsy) : y[k][j];
-                const F2 n = p.post ? fma(u, pw[j], pb[j]) : u;
-                F2 m = n, dn = dm;
-                if (p.gate) {
-                    const F2 sg = sigmoid(g[k][j]), si = g[k][j] * sg;
-                    m = n * si;
-                    dn = dm * si;
-                    // SiLU'(g) = sg + si (1 - sg)
-                    g[k][j] = dm * n * fma(si, splat(1.f) - sg, sg);
-                }
-                acc[0][k][j] = fma(da, m, acc[0][k][j]);
-                acc[1][k][j] = fma(dn, u, acc[1][k][j]);
-                acc[2][k][j] = acc[2][k][j] + dn;
-                y[k][j] = u;
-                d[k][j] = p.post ? dn * pw[j] : dn;
-                v0 = v0 + d[k][j];
-                v1 = fma(d[k][j], u, v1);
+                if (post) u[j] = u[j] * splat(rsy);
+                n[j] = u[j];
+                d[k][j] = dm[j] = in_row<VEC>(d[k][j], k, j, tid, nthr, D) * splat(p.alpha);
             }
-            if (p.gate) store8<VEC>((T *)p.dgate + row * p.dgate_stride, k, tid, nthr, D, g[k]);
-        }
-        if (p.post) {
-            v = team_sum2<BLOCK>(sum2(v0), sum2(v1), red, turn);
-            const F2 m0 = splat(LAYER ? -v.x * inv : 0.f), m1 = splat(-v.y * inv);
+            if (post) {
+                times<VEC>(n, p.post_w, k, tid, nthr, D);
+                plus<VEC>(n, p.post_b, k, tid, nthr, D);
+            }
+            times<VEC>(dm, p.scale, k, tid, nthr, D);
+            if (gate) {
+                F2 g[kP];
+                rg[k].get(g);
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+                for (int j = 0; j < kP; ++j) {
+                    const F2 sg = sigmoid(g[j]), si = g[j] * sg;
+                    acc[0][k][j] = fma(d[k][j], n[j] * si, acc[0][k][j]);
+                    // SiLU'(g) = sg + si (1 - sg)
+                    g[j] = dm[j] * n[j] * fma(si, splat(1.f) - sg, sg);
+                    d[k][j] = dm[j] * si;
+                }
+                store8<VEC>((T *)p.dgate + row * p.dgate_stride, k, tid, nthr, D, g);
+            } else {
 #pragma unroll
-                for (int j = 0; j < kP; ++j) d[k][j] = splat(rsy) * (d[k][j] + fma(y[k][j], m1, m0));
+                for (int j = 0; j < kP; ++j) {
+                    acc[0][k][j] = fma(d[k][j], n[j], acc[0][k][j]);
+                    d[k][j] = dm[j];
+                }
+            }
+            // d: gradient of the normalised (or plain) y
+            if (post) {
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    acc[1][k][j] = fma(d[k][j], u[j], acc[1][k][j]);
+                    acc[2][k][j] = acc[2][k][j] + d[k][j];
+                }
+                times<VEC>(d[k], p.post_w, k, tid, nthr, D);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    if (LAYER) v0 = v0 + d[k][j];
+                    v1 = fma(d[k][j], u[j], v1);
+                }
+            }
         }
+        if (row + teams < p.rows) fetch(row + teams);
+        if (post) {
+            float y0 = 0.f, y1;
+            if (LAYER) {
+                const float4 q = team_sum4<BLOCK>(make_float4(sum2(v0), sum2(v1), 0.f, 0.f), red, turn);
+                y0 = -rsy * (q.x * inv);
+                y1 = -rsy * (q.y * inv);
+            } else {
+                y1 = -rsy * (team_sum<BLOCK>(sum2(v1), red, turn) * inv);
+            }
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if (!has<VEC>(k, tid, nthr, D)) break;
+                centred(ry[k], my, k, f);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    const F2 q = fma(d[k][j], splat(rsy), (f[j] * splat(rsy)) * splat(y1));
+                    d[k][j] = LAYER ? q + splat(y0) : q;
+                }
+            }
+        }
+        if (row + teams < p.rows) fetch_y(row + teams);
 #pragma unroll
         for (int k = 0; k < NV; ++k) store8<VEC>((T *)p.dy + row * p.dy_stride, k, tid, nthr, D, d[k]);
     }
@@ -557,12 +608,13 @@ struct Team {
     int blocks;          // backward
 };
 
-// Forward: a warp per row up to 8 pieces a lane (4 of fp32, as many
-// registers); more warps for wider rows, and for so few rows that one warp
-// each would leave most of the GPU idle.
+// Forward: up to 4 pieces a lane (2 of fp32, as many registers): 2048 bf16
+// columns over 2 warps took 117 us for 32768 rows, over 1 warp of 8 pieces 134,
+// over 4 warps 121, over 8 157.  More warps for wider rows, and for so few
+// rows that these would leave most of the GPU idle.
 // Rows that are read element by element get a block with as few pieces as it can.
 Team fwd_team(int64_t rows, int64_t D, size_t es, bool vec) {
-    const int pieces = (int)((D + 32 * kE - 1) / (32 * kE)), most = !vec ? (D > 8192 ? 4 : D > 4096 ? 2 : 1) : es == 2 ? 8 : 4;
+    const int pieces = (int)((D + 32 * kE - 1) / (32 * kE)), most = !vec ? (D > 8192 ? 4 : D > 4096 ? 2 : 1) : es == 2 || D > 8192 ? 4 : 2;
     int warps = 1;
     while ((pieces + warps - 1) / warps > most) warps *= 2;
     while (warps < 16 && (pieces + warps - 1) / warps > 1 && rows * warps * 2 <= 148 * 16) warps *= 2;
@@ -633,8 +685,7 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
         if (!vec) HM_FWD_S(__nv_bfloat16);
         else if (t.nv == 1) HM_FWD_B(__nv_bfloat16, 1);
         else if (t.nv == 2) HM_FWD_B(__nv_bfloat16, 2);
-        else if (t.nv == 4) HM_FWD_B(__nv_bfloat16, 4);
-        else HM_FWD_B(__nv_bfloat16, 8);
+        else HM_FWD_B(__nv_bfloat16, 4);
     } else {
         if (!vec) HM_FWD_S(float);
         else if (t.nv == 1) HM_FWD_B(float, 1);
@@ -688,16 +739,19 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     cudaStream_t s = (cudaStream_t)stream;
     float *part = (float *)a->workspace;
     if (t.blocks > 0) {
-#define HM_BWD(T, V, N, B)                                                                             \
-    (a->norm == HM_NORM_LAYER                                                                          \
-         ? norm_gate_bwd_kernel<T, V, N, B, true><<<t.blocks, B ? t.nthr : 256, 0, s>>>(*a, part)      \
-         : norm_gate_bwd_kernel<T, V, N, B, false><<<t.blocks, B ? t.nthr : 256, 0, s>>>(*a, part))
-#define HM_BWD_N(T, V)                                                                                 \
-    (!block ? HM_BWD(T, V, 1, false)                                                                   \
-            : t.nv == 1 ? HM_BWD(T, V, 1, true) : t.nv == 2 ? HM_BWD(T, V, 2, true) : HM_BWD(T, V, 4, true))
+        const bool full = a->gate && a->post && a->dxn && a->dr_out && a->dr;
+#define HM_BWD_F(T, V, N, B, Y, Z)                                                                          \
+    (V && full ? norm_gate_bwd_kernel<T, V, N, B, Y, V, Z><<<t.blocks, B ? t.nthr : 256, 0, s>>>(*a, part)      \
+               : norm_gate_bwd_kernel<T, V, N, B, Y, false, Z><<<t.blocks, B ? t.nthr : 256, 0, s>>>(*a, part))
+#define HM_BWD(T, V, N, B, Z) (a->norm == HM_NORM_LAYER ? HM_BWD_F(T, V, N, B, true, Z) : HM_BWD_F(T, V, N, B, false, Z))
+#define HM_BWD_N(T, V)                                                                                      \
+    (!block ? HM_BWD(T, V, 1, false, 256)                                                                   \
+            : t.nv == 1 ? (t.nthr <= 256 ? HM_BWD(T, V, 1, true, 256) : HM_BWD(T, V, 1, true, 512))         \
+            : t.nv == 2 ? HM_BWD(T, V, 2, true, 512) : HM_BWD(T, V, 4, true, 512))
         if (a->io_dtype == HM_BF16) vec ? HM_BWD_N(__nv_bfloat16, true) : HM_BWD_N(__nv_bfloat16, false);
         else vec ? HM_BWD_N(float, true) : HM_BWD_N(float, false);
 #undef HM_BWD
+#undef HM_BWD_F
 #undef HM_BWD_N
         count_launches(1);
     }
