@@ -240,7 +240,7 @@ __device__ __forceinline__ F2 finish_window(const Exchange &x, int it, F2 hb) {
     const int i = it - 1;
     wait_bar(&x.high[i & 1], (i >> 1) & 1, x.abort_flag, x.err, 1);
     const Map2 *m = x.ctas + ((i & 1) * x.cluster + x.rank) * 32 + (threadIdx.x & 31);
-#pragma unroll 4
+#pragma unroll 2
     for (int r = x.rank; r < x.cluster; ++r, m += 32) hb = apply(*m, hb);
     return hb;
 }
@@ -248,6 +248,7 @@ __device__ __forceinline__ F2 finish_window(const Exchange &x, int it, F2 hb) {
 // After the block barrier of window `it` (all warps' maps in agg): the state
 // entering this warp's run, from `h`, the state at the start of the window.
 // h becomes the state at the block's runs (cluster > 1) or behind the window.
+// Only the last warp composes all the block's maps and hands them on.
 template <int W>
 __device__ __forceinline__ F2 enter_run(const Exchange &x, int it, int warp, F2 &h) {
     const int lane = threadIdx.x & 31;
@@ -261,23 +262,27 @@ __device__ __forceinline__ F2 enter_run(const Exchange &x, int it, int warp, F2 
         }
         return hin;
     }
-    Map2 before = {splat(1.f), splat(0.f)}, q = agg[0];
-#pragma unroll
-    for (int w = 1; w < W; ++w) {
-        if (w == warp) before = q;
-        q = then(q, agg[w * 32]);
+    Map2 before = {splat(1.f), splat(0.f)};
+    if (warp > 0) {
+        before = agg[0];
+#pragma unroll 1
+        for (int w = 1; w < warp; ++w) before = then(before, agg[w * 32]);
     }
-    const uint32_t slot = tc::smem_u32(x.ctas + ((it & 1) * x.cluster + x.rank) * 32 + lane);
-    const uint32_t lo = tc::smem_u32(&x.low[it & 1]), hi = tc::smem_u32(&x.high[it & 1]);
-    if (threadIdx.x == 0) {
-        tc::mbar_arrive_expect_tx(&x.high[it & 1], (uint32_t)(x.cluster - x.rank) * 512u);
-        if (x.rank) tc::mbar_arrive_expect_tx(&x.low[it & 1], (uint32_t)x.rank * 512u);
+    if (warp == W - 1) {
+        const Map2 q = then(before, agg[(W - 1) * 32]);
+        const uint32_t slot = tc::smem_u32(x.ctas + ((it & 1) * x.cluster + x.rank) * 32 + lane);
+        const uint32_t lo = tc::smem_u32(&x.low[it & 1]), hi = tc::smem_u32(&x.high[it & 1]);
+        if (lane == 0) {
+            tc::mbar_arrive_expect_tx(&x.high[it & 1], (uint32_t)(x.cluster - x.rank) * 512u);
+            if (x.rank) tc::mbar_arrive_expect_tx(&x.low[it & 1], (uint32_t)x.rank * 512u);
+        }
+#pragma unroll 1
+        for (int r = 0; r < x.cluster; ++r) st_async16(slot, x.rank < r ? lo : hi, (uint32_t)r, q);
     }
-    for (int r = warp; r < x.cluster; r += W) st_async16(slot, x.rank < r ? lo : hi, (uint32_t)r, q);
     if (x.rank) {
         wait_bar(&x.low[it & 1], (it >> 1) & 1, x.abort_flag, x.err, 2);
         const Map2 *m = x.ctas + (it & 1) * x.cluster * 32 + lane;
-#pragma unroll 4
+#pragma unroll 2
         for (int r = 0; r < x.rank; ++r, m += 32) h = apply(*m, h);
     }
     return warp ? apply(before, h) : h;
@@ -534,11 +539,13 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     const T *dyp = (const T *)p.dy + b * p.dy_stride_b + c;
     T *dxp = (T *)p.dx + b * p.dx_stride_b + c, *ddtp = (T *)p.ddt + b * p.ddt_stride_b + c;
     F2 sumA = splat(0.f), sumb = splat(0.f);
+    int stage = 0;
+    uint32_t phase = 0;
 
     for (int it = 0; it < iters; ++it) {
         const int chunk = chunk_of(it), t0 = chunk * kChunk + warp * kRb;
         const int m = chunk < 0 ? 0 : min(max(n - t0, 0), kRb);
-        T *tile = stage0 + (it % kBwdStages) * 3 * kTile + (warp * kRb) * kCols + 2 * lane;
+        T *tile = stage0 + stage * 3 * kTile + (warp * kRb) * kCols + 2 * lane;
         F2 a[kRb], h[kRb], step[kRb], sig[kRb], beta[kRb];
         Map2 mf = {splat(1.f), splat(0.f)}, mr = {splat(1.f), splat(0.f)};
         F2 hin = splat(0.f);
@@ -546,7 +553,7 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
             const float *st = (const float *)p.states + (b * f.nchunk + chunk) * p.D + c;
             hin = pk(st[0], in1 ? st[1] : 0.f);
         }
-        if (WIDE && chunk >= 0) wait_bar(&full[it % kBwdStages], (it / kBwdStages) & 1, &abort_flag, err, 3);
+        if (WIDE && chunk >= 0) wait_bar(&full[stage], phase, &abort_flag, err, 3);
         if (m > 0) {
             // a thread's own elements of the tile: element loads put them there, and tokens behind
             // the end become a step of zero, no input, no gradient of their own
@@ -617,7 +624,6 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
                 h[i] = hin;
                 hin = next;
             }
-            const bool whole = WIDE && m == kRb;
 #pragma unroll
             for (int i = kRb - 1; i >= 0; --i) {
                 Raw<T> rx, rdy;
@@ -635,21 +641,14 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
                 F2 dz = dla * par.nrate;
                 if (SCALE == HM_INPUT_STEP) dz = fma(g, xv, dz);
                 dz = dz * sig[i];
-                sumA = fma(dla, step[i] * par.nrate, sumA);
+                sumA = fma(dla, step[i], sumA);
                 sumb = sumb + dz;
                 const F2 dx = SCALE == HM_INPUT_PLAIN ? g
                               : SCALE == HM_INPUT_STEP ? g * (step[i] * splat(kLn2)) : g * beta[i];
-                if (whole) {
-                    st_pair(tile + i * kCols, dz);
-                    st_pair(tile + kTile + i * kCols, dx);
-                } else if (i < m) {
-                    const int64_t od = (int64_t)(t0 + i) * p.ddt_stride_t, ox = (int64_t)(t0 + i) * p.dx_stride_t;
-                    const float2 vz = un(dz), vx = un(dx);
-                    if (in0) hm_st(ddtp, od, vz.x), hm_st(dxp, ox, vx.x);
-                    if (in1) hm_st(ddtp, od + 1, vz.y), hm_st(dxp, ox + 1, vx.y);
-                }
+                st_pair(tile + i * kCols, dz);
+                st_pair(tile + kTile + i * kCols, dx);
             }
-            if (whole) {
+            if (WIDE && m == kRb) {
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -658,8 +657,17 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
                     tc::tma_store_3d(&map_dx, row + kTile, (int)c0, t0, (int)b);
                     tc::bulk_commit();
                 }
+            } else {             // a thread's own elements, one by one
+#pragma unroll 1
+                for (int i = 0; i < m; ++i) {
+                    T *oz = ddtp + (int64_t)(t0 + i) * p.ddt_stride_t, *ox = dxp + (int64_t)(t0 + i) * p.dx_stride_t;
+                    const T *q = tile + i * kCols;
+                    if (in0) oz[0] = q[0], ox[0] = q[kTile];
+                    if (in1) oz[1] = q[1], ox[1] = q[kTile + 1];
+                }
             }
         }
+        if (++stage == kBwdStages) stage = 0, phase ^= 1;
     }
     if (cluster > 1 && iters > 0) carry = finish_window(x, iters, carry);
     if (p.dh0 && rank == 0 && warp == 0) {
@@ -677,7 +685,7 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
             sumA = sumA + v.A;
             sumb = sumb + v.B;
         }
-        sumA = sumA * splat(kLn2);             // log a from its base-2 exponent
+        sumA = sumA * par.nrate * splat(kLn2); // log a = -rate Delta, Delta from its base-2 exponent
         float *o = f.part + (b * cluster + rank) * 2 * p.D + c;
         if (in0) o[0] = un(sumA).x, o[p.D] = un(sumb).x;
         if (in1) o[1] = un(sumA).y, o[p.D + 1] = un(sumb).y;
