@@ -439,7 +439,7 @@ typedef struct {
     size_t states_bytes;
 } hm_gated_scan_args;
 
-/* Bytes of `states` (0 on invalid sizes).  Grows with B * L * D / 32. */
+/* Bytes of `states` (0 on invalid sizes): about B * L * D / 16. */
 HM_API size_t hm_gated_scan_states_size(const hm_gated_scan_args *a);
 
 HM_API hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t stream);

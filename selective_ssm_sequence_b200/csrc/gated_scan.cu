@@ -215,7 +215,7 @@ struct Exchange {
 
 constexpr int kR = 16;        // tokens of a warp's run
 constexpr int kCols = 64;     // channels of a warp
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 constexpr int kStages = 2;
 
 // Bounded wait of every thread of the block.  After a timeout the kernel keeps
@@ -810,17 +810,28 @@ struct Split {
     int warps, cluster;       // of a block; blocks of a cluster
 };
 
-// The tokens are split over warps and blocks until about 14 warps stand on
-// each SM, or the sequence is.
-Split split_of(int64_t units, int64_t L) {
-    const int64_t runs = (L + kR - 1) / kR;
-    Split s{runs > 4 ? 8 : 4, 1};
-    while (s.cluster < kMaxCluster && units * s.cluster * s.warps * 2 <= 148 * 16 && (int64_t)s.warps * s.cluster < runs)
+// Forward.  Four warps a block for sequences up to 2048 and for fp32 (whose
+// tiles leave room for two such blocks on an SM), else eight; the tokens are
+// split over up to 8 blocks of a cluster until about 14 warps stand on each
+// SM, as long as a block keeps 2 windows or the SMs are mostly empty.  Measured
+// (bf16, 4 x 2048 x 2048): 4 warps x 1, 2, 4, 8 blocks 39, 33, 30, 36 us, 8 x
+// 1, 2, 4: 31, 31, 38; 8 x 4096 x 2048: 8 x 1: 82, 4 x 1: 89, 8 x 2: 100; one of
+// 32768: 8 x 8: 129, 4 x 8: 137, 8 x 4: 148, 8 x 16: 162; fp32 2 x 4096 x 2048:
+// 4 x 2, 4, 8: 52, 38, 46.  Padded batches count half their tokens (fp32 5 x
+// up to 1531 x 1001: 4 x 2, 4, 8: 121, 64, 39).
+Split split_of(int64_t units, int64_t L, hm_dtype t, bool padded) {
+    const int64_t runs = (L + kR - 1) / kR, warps = t == HM_BF16 && L > 2048 ? 8 : 4;
+    const int64_t most = (t == HM_BF16 ? 148 * 16 : 148 * 12) * (padded ? 2 : 1);
+    Split s{(int)warps, 1};
+    while (s.cluster < kMaxCluster && units * s.cluster * 2 * warps <= most && warps * s.cluster < runs &&
+           (runs >= 2 * warps * s.cluster * 2 || units * s.cluster * 2 <= 148))
         s.cluster *= 2;
     return s;
 }
 
-// the same rule for the backward, whose blocks have 8 warps and 64 tokens
+// Backward: 8 warps and a window of 64 tokens a block.  4 x 2048 x 2048 with
+// its forward: 1, 2, 4, 8 blocks 95, 91, 98, 109 us; one of 32768: 4, 8, 16:
+// 411, 337, 427.
 Split bwd_split(int64_t units, int64_t L) {
     const int64_t chunks = (L + kChunk - 1) / kChunk;
     Split s{kWb, 1};
@@ -907,10 +918,6 @@ template <typename K, typename... A>
 cudaError_t launch_cluster(K kernel, int64_t units, Split sp, size_t smem, cudaStream_t s, A... args) {
     cudaError_t e = tc::ensure_smem_limit(kernel, (int)smem);
     if (e != cudaSuccess) return e;
-    if (sp.cluster > 8) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * sp.cluster));
     cfg.blockDim = dim3(sp.warps * 32);
@@ -937,7 +944,7 @@ extern "C" hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t 
     FwdArgs f{*a, (a->D + kCols - 1) / kCols, (a->L + kChunk - 1) / kChunk};
     const int64_t units = a->B * f.groups;
     const size_t es = esize(a->io_dtype);
-    const Split sp = split_of(units, a->L);
+    const Split sp = split_of(units, a->L, a->io_dtype, a->lengths != nullptr);
     if (units * sp.cluster > 0x7fffffffLL)
         return fail_args(HM_ERR_UNSUPPORTED, "gated_scan_fwd: B * D / 64 is too large");
     CUtensorMap mdt{}, mx{}, my{};

@@ -335,10 +335,9 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_
 }
 
 // A team per row (the block, or with BLOCK false each warp), rows `teams`
-// apart.  A row stays in registers as it was loaded and is unpacked where a
-// pass needs it; what the last pass does not read is loaded for the next row
-// in front of it.  FULL: the common case that every row array is there and y
-// is normalised, known to the compiler.
+// apart, the next row's loads under way while one is worked on.  FULL: the
+// common case that every row array is there and y is normalised, known to the
+// compiler.
 // part[(team * 5 + i) * D + c]: the team's share of dscale, dpost_w, dpost_b,
 // dpre_w, dpre_b.
 template <typename T, bool VEC, int NV, bool BLOCK, bool LAYER, bool FULL, int THREADS>
@@ -359,13 +358,10 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
 #pragma unroll
             for (int j = 0; j < kP; ++j) acc[i][k][j] = splat(0.f);
     Raw8<T> ry[NV], rg[NV], rr[NV], rd[NV], re[NV];
-    auto fetch_y = [&](int64_t row) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k) ry[k] = load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
-    };
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            ry[k] = load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
             if (gate) rg[k] = load8<VEC>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D);
             if (pre) {
                 rr[k] = load8<VEC>((const T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D);
@@ -375,38 +371,39 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
             else rd[k].zero();
         }
     };
-    if (team < p.rows) {
-        fetch_y(team);
-        fetch(team);
-    }
+    if (team < p.rows) fetch(team);
     for (int64_t row = team; row < p.rows; row += teams) {
-        // means of y and of r_out
-        float my = 0.f, mr = 0.f;
-        F2 f[kP], v0 = splat(0.f), v1 = splat(0.f);
+        F2 y[NV][kP], r[NV][kP], d[NV][kP], e[NV][kP], g[NV][kP];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            ry[k].get(y[k]);
+            if (gate) rg[k].get(g[k]);
+            if (pre) rr[k].get(r[k]), re[k].get(e[k]);
+            rd[k].get(d[k]);
+        }
+        if (row + teams < p.rows) fetch(row + teams);
+        // y and r_out less their means
+        F2 v0 = splat(0.f), v1 = splat(0.f);
         if (LAYER) {
 #pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    v0 = v0 + y[k][j];
+                    if (pre) v1 = v1 + r[k][j];
+                }
+            const float4 v = team_sum4<BLOCK>(make_float4(sum2(v0), sum2(v1), 0.f, 0.f), red, turn);
+            const F2 my = splat(post ? -v.x * inv : 0.f), mr = splat(-v.y * inv);
+#pragma unroll
             for (int k = 0; k < NV; ++k) {
-                ry[k].get(f);
+                if (!has<VEC>(k, tid, nthr, D)) break;
 #pragma unroll
-                for (int j = 0; j < kP; ++j) v0 = v0 + f[j];
-                if (pre) {
-                    rr[k].get(f);
-#pragma unroll
-                    for (int j = 0; j < kP; ++j) v1 = v1 + f[j];
+                for (int j = 0; j < kP; ++j) {
+                    y[k][j] = in_row<VEC>(y[k][j] + my, k, j, tid, nthr, D);
+                    if (pre) r[k][j] = in_row<VEC>(r[k][j] + mr, k, j, tid, nthr, D);
                 }
             }
-            const float4 v = team_sum4<BLOCK>(make_float4(sum2(v0), sum2(v1), 0.f, 0.f), red, turn);
-            my = post ? -v.x * inv : 0.f;
-            mr = -v.y * inv;
         }
-        // a row of a piece, less its mean
-        auto centred = [&](const Raw8<T> &raw, float mean, int k, F2 *o) {
-            raw.get(o);
-            if (LAYER) {
-#pragma unroll
-                for (int j = 0; j < kP; ++j) o[j] = in_row<VEC>(o[j] + splat(mean), k, j, tid, nthr, D);
-            }
-        };
         // dr = dr_out + rstd (w e - mean(w e) - u mean(w e u)), u = (r - mean) rstd, e = dxn: the sums
         // over w e and w e (r - mean) go with those over the squares
         F2 v2 = splat(0.f), v3 = splat(0.f);
@@ -416,51 +413,44 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
             if (!has<VEC>(k, tid, nthr, D)) break;
             if (pre) {
                 F2 we[kP];
-                re[k].get(we);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) we[j] = e[k][j];
                 times<VEC>(we, p.pre_w, k, tid, nthr, D);        // zero behind D
-                centred(rr[k], mr, k, f);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
-                    v1 = fma(f[j], f[j], v1);
+                    v1 = fma(r[k][j], r[k][j], v1);
                     if (LAYER) v2 = v2 + we[j];
-                    v3 = fma(we[j], f[j], v3);
+                    v3 = fma(we[j], r[k][j], v3);
                 }
             }
-            centred(ry[k], my, k, f);
 #pragma unroll
-            for (int j = 0; j < kP; ++j) v0 = fma(f[j], f[j], v0);
+            for (int j = 0; j < kP; ++j) v0 = fma(y[k][j], y[k][j], v0);
         }
         const float4 v = team_sum4<BLOCK>(make_float4(sum2(v0), sum2(v1), sum2(v2), sum2(v3)), red, turn);
         const float rsy = post ? rsqrtf(v.x * inv + p.eps) : 1.f, rsr = rsqrtf(v.y * inv + p.eps);
         const float r0 = -rsr * (v.z * inv), r1 = -rsr * (rsr * (v.w * inv));
-        F2 d[NV][kP];
         v0 = v1 = splat(0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (!has<VEC>(k, tid, nthr, D)) break;
-            rd[k].get(d[k]);
             if (pre) {
-                F2 e[kP];
-                re[k].get(e);
-                centred(rr[k], mr, k, f);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
-                    const F2 u = f[j] * splat(rsr);
-                    acc[3][k][j] = fma(e[j], u, acc[3][k][j]);
-                    acc[4][k][j] = acc[4][k][j] + e[j];
+                    const F2 u = r[k][j] * splat(rsr);
+                    acc[3][k][j] = fma(e[k][j], u, acc[3][k][j]);
+                    acc[4][k][j] = acc[4][k][j] + e[k][j];
                     d[k][j] = fma(u, splat(r1), LAYER ? d[k][j] + splat(r0) : d[k][j]);
                 }
-                times<VEC>(e, p.pre_w, k, tid, nthr, D);
+                times<VEC>(e[k], p.pre_w, k, tid, nthr, D);
 #pragma unroll
-                for (int j = 0; j < kP; ++j) d[k][j] = fma(e[j], splat(rsr), d[k][j]);
+                for (int j = 0; j < kP; ++j) d[k][j] = fma(e[k][j], splat(rsr), d[k][j]);
             }
             if (FULL || p.dr) store8<VEC>((T *)p.dr + row * p.dr_stride, k, tid, nthr, D, d[k]);
-            F2 n[kP], dm[kP], u[kP];
-            centred(ry[k], my, k, u);
+            F2 n[kP], dm[kP];
 #pragma unroll
             for (int j = 0; j < kP; ++j) {
-                if (post) u[j] = u[j] * splat(rsy);
-                n[j] = u[j];
+                if (post) y[k][j] = y[k][j] * splat(rsy);
+                n[j] = y[k][j];
                 d[k][j] = dm[j] = in_row<VEC>(d[k][j], k, j, tid, nthr, D) * splat(p.alpha);
             }
             if (post) {
@@ -469,17 +459,15 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
             }
             times<VEC>(dm, p.scale, k, tid, nthr, D);
             if (gate) {
-                F2 g[kP];
-                rg[k].get(g);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
-                    const F2 sg = sigmoid(g[j]), si = g[j] * sg;
+                    const F2 sg = sigmoid(g[k][j]), si = g[k][j] * sg;
                     acc[0][k][j] = fma(d[k][j], n[j] * si, acc[0][k][j]);
                     // SiLU'(g) = sg + si (1 - sg)
-                    g[j] = dm[j] * n[j] * fma(si, splat(1.f) - sg, sg);
+                    g[k][j] = dm[j] * n[j] * fma(si, splat(1.f) - sg, sg);
                     d[k][j] = dm[j] * si;
                 }
-                store8<VEC>((T *)p.dgate + row * p.dgate_stride, k, tid, nthr, D, g);
+                store8<VEC>((T *)p.dgate + row * p.dgate_stride, k, tid, nthr, D, g[k]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
@@ -491,39 +479,34 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
             if (post) {
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
-                    acc[1][k][j] = fma(d[k][j], u[j], acc[1][k][j]);
+                    acc[1][k][j] = fma(d[k][j], y[k][j], acc[1][k][j]);
                     acc[2][k][j] = acc[2][k][j] + d[k][j];
                 }
                 times<VEC>(d[k], p.post_w, k, tid, nthr, D);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
                     if (LAYER) v0 = v0 + d[k][j];
-                    v1 = fma(d[k][j], u[j], v1);
+                    v1 = fma(d[k][j], y[k][j], v1);
                 }
             }
         }
-        if (row + teams < p.rows) fetch(row + teams);
         if (post) {
             float y0 = 0.f, y1;
             if (LAYER) {
                 const float4 q = team_sum4<BLOCK>(make_float4(sum2(v0), sum2(v1), 0.f, 0.f), red, turn);
-                y0 = -rsy * (q.x * inv);
-                y1 = -rsy * (q.y * inv);
+                y0 = -q.x * inv;
+                y1 = -q.y * inv;
             } else {
-                y1 = -rsy * (team_sum<BLOCK>(sum2(v1), red, turn) * inv);
+                y1 = -team_sum<BLOCK>(sum2(v1), red, turn) * inv;
             }
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                if (!has<VEC>(k, tid, nthr, D)) break;
-                centred(ry[k], my, k, f);
+            for (int k = 0; k < NV; ++k)
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
-                    const F2 q = fma(d[k][j], splat(rsy), (f[j] * splat(rsy)) * splat(y1));
-                    d[k][j] = LAYER ? q + splat(y0) : q;
+                    const F2 q = fma(y[k][j], splat(y1), d[k][j]);
+                    d[k][j] = splat(rsy) * (LAYER ? q + splat(y0) : q);
                 }
-            }
         }
-        if (row + teams < p.rows) fetch_y(row + teams);
 #pragma unroll
         for (int k = 0; k < NV; ++k) store8<VEC>((T *)p.dy + row * p.dy_stride, k, tid, nthr, D, d[k]);
     }
@@ -544,24 +527,21 @@ struct GradPtrs {
 };
 
 // the teams' shares summed in a fixed order; a block of threads per 32 columns
-// and parameter, 8 rows of it walking the shares
-__global__ void __launch_bounds__(256) norm_gate_sum_kernel(const float *part, int teams, int D, GradPtrs g) {
-    __shared__ float s[8][33];
+// and parameter, 32 rows of it walking the shares
+__global__ void __launch_bounds__(1024) norm_gate_sum_kernel(const float *part, int teams, int D, GradPtrs g) {
+    __shared__ float s[32][33];
     float *out = g.out[blockIdx.y];
     if (!out) return;
     const int c = blockIdx.x * 32 + threadIdx.x;
     float v = 0.f;
     if (c < D) {
 #pragma unroll 4
-        for (int b = threadIdx.y; b < teams; b += 8) v += part[((int64_t)b * 5 + blockIdx.y) * D + c];
+        for (int b = threadIdx.y; b < teams; b += 32) v += part[((int64_t)b * 5 + blockIdx.y) * D + c];
     }
     s[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
-    if (threadIdx.y == 0 && c < D) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x];
-        out[c] = v;
-    }
+    v = warp_sum(s[threadIdx.x][threadIdx.y]);     // a warp per column now
+    if (threadIdx.x == 0 && blockIdx.x * 32 + threadIdx.y < D) out[blockIdx.x * 32 + threadIdx.y] = v;
 }
 
 // ------------------------------------------------------------------ host
@@ -759,7 +739,7 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     if (e == cudaSuccess) {
         // without dxn the pre-norm's parameters had no part in the loss: their shares are zero
         const GradPtrs g = {{a->dscale, a->dpost_w, a->dpost_b, a->dpre_w, a->dpre_b}};
-        norm_gate_sum_kernel<<<dim3((unsigned)((a->D + 31) / 32), 5), dim3(32, 8), 0, s>>>(part, (int)shares, (int)a->D, g);
+        norm_gate_sum_kernel<<<dim3((unsigned)((a->D + 31) / 32), 5), dim3(32, 32), 0, s>>>(part, (int)shares, (int)a->D, g);
         count_launches(1);
         e = cudaGetLastError();
     }
