@@ -248,6 +248,23 @@ def _need_torch():
     return _torch
 
 
+_native = None
+
+
+def _filler():
+    """The native argument filler, built beside libhm.so (imported after torch, whose libraries it uses)."""
+    global _native
+    if _native is None:
+        _need_torch()
+        try:
+            from . import _marshal as mod
+        except ImportError as e:
+            raise ImportError("_marshal.so is not built; run __graft_entry__.build() or "
+                              "python selective_ssm_sequence_b200/_build.py (%s)" % e) from e
+        _native = mod
+    return _native
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         torch = _need_torch()
@@ -467,17 +484,9 @@ def hm_block_fwd(args: BlockArgs, workspace, stream=None) -> None:
 
 # ---- the operators around the mixer: gated recurrence, seam between blocks, rotary positions.
 # Their helpers check what the C side cannot see (shapes, dtypes, devices) and raise ValueError.
-# A decode loop calls them for every token, so each tensor is looked at once (_is); only when one
-# does not pass is it found out, by the slower checks below, what to say about which.
-
-def _is(t, shape, dtype, dev: int) -> bool:
-    return t.shape == shape and t.dtype is dtype and t.get_device() == dev
-
-
-def _current_device() -> int:
-    torch = _need_torch()
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
-
+# A decode loop calls them for every token, so the native module _marshal fills the struct in the
+# common case; where it gives up (None), the checks below say what is wrong with which tensor, or
+# fill the struct themselves.
 
 def _io(who: str, shape, like, **ts):
     """Each given tensor has `like`'s dtype, this shape and contiguous elements in its last axis."""
@@ -521,28 +530,25 @@ def gated_scan_args(x, dt, y, A_log, dt_bias=None, h0=None, h_out=None, lengths=
                     states=None) -> GatedScanArgs:
     """Fill an hm_gated_scan_args (x, dt, y: [B, L, D], channels contiguous; h0,
     h_out: [B, D] fp32; lengths: [B] int32; A_log, dt_bias: [D] fp32)."""
-    sh, ty, dev = x.shape, x.dtype, _current_device()
-    B, L, D = sh
-    f32 = _need_torch().float32
-    xs, ds = x.stride(), dt.stride()
-    ys = y.stride() if y is not None else (0, 0, 1)
-    if not (x.get_device() == dev and _is(dt, sh, ty, dev) and xs[2] == ds[2] == ys[2] == 1
-            and (y is None or _is(y, sh, ty, dev))
-            and _is(A_log, (D,), f32, dev) and A_log.is_contiguous()
-            and (dt_bias is None or _is(dt_bias, (D,), f32, dev) and dt_bias.is_contiguous())
-            and (h0 is None or _is(h0, (B, D), f32, dev) and h0.is_contiguous())
-            and (h_out is None or _is(h_out, (B, D), f32, dev) and h_out.is_contiguous())
-            and lengths is None and states is None):
-        who = "gated_scan_args"
-        _io(who, sh, x, x=x, dt=dt, y=y)
-        _dense(who, (D,), f32, A_log=A_log, dt_bias=dt_bias)
-        _dense(who, (B, D), f32, h0=h0, h_out=h_out)
-        _dense(who, (B,), _torch.int32, lengths=lengths)
-        _one_device(who, x, dt, y, A_log, dt_bias, h0, h_out, lengths, states)
+    refs = (x, dt, y, A_log, dt_bias, h0, h_out, lengths, states)
+    raw = _filler().gated_scan(*refs, input_scale)
+    if raw is not None:
+        a = GatedScanArgs.from_buffer_copy(raw)
+        a._refs = refs
+        return a
+    who = "gated_scan_args"
+    torch = _need_torch()
+    B, L, D = x.shape
+    _io(who, x.shape, x, x=x, dt=dt, y=y)
+    _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias)
+    _dense(who, (B, D), torch.float32, h0=h0, h_out=h_out)
+    _dense(who, (B,), torch.int32, lengths=lengths)
+    _one_device(who, *refs)
+    xs, ds, ys = x.stride(), dt.stride(), y.stride() if y is not None else (0, 0)
     a = GatedScanArgs(B, L, D, _dtype_code(x), int(input_scale), _ptr(x), _ptr(dt), _ptr(y), xs[0], xs[1], ds[0],
                       ds[1], ys[0], ys[1], _ptr(A_log), _ptr(dt_bias), _ptr(h0), _ptr(lengths), _ptr(h_out),
                       _ptr(states), states.numel() * states.element_size() if states is not None else 0)
-    a._refs = (x, dt, y, A_log, dt_bias, h0, h_out, lengths, states)
+    a._refs = refs
     return a
 
 
@@ -558,6 +564,12 @@ def gated_scan_bwd_args(x, dt, dy, dx, ddt, A_log, dA_log, states, dt_bias=None,
                         dh0=None, lengths=None, input_scale: int = 0, workspace=None) -> GatedScanBwdArgs:
     """Fill an hm_gated_scan_bwd_args (the forward's inputs and its `states`;
     dy, dx, ddt: [B, L, D]; dh_out, dh0: [B, D] fp32; dA_log, d_dt_bias: [D] fp32)."""
+    refs = (x, dt, dy, dx, ddt, A_log, dA_log, states, dt_bias, d_dt_bias, dh_out, dh0, lengths)
+    raw = _filler().gated_scan_bwd(*refs, input_scale, workspace)
+    if raw is not None:
+        a = GatedScanBwdArgs.from_buffer_copy(raw)
+        a._refs = refs, workspace
+        return a
     who = "gated_scan_bwd_args"
     torch = _need_torch()
     B, L, D = x.shape
@@ -565,14 +577,14 @@ def gated_scan_bwd_args(x, dt, dy, dx, ddt, A_log, dA_log, states, dt_bias=None,
     _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias, dA_log=dA_log, d_dt_bias=d_dt_bias)
     _dense(who, (B, D), torch.float32, dh_out=dh_out, dh0=dh0)
     _dense(who, (B,), torch.int32, lengths=lengths)
-    _one_device(who, x, dt, dy, dx, ddt, A_log, dA_log, dt_bias, d_dt_bias, dh_out, dh0, lengths, states, workspace)
+    _one_device(who, *refs, workspace)
     s = [v for t in (x, dt, dy, dx, ddt) for v in t.stride()[:2]]
     a = GatedScanBwdArgs(B, L, D, _dtype_code(x), int(input_scale), _ptr(x), _ptr(dt), _ptr(dy), _ptr(dx), _ptr(ddt),
                          *s, _ptr(A_log), _ptr(dt_bias), _ptr(lengths), _ptr(states),
                          states.numel() * states.element_size() if states is not None else 0, _ptr(dh_out),
                          _ptr(dA_log), _ptr(d_dt_bias), _ptr(dh0), _ptr(workspace),
                          workspace.numel() * workspace.element_size() if workspace is not None else 0)
-    a._refs = (x, dt, dy, dx, ddt, A_log, dA_log, states, dt_bias, d_dt_bias, dh_out, dh0, lengths, workspace)
+    a._refs = refs, workspace
     return a
 
 
@@ -586,22 +598,22 @@ def hm_gated_scan_bwd(args: GatedScanBwdArgs, stream=None) -> None:
 
 def gated_step_args(x, dt, y, h, h_out, A_log, dt_bias=None, input_scale: int = 0) -> GatedStepArgs:
     """Fill an hm_gated_step_args (x, dt, y: [B, D]; h, h_out: [B, D] fp32, may be one tensor)."""
-    sh, ty, dev = x.shape, x.dtype, _current_device()
-    B, D = sh
-    f32 = _need_torch().float32
-    xs, ds, ys = x.stride(), dt.stride(), y.stride()
-    if not (x.get_device() == dev and _is(dt, sh, ty, dev) and _is(y, sh, ty, dev) and xs[1] == ds[1] == ys[1] == 1
-            and _is(h, sh, f32, dev) and h.is_contiguous() and _is(h_out, sh, f32, dev) and h_out.is_contiguous()
-            and _is(A_log, (D,), f32, dev) and A_log.is_contiguous()
-            and (dt_bias is None or _is(dt_bias, (D,), f32, dev) and dt_bias.is_contiguous())):
-        who = "gated_step_args"
-        _io(who, sh, x, x=x, dt=dt, y=y)
-        _dense(who, (D,), f32, A_log=A_log, dt_bias=dt_bias)
-        _dense(who, (B, D), f32, h=h, h_out=h_out)
-        _one_device(who, x, dt, y, h, h_out, A_log, dt_bias)
-    a = GatedStepArgs(B, D, _dtype_code(x), int(input_scale), x.data_ptr(), dt.data_ptr(), y.data_ptr(), xs[0], ds[0],
-                      ys[0], A_log.data_ptr(), _ptr(dt_bias), h.data_ptr(), h_out.data_ptr())
-    a._refs = (x, dt, y, h, h_out, A_log, dt_bias)
+    refs = (x, dt, y, h, h_out, A_log, dt_bias)
+    raw = _filler().gated_step(*refs, input_scale)
+    if raw is not None:
+        a = GatedStepArgs.from_buffer_copy(raw)
+        a._refs = refs
+        return a
+    who = "gated_step_args"
+    torch = _need_torch()
+    B, D = x.shape
+    _io(who, x.shape, x, x=x, dt=dt, y=y)
+    _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias)
+    _dense(who, (B, D), torch.float32, h=h, h_out=h_out)
+    _one_device(who, *refs)
+    a = GatedStepArgs(B, D, _dtype_code(x), int(input_scale), x.data_ptr(), dt.data_ptr(), y.data_ptr(), x.stride(0),
+                      dt.stride(0), y.stride(0), A_log.data_ptr(), _ptr(dt_bias), h.data_ptr(), h_out.data_ptr())
+    a._refs = refs
     return a
 
 
@@ -630,29 +642,24 @@ def _row_stride(t) -> int:
 def norm_gate_args(y, r, r_out, xn, gate=None, norm: int = 0, post: bool = True, eps: float = 1e-5,
                    alpha: float = 1.0, scale=None, post_w=None, post_b=None, pre_w=None, pre_b=None) -> NormGateArgs:
     """Fill an hm_norm_gate_args (y, gate, r, r_out, xn: [..., D]; parameters: [D] fp32)."""
-    sh, ty, dev = y.shape, y.dtype, _current_device()
-    D = sh[-1]
-    f32, vec = _need_torch().float32, (D,)
-    st, flat = [], len(sh) == 2
-    ok = y.get_device() == dev
-    for t in (y, gate, r, r_out, xn):
-        if t is None:
-            st.append(0)
-            continue
-        ts = t.stride()
-        st.append(ts[0] if flat else _row_stride(t))
-        ok = ok and ts[-1] == 1 and (t is y or _is(t, sh, ty, dev))
-    for t in (scale, post_w, post_b, pre_w, pre_b):
-        ok = ok and (t is None or _is(t, vec, f32, dev) and t.is_contiguous())
-    if not ok:
-        who = "norm_gate_args"
-        _io(who, sh, y, y=y, gate=gate, r=r, r_out=r_out, xn=xn)
-        _dense(who, vec, f32, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, pre_b=pre_b)
-        _one_device(who, y, gate, r, r_out, xn, scale, post_w, post_b, pre_w, pre_b)
+    refs = (y, r, r_out, xn, gate)
+    par = (scale, post_w, post_b, pre_w, pre_b)
+    raw = _filler().norm_gate(*refs, norm, post, eps, alpha, *par)
+    if raw is not None:
+        a = NormGateArgs.from_buffer_copy(raw)
+        a._refs = refs, par
+        return a
+    who = "norm_gate_args"
+    torch = _need_torch()
+    D = y.shape[-1]
+    _io(who, y.shape, y, y=y, gate=gate, r=r, r_out=r_out, xn=xn)
+    _dense(who, (D,), torch.float32, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, pre_b=pre_b)
+    _one_device(who, *refs, *par)
+    st = [_row_stride(t) for t in (y, gate, r, r_out, xn)]
     a = NormGateArgs(y.numel() // D if D else 0, D, _dtype_code(y), int(norm), int(post), eps, alpha, _ptr(y),
                      _ptr(gate), _ptr(r), _ptr(r_out), _ptr(xn), *st, _ptr(scale), _ptr(post_w), _ptr(post_b), _ptr(pre_w),
                      _ptr(pre_b))
-    a._refs = (y, gate, r, r_out, xn, scale, post_w, post_b, pre_w, pre_b)
+    a._refs = refs, par
     return a
 
 
@@ -666,14 +673,20 @@ def norm_gate_bwd_args(y, r_out, dr_out, dxn, dy, dr, gate=None, dgate=None, nor
                        workspace=None) -> NormGateBwdArgs:
     """Fill an hm_norm_gate_bwd_args (y, gate and the forward's r_out, the gradients of its
     outputs, the gradient buffers; rows [..., D] of one dtype, parameters and theirs [D] fp32)."""
+    refs = (y, r_out, dr_out, dxn, dy, dr, gate, dgate)
+    par = (scale, post_w, post_b, pre_w, dscale, dpost_w, dpost_b, dpre_w, dpre_b, workspace)
+    raw = _filler().norm_gate_bwd(*refs, norm, post, eps, alpha, *par)
+    if raw is not None:
+        a = NormGateBwdArgs.from_buffer_copy(raw)
+        a._refs = refs, par
+        return a
     torch = _need_torch()
     who = "norm_gate_bwd_args"
     D = y.shape[-1]
     _io(who, y.shape, y, y=y, gate=gate, r_out=r_out, dr_out=dr_out, dxn=dxn, dy=dy, dgate=dgate, dr=dr)
     _dense(who, (D,), torch.float32, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, dscale=dscale,
            dpost_w=dpost_w, dpost_b=dpost_b, dpre_w=dpre_w, dpre_b=dpre_b)
-    _one_device(who, y, gate, r_out, dr_out, dxn, dy, dgate, dr, scale, post_w, post_b, pre_w, dscale, dpost_w,
-                dpost_b, dpre_w, dpre_b, workspace)
+    _one_device(who, *refs, *par)
     a = NormGateBwdArgs(y.numel() // D if D else 0, D, _dtype_code(y), int(norm), int(post), eps, alpha, _ptr(y),
                         _ptr(gate), _ptr(r_out), _ptr(dr_out), _ptr(dxn), _ptr(dy), _ptr(dgate), _ptr(dr),
                         _row_stride(y), _row_stride(gate), _row_stride(r_out), _row_stride(dr_out), _row_stride(dxn),
@@ -681,8 +694,7 @@ def norm_gate_bwd_args(y, r_out, dr_out, dxn, dy, dr, gate=None, dgate=None, nor
                         _ptr(post_b), _ptr(pre_w), _ptr(dscale), _ptr(dpost_w), _ptr(dpost_b), _ptr(dpre_w),
                         _ptr(dpre_b), _ptr(workspace),
                         workspace.numel() * workspace.element_size() if workspace is not None else 0)
-    a._refs = (y, r_out, dr_out, dxn, dy, dr, gate, dgate, scale, post_w, post_b, pre_w, dscale, dpost_w, dpost_b,
-               dpre_w, dpre_b, workspace)
+    a._refs = refs, par
     return a
 
 
@@ -699,39 +711,39 @@ def rotary_args(q, k, q_out, k_out, rot: int = 0, base: float = 10000.0, layout:
                 mscale: float = 1.0, transpose: bool = False, positions=None, pos0: int = 0) -> RotaryArgs:
     """Fill an hm_rotary_args (q, q_out: [B, L, Hq, d]; k, k_out: [B, L, Hk, d] or None; rot = 0
     turns whole heads; positions: int64 [B, L], or [1, L] / [B, 1] shared along an axis of their own)."""
+    refs = (q, k, q_out, k_out, positions)
+    raw = _filler().rotary(q, k, q_out, k_out, rot, base, layout, scaling, factor, orig_len, beta_slow, beta_fast,
+                            mscale, transpose, positions, pos0)
+    if raw is not None:
+        a = RotaryArgs.from_buffer_copy(raw)
+        a._refs = refs
+        return a
     who = "rotary_args"
     torch = _need_torch()
-    sh, ty, dev = q.shape, q.dtype, _current_device()
-    B, L, Hq, d = sh
+    B, L, Hq, d = q.shape
     Hk = 0
     qs, os = q.stride(), q_out.stride()
     ks = ko = (0, 0, 0, 1)
-    ok = q.get_device() == dev and _is(q_out, sh, ty, dev) and qs[3] == os[3] == 1
-    if k is not None:
-        Hk = k.shape[2]
-        ks, ko = k.stride(), k_out.stride()
-        ok = ok and _is(k, (B, L, Hk, d), ty, dev) and _is(k_out, (B, L, Hk, d), ty, dev) and ks[3] == ko[3] == 1
+    if (k is None) != (k_out is None):
+        raise ValueError("%s: k and k_out come together" % who)
     pb = pt = 0
     if positions is not None:
         if positions.dtype is not torch.int64 or positions.dim() != 2 or positions.shape[0] not in (1, B) \
                 or positions.shape[1] not in (1, L):
             raise ValueError("%s: positions must be int64 [B or 1, L or 1]" % who)
-        pb, pt = positions.stride()
-        if positions.shape[0] == 1:
-            pb = 0
-        if positions.shape[1] == 1:
-            pt = 0
-        ok = ok and positions.get_device() == dev
-    if not ok:
-        _io(who, sh, q, q=q, q_out=q_out)
-        if k is not None:
-            _io(who, (B, L, Hk, d), q, k=k, k_out=k_out)
-        _one_device(who, q, k, q_out, k_out, positions)
+        pb = 0 if positions.shape[0] == 1 else positions.stride(0)
+        pt = 0 if positions.shape[1] == 1 else positions.stride(1)
+    _io(who, q.shape, q, q=q, q_out=q_out)
+    if k is not None:
+        Hk = k.shape[2]
+        ks, ko = k.stride(), k_out.stride()
+        _io(who, (B, L, Hk, d), q, k=k, k_out=k_out)
+    _one_device(who, *refs)
     a = RotaryArgs(B, L, Hq, Hk, d, int(rot) or d, _dtype_code(q), int(layout), int(scaling), int(transpose), _ptr(q),
                    _ptr(k), _ptr(q_out), _ptr(k_out), qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], os[0], os[1], os[2],
                    ko[0], ko[1], ko[2], _ptr(positions), pb, pt, int(pos0), base, factor, orig_len, beta_slow,
                    beta_fast, mscale)
-    a._refs = (q, k, q_out, k_out, positions)
+    a._refs = refs
     return a
 
 
@@ -756,7 +768,11 @@ def hm_selftest_wait_timeout(polls: int, stream=None) -> None:
 
 def alloc_workspace(nbytes: int, device=None):
     """A 256-byte-aligned device byte buffer of at least nbytes (torch allocation)."""
-    import torch
+    torch = _need_torch()
+    if device is None and torch.cuda.is_initialized():
+        buf = _filler().alloc(nbytes)
+        if buf is not None:
+            return buf
     n = max(int(nbytes), 1) + 256
     buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
     off = (-buf.data_ptr()) % 256

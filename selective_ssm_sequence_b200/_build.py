@@ -4,6 +4,9 @@ Every .cu under csrc/ is compiled separately (in parallel) and linked into one
 shared object with the CUDA runtime linked statically, so the library loads
 without a GPU (its symbols can be inspected on a build host) and needs only
 the driver on a GPU host.
+
+csrc/marshal.cpp becomes the extension module _marshal.so beside it, with the
+host compiler, against torch's headers and libraries.
 """
 from __future__ import annotations
 
@@ -18,6 +21,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libhm.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 OBJDIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -49,8 +53,31 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_marshal(force: bool = False) -> str:
+    """Compile csrc/marshal.cpp into _marshal.so; returns its path."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not force and not _stale(MARSHAL, [src, os.path.join(INCLUDE, "hm.h")]):
+        return MARSHAL
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = MARSHAL + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE,
+           "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", cuda, "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile csrc/*.cu and link libhm.so; returns its path."""
+    """Compile csrc/*.cu and link libhm.so, and build _marshal.so; returns the library's path."""
+    build_marshal(force)
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = _sources()
     hdrs = _headers()
