@@ -27,21 +27,6 @@ namespace {
 constexpr int kChunk = 64;   // tokens between two stored states
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-struct Gate {
-    float z, step, la, a, beta;
-};
-
-template <int SCALE>
-__device__ __forceinline__ Gate gate_of(float dt, float bias, float rate) {
-    Gate g;
-    g.z = dt + bias;
-    g.step = hm_softplus(g.z);
-    g.la = rate == 0.f ? 0.f : -g.step * rate;
-    g.a = expf(g.la);
-    g.beta = SCALE == HM_INPUT_PLAIN ? 1.f : SCALE == HM_INPUT_STEP ? g.step : sqrtf(-expm1f(2.f * g.la));
-    return g;
-}
-
 __device__ __forceinline__ int64_t clamped_len(const int32_t *lengths, int64_t b, int64_t L) {
     if (!lengths) return L;
     const int64_t n = lengths[b];
@@ -76,15 +61,20 @@ struct Gate2 {
     F2 z, e, step, la, a;             // z, step and la divided by ln 2
 };
 
-__device__ __forceinline__ ChanParams chan_params(const float *A_log, const float *dt_bias, int64_t c, int64_t D) {
-    const int64_t c1 = c + 1 < D ? c + 1 : c;
+__device__ __forceinline__ ChanParams params_of(float A0, float A1, float bias0, float bias1) {
     ChanParams p;
-    float r0 = c < D ? expf(A_log[c]) : 0.f, r1 = c < D ? expf(A_log[c1]) : 0.f;
+    float r0 = expf(A0), r1 = expf(A1);
     if (r0 > 3e38f) r0 = 3e38f;       // finite, so that a step of zero decays nothing
     if (r1 > 3e38f) r1 = 3e38f;
     p.nrate = pk(-r0, -r1);
-    p.bias = (dt_bias && c < D ? pk(dt_bias[c], dt_bias[c1]) : splat(0.f)) * splat(kLog2e);
+    p.bias = pk(bias0, bias1) * splat(kLog2e);
     return p;
+}
+__device__ __forceinline__ ChanParams chan_params(const float *A_log, const float *dt_bias, int64_t c, int64_t c1,
+                                                  int64_t D) {
+    if (c >= D) return params_of(0.f, 0.f, 0.f, 0.f);
+    if (c1 >= D) c1 = c;
+    return params_of(A_log[c], A_log[c1], dt_bias ? dt_bias[c] : 0.f, dt_bias ? dt_bias[c1] : 0.f);
 }
 
 // log2(1 + e) / e for 0 <= e <= 1: the degree-7 polynomial of least maximal
@@ -156,6 +146,45 @@ __device__ __forceinline__ void st_pair(__nv_bfloat16 *p, F2 v) {
     *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(u.x, u.y);
 }
 __device__ __forceinline__ void st_pair(float *p, F2 v) { *reinterpret_cast<float2 *>(p) = un(v); }
+
+// How a block's tiles come and go.  kTma: boxes by TMA, where rows start on
+// 16-byte boundaries.  kAsync: each thread's own elements by cp.async, ahead
+// by the same number of windows: fp32 rows at any offset, bf16 rows on 4-byte
+// boundaries.  kPlain: element loads (bf16 rows at odd offsets).
+enum Mode { kPlain = 0, kAsync = 1, kTma = 2 };
+
+// A lane's two channels: neighbours where they move as one word or box; else
+// 32 apart, so that a warp's single elements are neighbours in memory.
+template <typename T, int MODE>
+struct Lanes {
+    static constexpr bool kSplit = MODE == kPlain || (MODE == kAsync && sizeof(T) == 4);
+    static constexpr int kFirst = kSplit ? 1 : 2, kSecond = kSplit ? 32 : 1;     // 1st: lane * kFirst; 2nd: that + kSecond
+    static __device__ __forceinline__ Raw<T> load(const T *p) {
+        Raw<T> r;
+        if constexpr (kSplit) r.set(hm_ld(p, 0), hm_ld(p, 32));
+        else r.load(p);
+        return r;
+    }
+};
+
+__device__ __forceinline__ void cp_async4(void *dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// a thread's two elements of one row; in0: the first is there, in1: the second too
+template <typename T, int MODE>
+__device__ __forceinline__ void own_pair(T *dst, const T *src, bool in1) {
+    if constexpr (Lanes<T, MODE>::kSplit) {
+        cp_async4(dst, src, 4);
+        if (in1) cp_async4(dst + 32, src + 32, 4);
+    } else {
+        cp_async4(dst, src, in1 ? 4 : 2);
+    }
+}
 
 // ------------------------------------------------------------------ exchange
 
@@ -296,20 +325,21 @@ struct FwdArgs {
     int64_t nchunk;
 };
 
-// blockIdx.x = (sequence, column group, rank in cluster).  WIDE: tiles come by
-// TMA (two stages, so the window after the next is on its way while one is
-// computed) and each warp sends its run's results by TMA from a staging tile of
-// its own, except the run in which a sequence ends; else element loads and
-// stores.
+// blockIdx.x = (sequence, column group, rank in cluster).  With kTma and kAsync
+// the window after the next is on its way while one is computed (two stages);
+// with kTma each warp sends its run's results from a staging tile of its own,
+// except the run in which a sequence ends; else element stores.
 //
 // The run's composed maps live in registers (64 of them): 16 warps on an SM.
-template <typename T, int SCALE, bool WIDE, int W>
+template <typename T, int SCALE, int MODE, int W>
 __global__ void __launch_bounds__(W * 32, 16 / W)
 gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_constant__ CUtensorMap map_x,
                  const __grid_constant__ CUtensorMap map_y, FwdArgs f, int cluster, DevErr err) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[kStages], low[2], high[2];
     __shared__ int abort_flag;
+    constexpr bool WIDE = MODE == kTma;
+    constexpr int kFirst = Lanes<T, MODE>::kFirst, kSecond = Lanes<T, MODE>::kSecond;
     constexpr int kRows = W * kR;                  // tokens of a block's window
     constexpr int kTile = kRows * kCols;           // elements of a tile
     constexpr uint32_t kBytes = kTile * sizeof(T);
@@ -317,14 +347,14 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int64_t unit = blockIdx.x / cluster, b = unit / f.groups;
-    const int64_t c0 = (unit - b * f.groups) * kCols, c = c0 + 2 * lane;
-    const bool in0 = c < p.D, in1 = c + 1 < p.D;
+    const int64_t c0 = (unit - b * f.groups) * kCols, c = c0 + kFirst * lane;
+    const bool in0 = c < p.D, in1 = c + kSecond < p.D;
     const int n = (int)clamped_len(p.lengths, b, p.L);          // L is at most 2^30
     const int window = cluster * kRows;
     const int iters = (int)(((unsigned)n + (unsigned)window - 1u) / (unsigned)window);
     T *stage0 = reinterpret_cast<T *>(smem), *out = stage0 + 2 * kStages * kTile + warp * kR * kCols;
     Exchange x;
-    x.agg = reinterpret_cast<Map2 *>(smem + (WIDE ? (2 * kStages + 1) * kBytes : 0));
+    x.agg = reinterpret_cast<Map2 *>(smem + (WIDE ? 2 * kStages + 1 : MODE == kAsync ? 2 * kStages : 0) * kBytes);
     x.ctas = x.agg + 2 * W * 32;
     x.low = low;
     x.high = high;
@@ -351,12 +381,25 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     if (WIDE && threadIdx.x == 0)
         for (int s = 0; s < kStages && s < iters; ++s) fetch(s);
 
-    const ChanParams par = chan_params(p.A_log, p.dt_bias, c, p.D);
+    const ChanParams par = chan_params(p.A_log, p.dt_bias, c, c + kSecond, p.D);
     // the state at the start of the window; between windows of a cluster that at this block's runs
     F2 h = splat(0.f);
-    if (p.h0) h = pk(in0 ? p.h0[b * p.D + c] : 0.f, in1 ? p.h0[b * p.D + c + 1] : 0.f);
+    if (p.h0) h = pk(in0 ? p.h0[b * p.D + c] : 0.f, in1 ? p.h0[b * p.D + c + kSecond] : 0.f);
     const T *dtp = (const T *)p.dt + b * p.dt_stride_b + c, *xp = (const T *)p.x + b * p.x_stride_b + c;
     T *yp = (T *)p.y + b * p.y_stride_b + c;
+    auto fetch_own = [&](int it) {                 // this thread's elements of window `it`
+        const int t = it * window + rank * kRows + warp * kR, m = in0 ? min(n - t, kR) : 0;
+        T *dst = stage0 + (it % kStages) * 2 * kTile + warp * kR * kCols + kFirst * lane;
+        const T *pd = dtp + t * p.dt_stride_t, *px = xp + t * p.x_stride_t;
+#pragma unroll 4
+        for (int i = 0; i < m; ++i, dst += kCols, pd += p.dt_stride_t, px += p.x_stride_t) {
+            own_pair<T, MODE>(dst, pd, in1);
+            own_pair<T, MODE>(dst + kTile, px, in1);
+        }
+        cp_async_commit();
+    };
+    if (MODE == kAsync)
+        for (int s = 0; s < kStages; ++s) fetch_own(s);
 
     int t0 = rank * kRows + warp * kR;             // the run's first token
     for (int it = 0; it < iters; ++it, t0 += window) {
@@ -364,14 +407,15 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         Map2 run[kR];                              // the run's composition up to each token
         Map2 all = {splat(1.f), splat(0.f)};
         if (WIDE) wait_bar(&full[it % kStages], (it / kStages) & 1, &abort_flag, err, 0);
+        if (MODE == kAsync) cp_async_wait<kStages - 1>();
         if (m > 0) {
             Raw<T> dv[kR], xv[kR];
-            const T *sdt = stage0 + (it % kStages) * 2 * kTile + (warp * kR) * kCols + 2 * lane;
-            if (WIDE) {
+            const T *sdt = stage0 + (it % kStages) * 2 * kTile + (warp * kR) * kCols + kFirst * lane;
+            if (MODE != kPlain) {
 #pragma unroll
                 for (int i = 0; i < kR; ++i) {
-                    dv[i].load(sdt + i * kCols);
-                    xv[i].load(sdt + kTile + i * kCols);
+                    dv[i] = Lanes<T, MODE>::load(sdt + i * kCols);
+                    xv[i] = Lanes<T, MODE>::load(sdt + kTile + i * kCols);
                 }
             } else {
 #pragma unroll
@@ -380,7 +424,7 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
                     if (i < m) {
                         const int64_t od = (int64_t)(t0 + i) * p.dt_stride_t, ox = (int64_t)(t0 + i) * p.x_stride_t;
                         if (in0) d0 = hm_ld(dtp, od), x0 = hm_ld(xp, ox);
-                        if (in1) d1 = hm_ld(dtp, od + 1), x1 = hm_ld(xp, ox + 1);
+                        if (in1) d1 = hm_ld(dtp, od + kSecond), x1 = hm_ld(xp, ox + kSecond);
                     }
                     dv[i].set(d0, d1);
                     xv[i].set(x0, x1);
@@ -408,12 +452,13 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         if (cluster > 1 && it > 0) h = finish_window(x, it, h);
         __syncthreads();         // maps written; this window's tiles, and the window before's maps, read
         if (WIDE && threadIdx.x == 0 && it + kStages < iters) fetch(it + kStages);
+        if (MODE == kAsync) fetch_own(it + kStages);
         const F2 hin = enter_run<W>(x, it, warp, h);
         if (m > 0) {
             if (p.states && t0 % kChunk == 0 && in0) {
                 float *st = (float *)p.states + (b * f.nchunk + t0 / kChunk) * p.D + c;
                 st[0] = un(hin).x;
-                if (in1) st[1] = un(hin).y;
+                if (in1) st[kSecond] = un(hin).y;
             }
             if (WIDE && p.y && m == kR) {
                 if (lane == 0) tc::bulk_wait_read_all();         // the last run's results have left
@@ -433,8 +478,12 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
                 for (int i = 0; i < kR; ++i) {
                     if (i < m) {
                         const float2 v = un(apply(run[i], hin));
-                        if (in0) hm_st(yr, 0, v.x);
-                        if (in1) hm_st(yr, 1, v.y);
+                        if (MODE == kAsync && kSecond == 1 && in1) {
+                            st_pair(yr, pk(v.x, v.y));
+                        } else {
+                            if (in0) hm_st(yr, 0, v.x);
+                            if (in1) hm_st(yr, kSecond, v.y);
+                        }
                     }
                     yr += p.y_stride_t;
                 }
@@ -442,12 +491,13 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         }
     }
     if (cluster > 1 && iters > 0) h = finish_window(x, iters, h);
+    if (WIDE && lane == 0) tc::bulk_wait_all();
+    if (cluster > 1) cluster_sync();               // no block leaves while others may still write to it,
+    else __syncthreads();                          // and h_out may be the h0 that all have now read
     if (p.h_out && rank == 0 && warp == 0) {
         if (in0) p.h_out[b * p.D + c] = un(h).x;
-        if (in1) p.h_out[b * p.D + c + 1] = un(h).y;
+        if (in1) p.h_out[b * p.D + c + kSecond] = un(h).y;
     }
-    if (WIDE && lane == 0) tc::bulk_wait_all();
-    if (cluster > 1) cluster_sync();               // no block leaves while others may still write to it
 }
 
 // ------------------------------------------------------------------ backward
@@ -480,7 +530,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 //
 // Registers hold a, h_{t-1}, Delta, sigmoid(z) (and beta) of 8 tokens: 16
 // warps on an SM; x and dy are read again from shared memory.
-template <typename T, int SCALE, bool WIDE>
+template <typename T, int SCALE, int MODE>
 __global__ void __launch_bounds__(kWb * 32, 2)
 gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_constant__ CUtensorMap map_x,
                  const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_dx,
@@ -488,14 +538,16 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[kBwdStages], low[2], high[2];
     __shared__ int abort_flag;
+    constexpr bool WIDE = MODE == kTma;
+    constexpr int kFirst = Lanes<T, MODE>::kFirst, kSecond = Lanes<T, MODE>::kSecond;
     constexpr int kTile = kChunk * kCols;
     constexpr uint32_t kBytes = kTile * sizeof(T);
     const hm_gated_scan_bwd_args &p = f.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = cluster > 1 ? (int)cluster_rank() : 0;
     const int64_t unit = blockIdx.x / cluster, b = unit / f.groups;
-    const int64_t c0 = (unit - b * f.groups) * kCols, c = c0 + 2 * lane;
-    const bool in0 = c < p.D, in1 = c + 1 < p.D;
+    const int64_t c0 = (unit - b * f.groups) * kCols, c = c0 + kFirst * lane;
+    const bool in0 = c < p.D, in1 = c + kSecond < p.D;
     const int n = (int)clamped_len(p.lengths, b, p.L);
     const int chunks = (n + kChunk - 1) / kChunk, iters = (chunks + cluster - 1) / cluster;
     T *stage0 = reinterpret_cast<T *>(smem);
@@ -532,12 +584,26 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     if (WIDE && threadIdx.x == 0)
         for (int s = 0; s < kBwdStages && s < iters; ++s) fetch(s);
 
-    const ChanParams par = chan_params(p.A_log, p.dt_bias, c, p.D);
+    const ChanParams par = chan_params(p.A_log, p.dt_bias, c, c + kSecond, p.D);
     F2 carry = splat(0.f);         // gradient entering the window from behind (between windows: this block's part)
-    if (p.dh_out) carry = pk(in0 ? p.dh_out[b * p.D + c] : 0.f, in1 ? p.dh_out[b * p.D + c + 1] : 0.f);
+    if (p.dh_out) carry = pk(in0 ? p.dh_out[b * p.D + c] : 0.f, in1 ? p.dh_out[b * p.D + c + kSecond] : 0.f);
     const T *dtp = (const T *)p.dt + b * p.dt_stride_b + c, *xp = (const T *)p.x + b * p.x_stride_b + c;
     const T *dyp = (const T *)p.dy + b * p.dy_stride_b + c;
     T *dxp = (T *)p.dx + b * p.dx_stride_b + c, *ddtp = (T *)p.ddt + b * p.ddt_stride_b + c;
+    auto fetch_own = [&](int it) {
+        const int t = chunk_of(it) * kChunk + warp * kRb, m = in0 && t >= 0 ? min(n - t, kRb) : 0;
+        T *dst = stage0 + it % kBwdStages * 3 * kTile + warp * kRb * kCols + kFirst * lane;
+        const T *pd = dtp + t * p.dt_stride_t, *px = xp + t * p.x_stride_t, *py = dyp + t * p.dy_stride_t;
+#pragma unroll 4
+        for (int i = 0; i < m; ++i, dst += kCols) {
+            own_pair<T, MODE>(dst, pd + i * p.dt_stride_t, in1);
+            own_pair<T, MODE>(dst + kTile, px + i * p.x_stride_t, in1);
+            own_pair<T, MODE>(dst + 2 * kTile, py + i * p.dy_stride_t, in1);
+        }
+        cp_async_commit();
+    };
+    if (MODE == kAsync)
+        for (int s = 0; s < kBwdStages - 1; ++s) fetch_own(s);
     F2 sumA = splat(0.f), sumb = splat(0.f);
     int stage = 0;
     uint32_t phase = 0;
@@ -545,40 +611,41 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     for (int it = 0; it < iters; ++it) {
         const int chunk = chunk_of(it), t0 = chunk * kChunk + warp * kRb;
         const int m = chunk < 0 ? 0 : min(max(n - t0, 0), kRb);
-        T *tile = stage0 + stage * 3 * kTile + (warp * kRb) * kCols + 2 * lane;
+        T *tile = stage0 + stage * 3 * kTile + (warp * kRb) * kCols + kFirst * lane;
         F2 a[kRb], h[kRb], step[kRb], sig[kRb], beta[kRb];
         Map2 mf = {splat(1.f), splat(0.f)}, mr = {splat(1.f), splat(0.f)};
         F2 hin = splat(0.f);
         if (chunk >= 0 && in0) {
             const float *st = (const float *)p.states + (b * f.nchunk + chunk) * p.D + c;
-            hin = pk(st[0], in1 ? st[1] : 0.f);
+            hin = pk(st[0], in1 ? st[kSecond] : 0.f);
         }
         if (WIDE && chunk >= 0) wait_bar(&full[stage], phase, &abort_flag, err, 3);
+        if (MODE == kAsync) {
+            fetch_own(it + kBwdStages - 1);                // over what this thread used one window ago
+            cp_async_wait<kBwdStages - 1>();
+        }
         if (m > 0) {
             // a thread's own elements of the tile: element loads put them there, and tokens behind
             // the end become a step of zero, no input, no gradient of their own
-            if (!WIDE || m < kRb) {
-                for (int i = WIDE ? m : 0; i < kRb; ++i) {
+            if (MODE == kPlain || m < kRb) {
+                for (int i = MODE == kPlain ? 0 : m; i < kRb; ++i) {
                     float d0 = -INFINITY, d1 = -INFINITY, x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
                     if (i < m) {
                         const int64_t t = t0 + i, od = t * p.dt_stride_t, ox = t * p.x_stride_t, oy = t * p.dy_stride_t;
                         if (in0) d0 = hm_ld(dtp, od), x0 = hm_ld(xp, ox), y0 = hm_ld(dyp, oy);
-                        if (in1) d1 = hm_ld(dtp, od + 1), x1 = hm_ld(xp, ox + 1), y1 = hm_ld(dyp, oy + 1);
+                        if (in1) d1 = hm_ld(dtp, od + kSecond), x1 = hm_ld(xp, ox + kSecond), y1 = hm_ld(dyp, oy + kSecond);
                     }
-                    Raw<T> r;
-                    r.set(d0, d1);
-                    r.store(tile + i * kCols);
-                    r.set(x0, x1);
-                    r.store(tile + kTile + i * kCols);
-                    r.set(y0, y1);
-                    r.store(tile + 2 * kTile + i * kCols);
+                    T *q = tile + i * kCols;
+                    hm_st(q, 0, d0), hm_st(q, kSecond, d1);
+                    hm_st(q, kTile, x0), hm_st(q, kTile + kSecond, x1);
+                    hm_st(q, 2 * kTile, y0), hm_st(q, 2 * kTile + kSecond, y1);
                 }
             }
             Raw<T> dv[kRb], xr[kRb];
 #pragma unroll
             for (int i = 0; i < kRb; ++i) {
-                dv[i].load(tile + i * kCols);
-                xr[i].load(tile + kTile + i * kCols);
+                dv[i] = Lanes<T, MODE>::load(tile + i * kCols);
+                xr[i] = Lanes<T, MODE>::load(tile + kTile + i * kCols);
             }
             F2 sum = splat(0.f);
 #pragma unroll
@@ -602,8 +669,7 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
             }
 #pragma unroll
             for (int i = kRb - 1; i >= 0; --i) {
-                Raw<T> dy;
-                dy.load(tile + 2 * kTile + i * kCols);
+                const Raw<T> dy = Lanes<T, MODE>::load(tile + 2 * kTile + i * kCols);
                 mr.B = a[i] * (dy.pair() + mr.B);
             }
             mf.A = mr.A = ex2(sum);
@@ -626,9 +692,8 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
             }
 #pragma unroll
             for (int i = kRb - 1; i >= 0; --i) {
-                Raw<T> rx, rdy;
-                rx.load(tile + kTile + i * kCols);
-                rdy.load(tile + 2 * kTile + i * kCols);
+                const Raw<T> rx = Lanes<T, MODE>::load(tile + kTile + i * kCols);
+                const Raw<T> rdy = Lanes<T, MODE>::load(tile + 2 * kTile + i * kCols);
                 const F2 xv = rx.pair(), g = rdy.pair() + cin;
                 cin = a[i] * g;
                 F2 dla = cin * h[i];
@@ -645,8 +710,19 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
                 sumb = sumb + dz;
                 const F2 dx = SCALE == HM_INPUT_PLAIN ? g
                               : SCALE == HM_INPUT_STEP ? g * (step[i] * splat(kLn2)) : g * beta[i];
-                st_pair(tile + i * kCols, dz);
-                st_pair(tile + kTile + i * kCols, dx);
+                if (WIDE) {
+                    st_pair(tile + i * kCols, dz);
+                    st_pair(tile + kTile + i * kCols, dx);
+                } else if (i < m) {
+                    T *oz = ddtp + (int64_t)(t0 + i) * p.ddt_stride_t, *ox = dxp + (int64_t)(t0 + i) * p.dx_stride_t;
+                    if (MODE == kAsync && kSecond == 1 && in1) {
+                        st_pair(oz, dz);
+                        st_pair(ox, dx);
+                    } else {
+                        if (in0) hm_st(oz, 0, un(dz).x), hm_st(ox, 0, un(dx).x);
+                        if (in1) hm_st(oz, kSecond, un(dz).y), hm_st(ox, kSecond, un(dx).y);
+                    }
+                }
             }
             if (WIDE && m == kRb) {
                 tc::fence_proxy_async_smem();
@@ -657,7 +733,8 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
                     tc::tma_store_3d(&map_dx, row + kTile, (int)c0, t0, (int)b);
                     tc::bulk_commit();
                 }
-            } else {             // a thread's own elements, one by one
+            } else if (WIDE) {   // a thread's own elements, one by one
+                tc::fence_proxy_async_smem();              // before a later box lands where they are
 #pragma unroll 1
                 for (int i = 0; i < m; ++i) {
                     T *oz = ddtp + (int64_t)(t0 + i) * p.ddt_stride_t, *ox = dxp + (int64_t)(t0 + i) * p.dx_stride_t;
@@ -670,10 +747,6 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         if (++stage == kBwdStages) stage = 0, phase ^= 1;
     }
     if (cluster > 1 && iters > 0) carry = finish_window(x, iters, carry);
-    if (p.dh0 && rank == 0 && warp == 0) {
-        if (in0) p.dh0[b * p.D + c] = un(carry).x;
-        if (in1) p.dh0[b * p.D + c + 1] = un(carry).y;
-    }
     // the block's share of the parameter gradients, its warps' in order
     if (WIDE && lane == 0) tc::bulk_wait_all();
     __syncthreads();
@@ -688,9 +761,13 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         sumA = sumA * par.nrate * splat(kLn2); // log a = -rate Delta, Delta from its base-2 exponent
         float *o = f.part + (b * cluster + rank) * 2 * p.D + c;
         if (in0) o[0] = un(sumA).x, o[p.D] = un(sumb).x;
-        if (in1) o[1] = un(sumA).y, o[p.D + 1] = un(sumb).y;
+        if (in1) o[kSecond] = un(sumA).y, o[p.D + kSecond] = un(sumb).y;
     }
-    if (cluster > 1) cluster_sync();
+    if (cluster > 1) cluster_sync();                       // all have read dh_out, which dh0 may be
+    if (p.dh0 && rank == 0 && warp == 0) {
+        if (in0) p.dh0[b * p.D + c] = un(carry).x;
+        if (in1) p.dh0[b * p.D + c + kSecond] = un(carry).y;
+    }
 }
 
 // the blocks' shares summed in order: 8 threads per channel, each a stride of
@@ -719,16 +796,53 @@ __global__ void __launch_bounds__(256) gated_sum_kernel(const float *part, int64
     }
 }
 
-template <typename T, int SCALE>
+// One token.  N = 16 bytes of x per thread where rows and widths allow (322 x
+// 8128 fp32: 20 -> 12 us against single elements), else one element; bytes
+// bound it, or with few sequences the launch.
+template <typename T, int SCALE, int N>
 __global__ void __launch_bounds__(256) gated_step_kernel(hm_gated_step_args p) {
-    const int64_t n = p.B * p.D;
+    const int64_t groups = p.D / N, n = p.B * groups;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t b = i / p.D, c = i - b * p.D;
-        const Gate g = gate_of<SCALE>(hm_ld((const T *)p.dt, b * p.dt_stride + c), p.dt_bias ? p.dt_bias[c] : 0.f,
-                                      expf(p.A_log[c]));
-        const float h = fmaf(g.a, p.h[i], g.beta * hm_ld((const T *)p.x, b * p.x_stride + c));
-        p.h_out[i] = h;
-        hm_st((T *)p.y, b * p.y_stride + c, h);
+        const int64_t b = n < (1LL << 31) ? (int64_t)((uint32_t)i / (uint32_t)groups) : i / groups;
+        const int64_t c = (i - b * groups) * N;
+        const T *dt = (const T *)p.dt + b * p.dt_stride + c, *x = (const T *)p.x + b * p.x_stride + c;
+        T *y = (T *)p.y + b * p.y_stride + c;
+        const float *hi = p.h + b * p.D + c;
+        float *ho = p.h_out + b * p.D + c;
+        if constexpr (N == 1) {
+            const ChanParams par = chan_params(p.A_log, p.dt_bias, c, c, p.D);
+            const Gate2 g = gates2(splat(hm_ld(dt, 0)), par);
+            const float v = un(fma(g.a, splat(hi[0]), input2<SCALE>(g, splat(hm_ld(x, 0))))).x;
+            ho[0] = v;
+            hm_st(y, 0, v);
+        } else {
+            union Words {
+                uint4 w;
+                Raw<T> r[16 / sizeof(Raw<T>)];
+                __device__ Words() {}
+            } wd, wx, wy;
+            wd.w = __ldcs(reinterpret_cast<const uint4 *>(dt));
+            wx.w = __ldcs(reinterpret_cast<const uint4 *>(x));
+            float4 h[N / 4], A[N / 4], bias[N / 4];
+#pragma unroll
+            for (int k = 0; k < N / 4; ++k) {
+                h[k] = __ldcs(reinterpret_cast<const float4 *>(hi) + k);
+                A[k] = __ldg(reinterpret_cast<const float4 *>(p.A_log + c) + k);
+                bias[k] = p.dt_bias ? __ldg(reinterpret_cast<const float4 *>(p.dt_bias + c) + k) : float4{0.f, 0.f, 0.f, 0.f};
+            }
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) {
+                const float *Ak = &A[k / 2].x + k % 2 * 2, *bk = &bias[k / 2].x + k % 2 * 2;
+                float *hk = &h[k / 2].x + k % 2 * 2;
+                const Gate2 g = gates2(wd.r[k].pair(), params_of(Ak[0], Ak[1], bk[0], bk[1]));
+                const float2 v = un(fma(g.a, pk(hk[0], hk[1]), input2<SCALE>(g, wx.r[k].pair())));
+                wy.r[k].set(v.x, v.y);
+                hk[0] = v.x, hk[1] = v.y;
+            }
+            *reinterpret_cast<uint4 *>(y) = wy.w;
+#pragma unroll
+            for (int k = 0; k < N / 4; ++k) reinterpret_cast<float4 *>(ho)[k] = h[k];
+        }
     }
 }
 
@@ -914,6 +1028,11 @@ bool tma_rows(const void *p, size_t es, int64_t B, int64_t L, int64_t sb, int64_
     return aligned_to(p, 16) && (L <= 1 || st * (int64_t)es % 16 == 0) && (B <= 1 || sb * (int64_t)es % 16 == 0);
 }
 
+// rows whose elements cp.async can fetch: 4-byte words of two bf16, or single fp32 elements
+bool word_rows(const void *p, size_t es, int64_t B, int64_t L, int64_t sb, int64_t st) {
+    return es == 4 || (aligned_to(p, 4) && (L <= 1 || st % 2 == 0) && (B <= 1 || sb % 2 == 0));
+}
+
 template <typename K, typename... A>
 cudaError_t launch_cluster(K kernel, int64_t units, Split sp, size_t smem, cudaStream_t s, A... args) {
     cudaError_t e = tc::ensure_smem_limit(kernel, (int)smem);
@@ -955,17 +1074,28 @@ extern "C" hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t 
                                  tile_map(&my, a->io_dtype, a->y, a->B, a->L, a->D, a->y_stride_b, a->y_stride_t, kR))) &&
                       tile_map(&mdt, a->io_dtype, a->dt, a->B, a->L, a->D, a->dt_stride_b, a->dt_stride_t, rows) &&
                       tile_map(&mx, a->io_dtype, a->x, a->B, a->L, a->D, a->x_stride_b, a->x_stride_t, rows);
+    const bool words = word_rows(a->x, es, a->B, a->L, a->x_stride_b, a->x_stride_t) &&
+                       word_rows(a->dt, es, a->B, a->L, a->dt_stride_b, a->dt_stride_t) &&
+                       (!a->y || word_rows(a->y, es, a->B, a->L, a->y_stride_b, a->y_stride_t));
     const DevErr err{device_error_word()};
     const cudaError_t e = by_type(a->io_dtype, a->input_scale, [&](auto *t, auto sc) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int S = decltype(sc)::value;
-        const size_t smem = (wide ? (size_t)(2 * kStages + 1) * rows * kCols * sizeof(T) : 0) +
-                            (size_t)2 * (sp.warps + sp.cluster) * 32 * sizeof(Map2);
-        auto go = [&](auto kernel) {
+        auto go = [&](auto kernel, int tiles) {
+            const size_t smem = (size_t)tiles * rows * kCols * sizeof(T) +
+                                (size_t)2 * (sp.warps + sp.cluster) * 32 * sizeof(Map2);
             return launch_cluster(kernel, units, sp, smem, (cudaStream_t)stream, mdt, mx, my, f, sp.cluster, err);
         };
-        if (sp.warps == 8) return wide ? go(gated_fwd_kernel<T, S, true, 8>) : go(gated_fwd_kernel<T, S, false, 8>);
-        return wide ? go(gated_fwd_kernel<T, S, true, 4>) : go(gated_fwd_kernel<T, S, false, 4>);
+        auto by_mode = [&](auto w) {
+            constexpr int W = decltype(w)::value;
+            if (wide) return go(gated_fwd_kernel<T, S, kTma, W>, 2 * kStages + 1);
+            if (words) return go(gated_fwd_kernel<T, S, kAsync, W>, 2 * kStages);
+            if constexpr (sizeof(T) == 2) return go(gated_fwd_kernel<T, S, kPlain, W>, 0);
+            return cudaErrorInvalidValue;          // not reached: fp32 rows are words
+        };
+        if constexpr (sizeof(T) == 2)
+            if (sp.warps == 8) return by_mode(std::integral_constant<int, 8>());
+        return by_mode(std::integral_constant<int, 4>());
     });
     return e == cudaSuccess ? HM_OK : fail_args(HM_ERR_CUDA, "gated_scan_fwd launch: %s", cudaGetErrorString(e));
 }
@@ -1003,10 +1133,12 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
                   {a->dy, a->dy_stride_b, a->dy_stride_t, kChunk, {}},
                   {a->dx, a->dx_stride_b, a->dx_stride_t, kRb, {}},
                   {a->ddt, a->ddt_stride_b, a->ddt_stride_t, kRb, {}}};
-        bool wide = a->L > 0;
-        for (auto &r : t)
+        bool wide = a->L > 0, words = true;
+        for (auto &r : t) {
+            words = words && word_rows(r.p, es, a->B, a->L, r.sb, r.st);
             wide = wide && tma_rows(r.p, es, a->B, a->L, r.sb, r.st) &&
                    tile_map(&r.map, a->io_dtype, r.p, a->B, a->L, a->D, r.sb, r.st, r.rows);
+        }
         const DevErr err{device_error_word()};
         e = by_type(a->io_dtype, a->input_scale, [&](auto *tp, auto sc) {
             using T = std::remove_pointer_t<decltype(tp)>;
@@ -1017,7 +1149,10 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
                 return launch_cluster(kernel, units, sp, smem, s, t[0].map, t[1].map, t[2].map, t[3].map, t[4].map, f,
                                       sp.cluster, err);
             };
-            return wide ? go(gated_bwd_kernel<T, S, true>) : go(gated_bwd_kernel<T, S, false>);
+            if (wide) return go(gated_bwd_kernel<T, S, kTma>);
+            if (words) return go(gated_bwd_kernel<T, S, kAsync>);
+            if constexpr (sizeof(T) == 2) return go(gated_bwd_kernel<T, S, kPlain>);
+            return cudaErrorInvalidValue;          // not reached: fp32 rows are words
         });
     }
     if (e == cudaSuccess) {
@@ -1044,11 +1179,19 @@ extern "C" hm_status hm_gated_scan_step(const hm_gated_step_args *a, hm_stream_t
     HM_TRY(check_f32(w, "h_out", a->h_out, a->B > 0));
     if (a->B == 0) return HM_OK;
     if (a->y == a->x || a->y == a->dt) return fail_args(HM_ERR_INVALID_ARG, "%s: y must not be x or dt", w);
-    const int64_t blocks = (a->B * a->D + 255) / 256;
+    const int wide = (int)(16 / es);          // elements of a 16-byte piece
+    bool vec = a->D % wide == 0;
+    const int64_t strides[] = {a->x_stride, a->dt_stride, a->y_stride};
+    for (const int64_t st : strides) vec = vec && (a->B == 1 || st % wide == 0);
+    const void *ptrs[] = {a->x, a->dt, a->y, a->h, a->h_out, a->A_log, a->dt_bias};
+    for (const void *q : ptrs) vec = vec && aligned_to(q, 16);
+    const int64_t blocks = (a->B * (vec ? a->D / wide : a->D) + 255) / 256;
+    const unsigned grid = (unsigned)(blocks < 148 * 32 ? blocks : 148 * 32);
     const cudaError_t e = by_type(a->io_dtype, a->input_scale, [&](auto *t, auto sc) {
         using T = std::remove_pointer_t<decltype(t)>;
-        gated_step_kernel<T, decltype(sc)::value>
-            <<<(unsigned)(blocks < 148 * 32 ? blocks : 148 * 32), 256, 0, (cudaStream_t)stream>>>(*a);
+        constexpr int S = decltype(sc)::value, N = 16 / (int)sizeof(T);
+        if (vec) gated_step_kernel<T, S, N><<<grid, 256, 0, (cudaStream_t)stream>>>(*a);
+        else gated_step_kernel<T, S, 1><<<grid, 256, 0, (cudaStream_t)stream>>>(*a);
         count_launches(1);
         return cudaGetLastError();
     });

@@ -179,18 +179,19 @@ __device__ __forceinline__ float sum2(F2 f) {
     return u.x + u.y;
 }
 
-// Sums over the team (a warp, or with BLOCK the whole block of up to 16
-// warps) of one or of four values; every thread gets them, always added in
+// Sums over the team (TEAM lanes of a warp: 8, 16 or 32; or with TEAM = 0 the
+// whole block of up to 16 warps) of one or of four values; every thread gets them, always added in
 // the same order.  `red` alternates between two buffers, so one barrier per
 // call is enough: a call's reads are separated from the next-but-one call's
 // writes by the next call's barrier.
 constexpr int kMaxWarps = 16;
 __device__ __forceinline__ float xor_add(float v, int o) { return v + __shfl_xor_sync(0xffffffffu, v, o); }
 
-template <bool BLOCK>
+template <int TEAM>
 __device__ __forceinline__ float team_sum(float v, float (*red)[kMaxWarps][4], int &turn) {
-    v = warp_sum(v);
-    if (!BLOCK) return v;
+#pragma unroll
+    for (int o = (TEAM ? TEAM : 32) / 2; o > 0; o /= 2) v = xor_add(v, o);
+    if (TEAM) return v;
     float (*r)[4] = red[turn & 1];
     ++turn;
     const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
@@ -202,16 +203,22 @@ __device__ __forceinline__ float team_sum(float v, float (*red)[kMaxWarps][4], i
 
 // The four values travel together: each exchange halves what a lane carries,
 // so that a quarter of the warp ends with each sum.
-template <bool BLOCK>
+template <int TEAM>
 __device__ __forceinline__ float4 team_sum4(float4 q, float (*red)[kMaxWarps][4], int &turn) {
     const int lane = threadIdx.x & 31;
+    if (TEAM == 8 || TEAM == 16) {
+#pragma unroll
+        for (int o = TEAM / 2; o > 0; o /= 2)
+            q = make_float4(xor_add(q.x, o), xor_add(q.y, o), xor_add(q.z, o), xor_add(q.w, o));
+        return q;
+    }
     const bool b16 = (lane & 16) != 0, b8 = (lane & 8) != 0;
     const float s0 = b16 ? q.x : q.z, s1 = b16 ? q.y : q.w;
     const float k0 = (b16 ? q.z : q.x) + __shfl_xor_sync(0xffffffffu, s0, 16);
     const float k1 = (b16 ? q.w : q.y) + __shfl_xor_sync(0xffffffffu, s1, 16);
     float v = (b8 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, b8 ? k0 : k1, 8);
     v = xor_add(xor_add(xor_add(v, 4), 2), 1);          // lanes 8 i .. 8 i + 7: the i-th value
-    if (BLOCK) {
+    if (TEAM == 0) {
         float (*r)[4] = red[turn & 1];
         ++turn;
         const int nw = blockDim.x >> 5, w = lane & 7, i = lane >> 3;
@@ -236,15 +243,19 @@ __device__ __forceinline__ F2 sigmoid(F2 x) {
     return pk(z.x, z.y);
 }
 
-// One row per team: a warp of four (BLOCK false), or the block.
-template <typename T, bool VEC, int NV, bool BLOCK, bool LAYER>
-__global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_norm_gate_args p) {
+// One row per team: a block of 128 threads has several, or is one itself.  Teams
+// of less than a warp (D <= 128) stay to the end when they have no row, with no
+// columns either, since their warp's shuffles need them.
+template <typename T, bool VEC, int NV, int TEAM, bool LAYER>
+__global__ void __launch_bounds__(TEAM ? 128 : 512, 1) norm_gate_fwd_kernel(hm_norm_gate_args p) {
     __shared__ float red[2][kMaxWarps][4];
     int turn = 0;
-    const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nthr = BLOCK ? blockDim.x : 32, D = (int)p.D;
-    const float inv = 1.f / (float)D;
-    const int64_t row = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= p.rows) return;         // whole teams
+    constexpr int kTeam = TEAM ? TEAM : 1;
+    const int tid = TEAM ? threadIdx.x % kTeam : threadIdx.x, nthr = TEAM ? TEAM : blockDim.x;
+    const float inv = 1.f / (float)p.D;
+    const int64_t row = TEAM ? (int64_t)blockIdx.x * (128 / kTeam) + threadIdx.x / kTeam : (int64_t)blockIdx.x;
+    if (row >= p.rows && (TEAM == 0 || TEAM == 32)) return;         // whole teams
+    const int D = row < p.rows ? (int)p.D : 0;
     Raw8<T> ry[NV], rg[NV], rr[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -263,7 +274,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_
 #pragma unroll
                 for (int j = 0; j < kP; ++j) v = v + f[j];
             }
-            mean = team_sum<BLOCK>(sum2(v), red, turn) * inv;
+            mean = team_sum<TEAM>(sum2(v), red, turn) * inv;
             v = splat(0.f);
         }
 #pragma unroll
@@ -276,7 +287,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_
                 v = fma(d, d, v);
             }
         }
-        rstd = rsqrtf(team_sum<BLOCK>(sum2(v), red, turn) * inv + p.eps);
+        rstd = rsqrtf(team_sum<TEAM>(sum2(v), red, turn) * inv + p.eps);
     }
     F2 r[NV][kP], v = splat(0.f);
 #pragma unroll
@@ -306,7 +317,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_
         if (p.r_out) store8<VEC>((T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D, r[k]);
     }
     if (!p.xn) return;
-    float q = team_sum<BLOCK>(sum2(v), red, turn);
+    float q = team_sum<TEAM>(sum2(v), red, turn);
     mean = 0.f;
     if (LAYER) {
         mean = q * inv;
@@ -320,7 +331,7 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_
                 v = fma(d, d, v);
             }
         }
-        q = team_sum<BLOCK>(sum2(v), red, turn);
+        q = team_sum<TEAM>(sum2(v), red, turn);
     }
     rstd = rsqrtf(q * inv + p.eps);
 #pragma unroll
@@ -334,22 +345,25 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 128, 1) norm_gate_fwd_kernel(hm_
     }
 }
 
-// A team per row (the block, or with BLOCK false each warp), rows `teams`
-// apart, the next row's loads under way while one is worked on.  FULL: the
-// common case that every row array is there and y is normalised, known to the
-// compiler.
-// part[(team * 5 + i) * D + c]: the team's share of dscale, dpost_w, dpost_b,
-// dpre_w, dpre_b.
-template <typename T, bool VEC, int NV, bool BLOCK, bool LAYER, bool FULL, int THREADS>
+// A team per row: the block, or TEAM lanes of a warp; each team's rows lie
+// `stride` apart, the next one's loads under way while one is worked on (the
+// teams of a warp go on together; one behind the last row has no columns).
+// FULL: the common case that every row array is there and y is normalised,
+// known to the compiler.
+// part[(w * 5 + i) * D + c]: dscale, dpost_w, dpost_b, dpre_w, dpre_b as the
+// w-th block, or warp, has summed them.
+template <typename T, bool VEC, int NV, int TEAM, bool LAYER, bool FULL, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1)
 norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
     __shared__ float red[2][kMaxWarps][4];
     int turn = 0;
+    constexpr int kTeam = TEAM ? TEAM : 1, kRows = TEAM ? 32 / kTeam : 1;       // rows of a warp, or block
     const bool gate = FULL || p.gate, post = FULL || p.post, pre = FULL || p.dxn;
-    const int tid = BLOCK ? threadIdx.x : threadIdx.x & 31, nthr = BLOCK ? blockDim.x : 32, D = (int)p.D;
-    const float inv = 1.f / (float)D;
-    const int64_t team = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int64_t teams = BLOCK ? (int64_t)gridDim.x : (int64_t)gridDim.x * 8;
+    const int tid = TEAM ? threadIdx.x % kTeam : threadIdx.x, nthr = TEAM ? TEAM : blockDim.x;
+    const float inv = 1.f / (float)p.D;
+    const int64_t unit = TEAM ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+    const int64_t stride = (TEAM ? (int64_t)gridDim.x * 8 : (int64_t)gridDim.x) * kRows;
+    const int64_t first = unit * kRows, mine = TEAM ? threadIdx.x % 32 / kTeam : 0;
     F2 acc[5][NV][kP];
 #pragma unroll
     for (int i = 0; i < 5; ++i)
@@ -359,6 +373,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
             for (int j = 0; j < kP; ++j) acc[i][k][j] = splat(0.f);
     Raw8<T> ry[NV], rg[NV], rr[NV], rd[NV], re[NV];
     auto fetch = [&](int64_t row) {
+        const int D = row < p.rows ? (int)p.D : 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             ry[k] = load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
@@ -371,8 +386,10 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
             else rd[k].zero();
         }
     };
-    if (team < p.rows) fetch(team);
-    for (int64_t row = team; row < p.rows; row += teams) {
+    if (first < p.rows) fetch(first + mine);
+    for (int64_t base = first; base < p.rows; base += stride) {
+        const int64_t row = base + mine;
+        const int D = row < p.rows ? (int)p.D : 0;
         F2 y[NV][kP], r[NV][kP], d[NV][kP], e[NV][kP], g[NV][kP];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -381,7 +398,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
             if (pre) rr[k].get(r[k]), re[k].get(e[k]);
             rd[k].get(d[k]);
         }
-        if (row + teams < p.rows) fetch(row + teams);
+        if (base + stride < p.rows) fetch(row + stride);
         // y and r_out less their means
         F2 v0 = splat(0.f), v1 = splat(0.f);
         if (LAYER) {
@@ -392,7 +409,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
                     v0 = v0 + y[k][j];
                     if (pre) v1 = v1 + r[k][j];
                 }
-            const float4 v = team_sum4<BLOCK>(make_float4(sum2(v0), sum2(v1), 0.f, 0.f), red, turn);
+            const float4 v = team_sum4<TEAM>(make_float4(sum2(v0), sum2(v1), 0.f, 0.f), red, turn);
             const F2 my = splat(post ? -v.x * inv : 0.f), mr = splat(-v.y * inv);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
@@ -426,7 +443,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
 #pragma unroll
             for (int j = 0; j < kP; ++j) v0 = fma(y[k][j], y[k][j], v0);
         }
-        const float4 v = team_sum4<BLOCK>(make_float4(sum2(v0), sum2(v1), sum2(v2), sum2(v3)), red, turn);
+        const float4 v = team_sum4<TEAM>(make_float4(sum2(v0), sum2(v1), sum2(v2), sum2(v3)), red, turn);
         const float rsy = post ? rsqrtf(v.x * inv + p.eps) : 1.f, rsr = rsqrtf(v.y * inv + p.eps);
         const float r0 = -rsr * (v.z * inv), r1 = -rsr * (rsr * (v.w * inv));
         v0 = v1 = splat(0.f);
@@ -493,11 +510,11 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
         if (post) {
             float y0 = 0.f, y1;
             if (LAYER) {
-                const float4 q = team_sum4<BLOCK>(make_float4(sum2(v0), sum2(v1), 0.f, 0.f), red, turn);
+                const float4 q = team_sum4<TEAM>(make_float4(sum2(v0), sum2(v1), 0.f, 0.f), red, turn);
                 y0 = -q.x * inv;
                 y1 = -q.y * inv;
             } else {
-                y1 = -team_sum<BLOCK>(sum2(v1), red, turn) * inv;
+                y1 = -team_sum<TEAM>(sum2(v1), red, turn) * inv;
             }
 #pragma unroll
             for (int k = 0; k < NV; ++k)
@@ -510,6 +527,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) store8<VEC>((T *)p.dy + row * p.dy_stride, k, tid, nthr, D, d[k]);
     }
+    const int D = (int)p.D;
 #pragma unroll
     for (int i = 0; i < 5; ++i)
 #pragma unroll
@@ -517,8 +535,11 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
                 const int c = col_of<VEC>(k, j, tid, nthr);
-                const float2 u = un(acc[i][k][j / 2]);
-                if (c < D) part[(team * 5 + i) * D + c] = j & 1 ? u.y : u.x;
+                float v = j & 1 ? un(acc[i][k][j / 2]).y : un(acc[i][k][j / 2]).x;
+                if (TEAM)
+#pragma unroll
+                    for (int o = 16; o >= kTeam; o /= 2) v = xor_add(v, o);     // the warp's teams
+                if (c < D && mine == 0) part[(unit * 5 + i) * D + c] = v;
             }
 }
 
@@ -584,7 +605,7 @@ bool wide(const Row &r, size_t es) {
 }
 
 struct Team {
-    int nthr, nv;        // threads that share a row (32: a warp), pieces of 8 columns per thread
+    int nthr, nv;        // threads that share a row (up to 32: of one warp), pieces of 8 columns per thread
     int blocks;          // backward
 };
 
@@ -592,10 +613,12 @@ struct Team {
 // columns over 2 warps took 117 us for 32768 rows, over 1 warp of 8 pieces 134,
 // over 4 warps 121, over 8 157.  More warps for wider rows, and for so few
 // rows that these would leave most of the GPU idle.
+// Rows of up to 64 or 128 columns share a warp (320719 rows of 64, bf16: 117 -> 37 us).
 // Rows that are read element by element get a block with as few pieces as it can.
 Team fwd_team(int64_t rows, int64_t D, size_t es, bool vec) {
     const int pieces = (int)((D + 32 * kE - 1) / (32 * kE)), most = !vec ? (D > 8192 ? 4 : D > 4096 ? 2 : 1) : es == 2 || D > 8192 ? 4 : 2;
     int warps = 1;
+    if (vec && D <= 128) return {D <= 64 ? 8 : 16, 1, 0};
     while ((pieces + warps - 1) / warps > most) warps *= 2;
     while (warps < 16 && (pieces + warps - 1) / warps > 1 && rows * warps * 2 <= 148 * 16) warps *= 2;
     int nv = 1;
@@ -605,16 +628,19 @@ Team fwd_team(int64_t rows, int64_t D, size_t es, bool vec) {
 
 // Backward: as many threads as there are pieces in a row, up to 512; blocks
 // (or warps) to fill the SMs once at 512 threads each.
+// Rows of up to 64 or 128 columns share a warp.
 Team bwd_team(int64_t rows, int64_t D) {
     const int pieces = (int)((D + 32 * kE - 1) / (32 * kE));
     int nv = 1;
     while (nv * 16 < pieces) nv *= 2;
     const int warps = (pieces + nv - 1) / nv;
-    const int64_t most = warps == 1 ? 148 * 2 : 148 * (16 / warps), need = warps == 1 ? (rows + 7) / 8 : rows;
-    return {warps * 32, nv, (int)(need < most ? need : most)};
+    const int lanes = D <= 64 ? 8 : D <= 128 ? 16 : 32, of_block = 8 * 32 / lanes;     // rows of a block of warps
+    const int64_t most = warps == 1 ? 148 * 2 : 148 * (16 / warps);
+    const int64_t need = warps == 1 ? (rows + of_block - 1) / of_block : rows;
+    return {warps == 1 ? lanes : warps * 32, nv, (int)(need < most ? need : most)};
 }
 
-int64_t bwd_shares(const Team &t) { return t.nthr == 32 ? t.blocks * 8LL : t.blocks; }
+int64_t bwd_shares(const Team &t) { return t.nthr <= 32 ? t.blocks * 8LL : t.blocks; }
 
 }  // namespace
 
@@ -654,20 +680,25 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
     if (a->r_out == a->xn) return fail_args(HM_ERR_INVALID_ARG, "%s: r_out and xn are the same array", w);
     const Team t = fwd_team(a->rows, a->D, es, vec);
     const bool block = t.nthr > 32 || !vec;
-    const int64_t blocks = block ? a->rows : (a->rows + 3) / 4;
+    const int of_block = block ? 1 : 128 / t.nthr;         // rows
+    const int64_t blocks = (a->rows + of_block - 1) / of_block;
     if (blocks > 0x7fffffffLL) return fail_args(HM_ERR_UNSUPPORTED, "%s: too many rows", w);
     cudaStream_t s = (cudaStream_t)stream;
-#define HM_FWD(T, V, N, B, Y) norm_gate_fwd_kernel<T, V, N, B, Y><<<(unsigned)blocks, B ? t.nthr : 128, 0, s>>>(*a)
+#define HM_FWD(T, V, N, B, Y) norm_gate_fwd_kernel<T, V, N, B, Y><<<(unsigned)blocks, B ? 128 : t.nthr, 0, s>>>(*a)
 #define HM_FWD_Y(T, V, N, B) (a->norm == HM_NORM_LAYER ? HM_FWD(T, V, N, B, true) : HM_FWD(T, V, N, B, false))
-#define HM_FWD_B(T, N) (block ? HM_FWD_Y(T, true, N, true) : HM_FWD_Y(T, true, N, false))
-#define HM_FWD_S(T) (t.nv == 1 ? HM_FWD_Y(T, false, 1, true) : t.nv == 2 ? HM_FWD_Y(T, false, 2, true) : HM_FWD_Y(T, false, 4, true))
+#define HM_FWD_B(T, N) (block ? HM_FWD_Y(T, true, N, 0) : HM_FWD_Y(T, true, N, 32))
+#define HM_FWD_S(T) (t.nv == 1 ? HM_FWD_Y(T, false, 1, 0) : t.nv == 2 ? HM_FWD_Y(T, false, 2, 0) : HM_FWD_Y(T, false, 4, 0))
     if (a->io_dtype == HM_BF16) {
         if (!vec) HM_FWD_S(__nv_bfloat16);
+        else if (t.nthr == 8) HM_FWD_Y(__nv_bfloat16, true, 1, 8);
+        else if (t.nthr == 16) HM_FWD_Y(__nv_bfloat16, true, 1, 16);
         else if (t.nv == 1) HM_FWD_B(__nv_bfloat16, 1);
         else if (t.nv == 2) HM_FWD_B(__nv_bfloat16, 2);
         else HM_FWD_B(__nv_bfloat16, 4);
     } else {
         if (!vec) HM_FWD_S(float);
+        else if (t.nthr == 8) HM_FWD_Y(float, true, 1, 8);
+        else if (t.nthr == 16) HM_FWD_Y(float, true, 1, 16);
         else if (t.nv == 1) HM_FWD_B(float, 1);
         else if (t.nv == 2) HM_FWD_B(float, 2);
         else HM_FWD_B(float, 4);
@@ -714,20 +745,21 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     if (need > 0 && (!a->workspace || a->workspace_bytes < need || ((uintptr_t)a->workspace & 255) != 0))
         return fail_args(HM_ERR_INVALID_ARG, "%s: workspace of %zu bytes, 256-byte aligned, is needed", w, need);
     const Team t = bwd_team(a->rows, a->D);
-    const bool block = t.nthr > 32;
     const int64_t shares = bwd_shares(t);
     cudaStream_t s = (cudaStream_t)stream;
     float *part = (float *)a->workspace;
     if (t.blocks > 0) {
         const bool full = a->gate && a->post && a->dxn && a->dr_out && a->dr;
 #define HM_BWD_F(T, V, N, B, Y, Z)                                                                          \
-    (V && full ? norm_gate_bwd_kernel<T, V, N, B, Y, V, Z><<<t.blocks, B ? t.nthr : 256, 0, s>>>(*a, part)      \
-               : norm_gate_bwd_kernel<T, V, N, B, Y, false, Z><<<t.blocks, B ? t.nthr : 256, 0, s>>>(*a, part))
+    (V && full ? norm_gate_bwd_kernel<T, V, N, B, Y, V, Z><<<t.blocks, B ? 256 : t.nthr, 0, s>>>(*a, part)      \
+               : norm_gate_bwd_kernel<T, V, N, B, Y, false, Z><<<t.blocks, B ? 256 : t.nthr, 0, s>>>(*a, part))
 #define HM_BWD(T, V, N, B, Z) (a->norm == HM_NORM_LAYER ? HM_BWD_F(T, V, N, B, true, Z) : HM_BWD_F(T, V, N, B, false, Z))
 #define HM_BWD_N(T, V)                                                                                      \
-    (!block ? HM_BWD(T, V, 1, false, 256)                                                                   \
-            : t.nv == 1 ? (t.nthr <= 256 ? HM_BWD(T, V, 1, true, 256) : HM_BWD(T, V, 1, true, 512))         \
-            : t.nv == 2 ? HM_BWD(T, V, 2, true, 512) : HM_BWD(T, V, 4, true, 512))
+    (t.nthr == 8 ? HM_BWD(T, V, 1, 8, 256)                                                                  \
+     : t.nthr == 16 ? HM_BWD(T, V, 1, 16, 256)                                                              \
+     : t.nthr == 32 ? HM_BWD(T, V, 1, 32, 256)                                                              \
+     : t.nv == 1 ? (t.nthr <= 256 ? HM_BWD(T, V, 1, 0, 256) : HM_BWD(T, V, 1, 0, 512))                      \
+     : t.nv == 2 ? HM_BWD(T, V, 2, 0, 512) : HM_BWD(T, V, 4, 0, 512))
         if (a->io_dtype == HM_BF16) vec ? HM_BWD_N(__nv_bfloat16, true) : HM_BWD_N(__nv_bfloat16, false);
         else vec ? HM_BWD_N(float, true) : HM_BWD_N(float, false);
 #undef HM_BWD
