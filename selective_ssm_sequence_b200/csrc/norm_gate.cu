@@ -11,7 +11,10 @@
 // thread keeps the five parameter gradients of its columns in registers over
 // all its rows (40 of them for 8 columns), so there a block shares a row; the
 // blocks' shares are summed by a second, small kernel in a fixed order.
+#include <type_traits>
+
 #include "packed.cuh"
+#include "tc_common.cuh"
 
 namespace hm {
 
@@ -543,26 +546,302 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
             }
 }
 
+// Sums of N = 2, 4 or 8 values over a block of up to MW warps; every thread gets
+// them, always added in the same order.  Each exchange halves what a lane
+// carries, so N values cost N + 3 shuffles or so in place of 5 N.  `red` as in
+// team_sum.
+template <int N, int MW>
+__device__ __forceinline__ void block_sums(float (&v)[N], float (*red)[MW][8], int &turn) {
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    constexpr int kLanes = 32 / N;         // lanes that end with the same value
+#pragma unroll
+    for (int n = N / 2, o = 16; n >= 1; n /= 2, o /= 2) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    float s = v[0];
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o /= 2) s = xor_add(s, o);
+    float (*r)[8] = red[turn & 1];
+    ++turn;
+    const int i = lane / kLanes, w = lane % kLanes;
+    if (w == 0) r[threadIdx.x >> 5][i] = s;
+    __syncthreads();
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < MW; k += kLanes)
+        if (k + w < nw) s += r[k + w][i];
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o /= 2) s = xor_add(s, o);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __shfl_sync(0xffffffffu, s, k * kLanes);
+}
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes) {
+    const unsigned d = (unsigned)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+}
+
+// The common case of the backward (every row array there, y normalised, rows on
+// 16-byte boundaries), for bf16 rows of 512 to 4096 columns: R rows at a time.
+// Their sums share the exchanges and barriers, and the rows wait in shared
+// memory (each thread's own columns, by cp.async, the next R behind them), which
+// leaves the registers to the parameter gradients.  8192 x 2048 layer norms:
+// 91 us against 95 with a row in registers, 260 x 2752 17.6 against 23.8; fp32
+// rows gain nothing (184 against 160) and narrow ones neither (65536 x 264: 128
+// against 122).  715 instructions per warp and row, half of the issue slots
+// used: latency at 16 warps per SM bounds it.
+//
+// FAR: rows of 4096 to 8192 columns of either type, one at a time over 1024
+// threads, whose registers have no room for rows nor sums: the parameter
+// gradients lie in shared memory, and a row is read again, from L2, in each of
+// the three passes.
+template <typename T, bool LAYER, int R, int THREADS, bool FAR>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1)
+norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
+    extern __shared__ __align__(16) uint4 tile[];
+    __shared__ float red[2][THREADS / 32][8];
+    float4 *sums = reinterpret_cast<float4 *>(tile);       // FAR: [5][2][threads]
+    constexpr int Q = kE * (int)sizeof(T) / 16;
+    int turn = 0;
+    const int tid = threadIdx.x, nthr = blockDim.x, D = (int)p.D, c = tid * kE;
+    const bool live = c < D;
+    const float inv = 1.f / (float)D;
+    const int64_t groups = (p.rows + R - 1) / R;
+    F2 acc[FAR ? 1 : 5][kP];
+    if (FAR) {
+#pragma unroll
+        for (int i = 0; i < 10; ++i) sums[i * nthr + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+#pragma unroll
+            for (int j = 0; j < kP; ++j) acc[i][j] = splat(0.f);
+    }
+    // the i-th parameter's gradient += u * w
+    auto add = [&](int i, const F2 *u, const F2 *w) {
+        if constexpr (FAR) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 *q = &sums[(i * 2 + h) * nthr + tid];
+                const float4 o = *q;
+                const float2 a = un(fma(u[2 * h], w[2 * h], pk(o.x, o.y))), b = un(fma(u[2 * h + 1], w[2 * h + 1], pk(o.z, o.w)));
+                *q = make_float4(a.x, a.y, b.x, b.y);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kP; ++j) acc[i][j] = fma(u[j], w[j], acc[i][j]);
+        }
+    };
+    const F2 one[kP] = {splat(1.f), splat(1.f), splat(1.f), splat(1.f)};
+    const T *const base[5] = {(const T *)p.y, (const T *)p.gate, (const T *)p.r_out, (const T *)p.dr_out, (const T *)p.dxn};
+    const int64_t strides[5] = {p.y_stride, p.gate_stride, p.r_out_stride, p.dr_out_stride, p.dxn_stride};
+    auto fetch = [&](int64_t g, int s) {
+        if (FAR) return;
+        if (g < groups) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int64_t row = g * R + k;
+                const bool on = live && row < p.rows;          // else zeros
+#pragma unroll
+                for (int a = 0; a < 5; ++a) {
+                    const T *src = base[a] + (on ? row * strides[a] + c : 0);
+#pragma unroll
+                    for (int q = 0; q < Q; ++q)
+                        cp_async16(&tile[(((s * R + k) * 5 + a) * Q + q) * nthr + tid], src + q * (16 / sizeof(T)),
+                                   on ? 16 : 0);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(blockIdx.x, 0);
+    fetch((int64_t)blockIdx.x + gridDim.x, 1);
+    int s = 0;
+    for (int64_t g = blockIdx.x; g < groups; g += gridDim.x, s ^= 1) {
+        if (!FAR) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        auto get = [&](int k, int a, F2 *f) {
+            if (FAR) {
+                Raw8<T> r;
+                if (live) r.load(base[a] + g * strides[a] + c);
+                else r.zero();
+                r.get(f);
+                return;
+            }
+            const uint4 *q = &tile[((s * R + k) * 5 + a) * Q * nthr + tid];
+            Raw8<T> r;
+            if constexpr (Q == 1) {
+                r.w = q[0];
+            } else {
+                r.a = *reinterpret_cast<const float4 *>(q);
+                r.b = *reinterpret_cast<const float4 *>(q + nthr);
+            }
+            r.get(f);
+        };
+        float my[R] = {}, mr[R] = {};                          // less the means
+        if (LAYER) {
+            float v[2 * R];
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                F2 y[kP], r[kP];
+                get(k, 0, y);
+                get(k, 2, r);
+                v[2 * k] = sum2((y[0] + y[1]) + (y[2] + y[3]));
+                v[2 * k + 1] = sum2((r[0] + r[1]) + (r[2] + r[3]));
+            }
+            block_sums(v, red, turn);
+#pragma unroll
+            for (int k = 0; k < R; ++k) my[k] = -v[2 * k] * inv, mr[k] = -v[2 * k + 1] * inv;
+        }
+        float rsy[R], rsr[R], r0[R], r1[R];
+        {
+            float v[4 * R] = {};
+            if (live) {
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    F2 y[kP], r[kP], e[kP], v0 = splat(0.f), v1 = v0, v2 = v0, v3 = v0;
+                    get(k, 0, y);
+                    get(k, 2, r);
+                    get(k, 4, e);
+                    times<true>(e, p.pre_w, 0, tid, nthr, D);
+#pragma unroll
+                    for (int j = 0; j < kP; ++j) {
+                        const F2 yc = LAYER ? y[j] + splat(my[k]) : y[j], rc = LAYER ? r[j] + splat(mr[k]) : r[j];
+                        v0 = fma(yc, yc, v0);
+                        v1 = fma(rc, rc, v1);
+                        if (LAYER) v2 = v2 + e[j];
+                        v3 = fma(e[j], rc, v3);
+                    }
+                    v[4 * k] = sum2(v0), v[4 * k + 1] = sum2(v1), v[4 * k + 2] = sum2(v2), v[4 * k + 3] = sum2(v3);
+                }
+            }
+            block_sums(v, red, turn);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                rsy[k] = rsqrtf(v[4 * k] * inv + p.eps);
+                rsr[k] = rsqrtf(v[4 * k + 1] * inv + p.eps);
+                r0[k] = -rsr[k] * (v[4 * k + 2] * inv);
+                r1[k] = -rsr[k] * (rsr[k] * (v[4 * k + 3] * inv));
+            }
+        }
+        F2 dn[R][kP];
+        float v[2 * R] = {};
+        if (live) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int64_t row = g * R + k;
+                F2 d[kP], e[kP], u[kP];
+                get(k, 2, u);
+                get(k, 3, d);
+                get(k, 4, e);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    u[j] = (LAYER ? u[j] + splat(mr[k]) : u[j]) * splat(rsr[k]);
+                    d[j] = fma(u[j], splat(r1[k]), LAYER ? d[j] + splat(r0[k]) : d[j]);
+                }
+                add(3, e, u);
+                add(4, e, one);
+                times<true>(e, p.pre_w, 0, tid, nthr, D);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) d[j] = fma(e[j], splat(rsr[k]), d[j]);
+                if (row < p.rows) store8<true>((T *)p.dr + row * p.dr_stride, 0, tid, nthr, D, d);
+                F2 y[kP], n[kP], gt[kP];
+                get(k, 0, y);
+                get(k, 1, gt);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    y[j] = (LAYER ? y[j] + splat(my[k]) : y[j]) * splat(rsy[k]);
+                    n[j] = y[j];
+                    d[j] = d[j] * splat(p.alpha);
+                    dn[k][j] = d[j];
+                }
+                times<true>(n, p.post_w, 0, tid, nthr, D);
+                plus<true>(n, p.post_b, 0, tid, nthr, D);
+                times<true>(dn[k], p.scale, 0, tid, nthr, D);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    const F2 sg = sigmoid(gt[j]), si = gt[j] * sg;
+                    gt[j] = dn[k][j] * n[j] * fma(si, splat(1.f) - sg, sg);       // SiLU'(g) = sg + si (1 - sg)
+                    n[j] = n[j] * si;
+                    dn[k][j] = dn[k][j] * si;
+                }
+                add(0, d, n);
+                add(1, dn[k], y);
+                add(2, dn[k], one);
+                if (row < p.rows) store8<true>((T *)p.dgate + row * p.dgate_stride, 0, tid, nthr, D, gt);
+                times<true>(dn[k], p.post_w, 0, tid, nthr, D);
+                F2 v0 = splat(0.f), v1 = v0;
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    if (LAYER) v0 = v0 + dn[k][j];
+                    v1 = fma(dn[k][j], y[j], v1);
+                }
+                v[2 * k] = sum2(v1);
+                v[2 * k + 1] = sum2(v0);
+            }
+        }
+        block_sums(v, red, turn);
+        if (live) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int64_t row = g * R + k;
+                const F2 y1 = splat(-v[2 * k] * inv), y0 = splat(-v[2 * k + 1] * inv);
+                F2 y[kP];
+                get(k, 0, y);
+#pragma unroll
+                for (int j = 0; j < kP; ++j) {
+                    y[j] = (LAYER ? y[j] + splat(my[k]) : y[j]) * splat(rsy[k]);
+                    const F2 q = fma(y[j], y1, dn[k][j]);
+                    y[j] = splat(rsy[k]) * (LAYER ? q + y0 : q);
+                }
+                if (row < p.rows) store8<true>((T *)p.dy + row * p.dy_stride, 0, tid, nthr, D, y);
+            }
+        }
+        fetch(g + 2 * (int64_t)gridDim.x, s);              // over what this thread has read
+    }
+    if (!FAR) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!live) return;
+    if constexpr (FAR) {
+#pragma unroll
+        for (int i = 0; i < 10; ++i)
+            *reinterpret_cast<float4 *>(part + ((int64_t)blockIdx.x * 5 + i / 2) * D + c + i % 2 * 4) = sums[i * nthr + tid];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < (FAR ? 0 : 5); ++i)
+#pragma unroll
+        for (int j = 0; j < kP; ++j)
+            *reinterpret_cast<float2 *>(part + ((int64_t)blockIdx.x * 5 + i) * D + c + 2 * j) = un(acc[i][j]);
+}
+
 struct GradPtrs {
     float *out[5];
 };
 
 // the teams' shares summed in a fixed order; a block of threads per 32 columns
-// and parameter, 32 rows of it walking the shares
-__global__ void __launch_bounds__(1024) norm_gate_sum_kernel(const float *part, int teams, int D, GradPtrs g) {
-    __shared__ float s[32][33];
+// and parameter, ROWS rows of it walking the shares
+template <int ROWS>
+__global__ void __launch_bounds__(32 * ROWS) norm_gate_sum_kernel(const float *part, int teams, int D, GradPtrs g) {
+    __shared__ float s[ROWS][33];
     float *out = g.out[blockIdx.y];
     if (!out) return;
     const int c = blockIdx.x * 32 + threadIdx.x;
     float v = 0.f;
     if (c < D) {
-#pragma unroll 4
-        for (int b = threadIdx.y; b < teams; b += 32) v += part[((int64_t)b * 5 + blockIdx.y) * D + c];
+#pragma unroll 10
+        for (int b = threadIdx.y; b < teams; b += ROWS) v += part[((int64_t)b * 5 + blockIdx.y) * D + c];
     }
     s[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
-    v = warp_sum(s[threadIdx.x][threadIdx.y]);     // a warp per column now
-    if (threadIdx.x == 0 && blockIdx.x * 32 + threadIdx.y < D) out[blockIdx.x * 32 + threadIdx.y] = v;
+    if (threadIdx.y == 0 && c < D) {
+#pragma unroll
+        for (int i = 1; i < ROWS; ++i) v += s[i][threadIdx.x];
+        out[c] = v;
+    }
 }
 
 // ------------------------------------------------------------------ host
@@ -745,11 +1024,31 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     if (need > 0 && (!a->workspace || a->workspace_bytes < need || ((uintptr_t)a->workspace & 255) != 0))
         return fail_args(HM_ERR_INVALID_ARG, "%s: workspace of %zu bytes, 256-byte aligned, is needed", w, need);
     const Team t = bwd_team(a->rows, a->D);
-    const int64_t shares = bwd_shares(t);
+    int64_t shares = bwd_shares(t);
     cudaStream_t s = (cudaStream_t)stream;
     float *part = (float *)a->workspace;
     if (t.blocks > 0) {
         const bool full = a->gate && a->post && a->dxn && a->dr_out && a->dr;
+        const bool far = vec && full && a->D > 4096 && a->D <= 8192;
+        const bool tiled = far || (vec && full && es == 2 && a->D > 512 && t.nv == 1);
+        auto rows_kernel = [&](auto kernel, int R) {
+            const int nthr = far ? (int)((a->D / kE + 31) / 32 * 32) : t.nthr;
+            const size_t smem = far ? (size_t)10 * sizeof(float4) * nthr : (size_t)2 * R * 5 * kE * es * nthr;
+            const cudaError_t e = tc::ensure_smem_limit(kernel, (int)smem);
+            if (e != cudaSuccess) return e;
+            const int64_t groups = (a->rows + R - 1) / R;
+            shares = groups < t.blocks ? groups : t.blocks;
+            kernel<<<(unsigned)shares, nthr, smem, s>>>(*a, part);
+            return cudaGetLastError();
+        };
+        auto rows_by = [&](auto layer) {
+            constexpr bool Y = decltype(layer)::value;
+            if (far)
+                return es == 2 ? rows_kernel(norm_gate_bwd_rows_kernel<__nv_bfloat16, Y, 1, 1024, true>, 1)
+                               : rows_kernel(norm_gate_bwd_rows_kernel<float, Y, 1, 1024, true>, 1);
+            return t.nthr <= 256 ? rows_kernel(norm_gate_bwd_rows_kernel<__nv_bfloat16, Y, 2, 256, false>, 2)
+                                 : rows_kernel(norm_gate_bwd_rows_kernel<__nv_bfloat16, Y, 2, 512, false>, 2);
+        };
 #define HM_BWD_F(T, V, N, B, Y, Z)                                                                          \
     (V && full ? norm_gate_bwd_kernel<T, V, N, B, Y, V, Z><<<t.blocks, B ? 256 : t.nthr, 0, s>>>(*a, part)      \
                : norm_gate_bwd_kernel<T, V, N, B, Y, false, Z><<<t.blocks, B ? 256 : t.nthr, 0, s>>>(*a, part))
@@ -760,7 +1059,10 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
      : t.nthr == 32 ? HM_BWD(T, V, 1, 32, 256)                                                              \
      : t.nv == 1 ? (t.nthr <= 256 ? HM_BWD(T, V, 1, 0, 256) : HM_BWD(T, V, 1, 0, 512))                      \
      : t.nv == 2 ? HM_BWD(T, V, 2, 0, 512) : HM_BWD(T, V, 4, 0, 512))
-        if (a->io_dtype == HM_BF16) vec ? HM_BWD_N(__nv_bfloat16, true) : HM_BWD_N(__nv_bfloat16, false);
+        if (tiled) {
+            const cudaError_t e = a->norm == HM_NORM_LAYER ? rows_by(std::true_type()) : rows_by(std::false_type());
+            if (e != cudaSuccess) return fail_args(HM_ERR_CUDA, "%s launch: %s", w, cudaGetErrorString(e));
+        } else if (a->io_dtype == HM_BF16) vec ? HM_BWD_N(__nv_bfloat16, true) : HM_BWD_N(__nv_bfloat16, false);
         else vec ? HM_BWD_N(float, true) : HM_BWD_N(float, false);
 #undef HM_BWD
 #undef HM_BWD_F
@@ -771,7 +1073,10 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     if (e == cudaSuccess) {
         // without dxn the pre-norm's parameters had no part in the loss: their shares are zero
         const GradPtrs g = {{a->dscale, a->dpost_w, a->dpost_b, a->dpre_w, a->dpre_b}};
-        norm_gate_sum_kernel<<<dim3((unsigned)((a->D + 31) / 32), 5), dim3(32, 32), 0, s>>>(part, (int)shares, (int)a->D, g);
+        // more rows of threads for many shares (2368 of 64 columns: 41.8 us a call against 47.7 with 16)
+        const dim3 grid((unsigned)((a->D + 31) / 32), 5);
+        if (shares > 512) norm_gate_sum_kernel<32><<<grid, dim3(32, 32), 0, s>>>(part, (int)shares, (int)a->D, g);
+        else norm_gate_sum_kernel<16><<<grid, dim3(32, 16), 0, s>>>(part, (int)shares, (int)a->D, g);
         count_launches(1);
         e = cudaGetLastError();
     }

@@ -190,6 +190,25 @@ def test_many_rows(hm):
     _backward(hm, _inputs(35, 1000, 24, "f32"), "f32", True, True, True)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("n,D", [(33, 8), (17, 64), (13, 72), (9, 128), (2500, 16)])
+def test_narrow_rows(hm, io, n, D):
+    """Rows that share a warp, in numbers that leave its last teams without one."""
+    c = _inputs(37, n, D, io, True)
+    _forward(hm, c, io, True, True, True)
+    _backward(hm, c, io, True, True, True)
+    _backward(hm, c, io, False, True, False)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("n,D", [(1, 264), (700, 264), (601, 1000), (1203, 2048), (299, 2056), (450, 4096), (200, 4104),
+                                 (151, 8192)])
+def test_backward_rows_at_a_time(hm, io, layer, n, D):
+    """Odd numbers of rows, threads without columns, several steps of a block."""
+    _backward(hm, _inputs(38, n, D, io, layer), io, layer, True, True)
+
+
 def test_far_from_zero_mean(hm):
     """A mean many times the spread: the variance comes from centred values."""
     c = _inputs(36, 6, 512, "f32", mean=300.0)
