@@ -244,7 +244,6 @@ struct Exchange {
 
 constexpr int kR = 16;        // tokens of a warp's run
 constexpr int kCols = 64;     // channels of a warp
-constexpr int kMaxCluster = 8;
 constexpr int kStages = 2;
 
 // Bounded wait of every thread of the block.  After a timeout the kernel keeps
@@ -511,6 +510,7 @@ struct BwdArgs {
     int64_t groups;
     int64_t nchunk;
     float *part;                   // [B * cluster][2][D]: the blocks' shares of dA_log and d_dt_bias
+    float *maps;                   // two passes: [3][B, nchunk, D]: A, R and c of every chunk; else NULL
 };
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -530,11 +530,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
 //
 // Registers hold a, h_{t-1}, Delta, sigmoid(z) (and beta) of 8 tokens: 16
 // warps on an SM; x and dy are read again from shared memory.
+//
+// A long sequence of few channels does not fill the GPU with clusters.  There
+// the backward takes two passes (maps given): gated_adjoint_kernel forms every chunk's adjoint map from
+// dt and dy, gated_carry_kernel runs through them to the c that enters each
+// chunk, and here every chunk stands for itself; dt and dy are read twice.
 template <typename T, int SCALE, int MODE>
 __global__ void __launch_bounds__(kWb * 32, 2)
 gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_constant__ CUtensorMap map_x,
                  const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_dx,
-                 const __grid_constant__ CUtensorMap map_ddt, BwdArgs f, int cluster, DevErr err) {
+                 const __grid_constant__ CUtensorMap map_ddt, BwdArgs f, int splits, DevErr err) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[kBwdStages], low[2], high[2];
     __shared__ int abort_flag;
@@ -544,12 +549,13 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     constexpr uint32_t kBytes = kTile * sizeof(T);
     const hm_gated_scan_bwd_args &p = f.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = cluster > 1 ? (int)cluster_rank() : 0;
-    const int64_t unit = blockIdx.x / cluster, b = unit / f.groups;
+    const int cluster = f.maps ? 1 : splits;       // blocks that exchange
+    const int rank = f.maps ? (int)(blockIdx.x % splits) : cluster > 1 ? (int)cluster_rank() : 0;
+    const int64_t unit = blockIdx.x / splits, b = unit / f.groups;
     const int64_t c0 = (unit - b * f.groups) * kCols, c = c0 + kFirst * lane;
     const bool in0 = c < p.D, in1 = c + kSecond < p.D;
     const int n = (int)clamped_len(p.lengths, b, p.L);
-    const int chunks = (n + kChunk - 1) / kChunk, iters = (chunks + cluster - 1) / cluster;
+    const int chunks = (n + kChunk - 1) / kChunk, iters = (chunks + splits - 1) / splits;
     T *stage0 = reinterpret_cast<T *>(smem);
     Exchange x;
     x.agg = reinterpret_cast<Map2 *>(smem + kBwdStages * 3 * kBytes);   // adjoint maps, last warp first
@@ -569,7 +575,7 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         tc::mbar_fence_init();
     }
     // chunk of window `it`: from the sequence's end; negative: none
-    auto chunk_of = [&](int it) { return chunks - 1 - (it * cluster + rank); };
+    auto chunk_of = [&](int it) { return chunks - 1 - (it * splits + rank); };
     auto fetch = [&](int it) {
         const int s = it % kBwdStages, t = chunk_of(it) * kChunk;
         if (t < 0) return;
@@ -618,6 +624,10 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         if (chunk >= 0 && in0) {
             const float *st = (const float *)p.states + (b * f.nchunk + chunk) * p.D + c;
             hin = pk(st[0], in1 ? st[kSecond] : 0.f);
+            if (f.maps) {
+                const float *q = f.maps + ((2 * p.B + b) * f.nchunk + chunk) * p.D + c;
+                carry = pk(q[0], in1 ? q[kSecond] : 0.f);
+            }
         }
         if (WIDE && chunk >= 0) wait_bar(&full[stage], phase, &abort_flag, err, 3);
         if (MODE == kAsync) {
@@ -759,15 +769,102 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
             sumb = sumb + v.B;
         }
         sumA = sumA * par.nrate * splat(kLn2); // log a = -rate Delta, Delta from its base-2 exponent
-        float *o = f.part + (b * cluster + rank) * 2 * p.D + c;
+        float *o = f.part + (b * splits + rank) * 2 * p.D + c;
         if (in0) o[0] = un(sumA).x, o[p.D] = un(sumb).x;
         if (in1) o[kSecond] = un(sumA).y, o[p.D + kSecond] = un(sumb).y;
     }
     if (cluster > 1) cluster_sync();                       // all have read dh_out, which dh0 may be
-    if (p.dh0 && rank == 0 && warp == 0) {
+    if (p.dh0 && !f.maps && rank == 0 && warp == 0) {
         if (in0) p.dh0[b * p.D + c] = un(carry).x;
         if (in1) p.dh0[b * p.D + c + kSecond] = un(carry).y;
     }
+}
+
+// A warp per chunk and 64 channels: the chunk's adjoint map c -> A c + R, R from
+// its last token to its first, A = 2^(sum of the exponents).  Nothing is kept of
+// the tokens, so many warps fit and HBM bounds it (two reads, of dt and dy).
+template <typename T, int MODE>
+__global__ void __launch_bounds__(256) gated_adjoint_kernel(BwdArgs f) {
+    constexpr int kFirst = Lanes<T, MODE>::kFirst, kSecond = Lanes<T, MODE>::kSecond, U = 8;
+    const hm_gated_scan_bwd_args &p = f.p;
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t at = warp / f.groups, b = at / f.nchunk;      // neighbours in memory: groups of a chunk
+    if (b >= p.B) return;
+    const int chunk = (int)(at - b * f.nchunk), n = (int)clamped_len(p.lengths, b, p.L);
+    const int64_t c = (warp - at * f.groups) * kCols + kFirst * lane;
+    const bool in0 = c < p.D, in1 = c + kSecond < p.D;
+    const int t0 = chunk * kChunk, t1 = min(n, t0 + kChunk);
+    if (t0 >= n || !in0) return;
+    const ChanParams par = chan_params(p.A_log, p.dt_bias, c, c + kSecond, p.D);
+    const T *dtp = (const T *)p.dt + b * p.dt_stride_b + c, *dyp = (const T *)p.dy + b * p.dy_stride_b + c;
+    auto own = [&](const T *q) {
+        if (in1) return Lanes<T, MODE>::load(q);
+        Raw<T> r;
+        r.set(hm_ld(q, 0), 0.f);
+        return r;
+    };
+    F2 R = splat(0.f), sum = splat(0.f);
+    int t = t1;
+    for (; t - t0 >= U; t -= U) {
+        Raw<T> d[U], y[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            d[i] = own(dtp + (int64_t)(t - 1 - i) * p.dt_stride_t);
+            y[i] = own(dyp + (int64_t)(t - 1 - i) * p.dy_stride_t);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const Gate2 g = gates2(d[i].pair(), par);
+            sum = sum + g.la;
+            R = g.a * (y[i].pair() + R);
+        }
+    }
+    for (; t > t0; --t) {
+        const Gate2 g = gates2(own(dtp + (int64_t)(t - 1) * p.dt_stride_t).pair(), par);
+        sum = sum + g.la;
+        R = g.a * (own(dyp + (int64_t)(t - 1) * p.dy_stride_t).pair() + R);
+    }
+    const float2 A = un(ex2(sum)), r = un(R);
+    float *o = f.maps + at * p.D + c;
+    const int64_t plane = p.B * f.nchunk * p.D;
+    o[0] = A.x, o[plane] = r.x;
+    if (in1) o[kSecond] = A.y, o[plane + kSecond] = r.y;
+}
+
+// c at the end of every chunk (third plane) and before the first (dh0): 16
+// segments of a sequence's chunks, each composed, then walked from the c that
+// enters it; 32 channels a block.
+__global__ void __launch_bounds__(512) gated_carry_kernel(BwdArgs f) {
+    __shared__ float2 seg[16][32];
+    const hm_gated_scan_bwd_args &p = f.p;
+    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x, b = blockIdx.y, plane = p.B * f.nchunk * p.D;
+    const bool on = c < p.D;
+    const int n = (int)clamped_len(p.lengths, b, p.L), chunks = (n + kChunk - 1) / kChunk;
+    const int s = threadIdx.y, S = (chunks + 15) / 16, lo = s * S, hi = min(lo + S, chunks);
+    const float *__restrict__ A = f.maps + b * f.nchunk * p.D + c;
+    const float *__restrict__ R = A + plane;
+    float *__restrict__ out = f.maps + 2 * plane + b * f.nchunk * p.D + c;
+    float a = 1.f, r = 0.f;
+    if (on) {
+#pragma unroll 8
+        for (int k = hi - 1; k >= lo; --k) {
+            const float m = A[k * p.D];
+            r = fmaf(m, r, R[k * p.D]);
+            a *= m;
+        }
+    }
+    seg[s][threadIdx.x] = make_float2(a, r);
+    float v = on && p.dh_out ? p.dh_out[b * p.D + c] : 0.f;
+    __syncthreads();
+    for (int k = 15; k > s; --k) v = fmaf(seg[k][threadIdx.x].x, v, seg[k][threadIdx.x].y);
+    if (!on) return;
+#pragma unroll 8
+    for (int k = hi - 1; k >= lo; --k) {
+        out[k * p.D] = v;
+        v = fmaf(A[k * p.D], v, R[k * p.D]);
+    }
+    if (s == 0 && p.dh0) p.dh0[b * p.D + c] = v;
 }
 
 // the blocks' shares summed in order: 8 threads per channel, each a stride of
@@ -933,11 +1030,18 @@ struct Split {
 // 32768: 8 x 8: 129, 4 x 8: 137, 8 x 4: 148, 8 x 16: 162; fp32 2 x 4096 x 2048:
 // 4 x 2, 4, 8: 52, 38, 46.  Padded batches count half their tokens (fp32 5 x
 // up to 1531 x 1001: 4 x 2, 4, 8: 121, 64, 39).
+//
+// Clusters are of at most 8 blocks, or 16 where even those leave SMs idle
+// (fp32 1 x 16384 x 512: 57 -> 42 us; bf16 1 x 32768 x 300: 105 -> 60, 1 x 4096 x 512:
+// 14.8 -> 12.8); with more channels 16 do not find room (32768 x 2048, above).
+int most_blocks(int64_t units) { return units * 16 <= 148 ? 16 : 8; }
+
 Split split_of(int64_t units, int64_t L, hm_dtype t, bool padded) {
     const int64_t runs = (L + kR - 1) / kR, warps = t == HM_BF16 && L > 2048 ? 8 : 4;
     const int64_t most = (t == HM_BF16 ? 148 * 16 : 148 * 12) * (padded ? 2 : 1);
     Split s{(int)warps, 1};
-    while (s.cluster < kMaxCluster && units * s.cluster * 2 * warps <= most && warps * s.cluster < runs &&
+    const int lim = most_blocks(units);
+    while (s.cluster < lim && units * s.cluster * 2 * warps <= most && warps * s.cluster < runs &&
            (runs >= 2 * warps * s.cluster * 2 || units * s.cluster * 2 <= 148))
         s.cluster *= 2;
     return s;
@@ -945,17 +1049,33 @@ Split split_of(int64_t units, int64_t L, hm_dtype t, bool padded) {
 
 // Backward: 8 warps and a window of 64 tokens a block.  4 x 2048 x 2048 with
 // its forward: 1, 2, 4, 8 blocks 95, 91, 98, 109 us; one of 32768: 4, 8, 16:
-// 411, 337, 427.
-Split bwd_split(int64_t units, int64_t L) {
+// 411, 337, 427.  16 as in the forward for bf16 (2 x 1909 x 64: 27 -> 23 us, 1 x
+// 4096 x 512: 42 -> 38); fp32 4 x 2885 x 128: 38 -> 42.
+Split bwd_split(int64_t units, int64_t L, hm_dtype t) {
     const int64_t chunks = (L + kChunk - 1) / kChunk;
+    const int lim = t == HM_BF16 ? most_blocks(units) : 8;
     Split s{kWb, 1};
-    while (s.cluster < kMaxCluster && units * s.cluster * 2 <= 148 * 2 && s.cluster < chunks) s.cluster *= 2;
+    while (s.cluster < lim && units * s.cluster * 2 <= 148 * 2 && s.cluster < chunks) s.cluster *= 2;
     return s;
+}
+// Two passes, for long sequences of so few channels that clusters of 8 leave
+// SMs idle; a sequence's chunks then go to two blocks on every SM.  Forward and
+// backward, one pass and two: fp32 1 x 16384 x 1024: 236, 202 us; bf16 1 x 32768 x
+// 512: 185, 165; 1 x 16384 x 64: 77, 59; but 1 x 8192 x 1024: 93, 91; 1 x 4096 x
+// 512: 38, 45; 1 x 32768 x 2048: 388, 463 (what is read twice costs more than the
+// waits).
+bool two_passes(int64_t units, int64_t L) { return units * 8 <= 148 && L > 8192; }
+int bwd_blocks(int64_t units, int64_t L, hm_dtype t) {
+    if (!two_passes(units, L)) return bwd_split(units, L, t).cluster;
+    const int64_t chunks = (L + kChunk - 1) / kChunk, most = 148 * 2 / units;
+    return (int)(most < chunks ? most : chunks);
 }
 
 size_t bwd_workspace(const hm_gated_scan_bwd_args *a) {
-    const int64_t units = a->B * ((a->D + kCols - 1) / kCols);
-    return (size_t)(a->B * bwd_split(units, a->L).cluster * 2 * a->D) * sizeof(float);
+    const int64_t units = a->B * ((a->D + kCols - 1) / kCols), nchunk = (a->L + kChunk - 1) / kChunk;
+    if (units == 0) return 0;
+    const int64_t maps = two_passes(units, a->L) ? 3 * a->B * nchunk * a->D : 0;
+    return (size_t)(a->B * bwd_blocks(units, a->L, a->io_dtype) * 2 * a->D + maps) * sizeof(float);
 }
 
 hm_status check_bwd(const hm_gated_scan_bwd_args *a) {
@@ -1037,6 +1157,10 @@ template <typename K, typename... A>
 cudaError_t launch_cluster(K kernel, int64_t units, Split sp, size_t smem, cudaStream_t s, A... args) {
     cudaError_t e = tc::ensure_smem_limit(kernel, (int)smem);
     if (e != cudaSuccess) return e;
+    if (sp.cluster > 8) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(units * sp.cluster));
     cfg.blockDim = dim3(sp.warps * 32);
@@ -1116,12 +1240,15 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
     cudaError_t e = cudaSuccess;
     int64_t shares = 0;
     if (a->B > 0) {
-        BwdArgs f{*a, (a->D + kCols - 1) / kCols, (a->L + kChunk - 1) / kChunk, (float *)a->workspace};
+        BwdArgs f{*a, (a->D + kCols - 1) / kCols, (a->L + kChunk - 1) / kChunk, (float *)a->workspace, nullptr};
         const int64_t units = a->B * f.groups;
-        const Split sp = bwd_split(units, a->L);
-        if (units * sp.cluster > 0x7fffffffLL)
+        const bool two = two_passes(units, a->L);
+        const int splits = bwd_blocks(units, a->L, a->io_dtype);
+        const Split sp{kWb, two ? 1 : splits};
+        if (units * splits > 0x7fffffffLL)
             return fail_args(HM_ERR_UNSUPPORTED, "gated_scan_bwd: B * D / 64 is too large");
-        shares = a->B * sp.cluster;
+        shares = a->B * splits;
+        if (two) f.maps = f.part + shares * 2 * a->D;
         const size_t es = esize(a->io_dtype);
         struct {
             const void *p;
@@ -1145,13 +1272,20 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
             constexpr int S = decltype(sc)::value;
             const size_t smem = (size_t)kBwdStages * 3 * kChunk * kCols * sizeof(T) +
                                 (size_t)2 * (2 * kWb + sp.cluster) * 32 * sizeof(Map2);
-            auto go = [&](auto kernel) {
-                return launch_cluster(kernel, units, sp, smem, s, t[0].map, t[1].map, t[2].map, t[3].map, t[4].map, f,
-                                      sp.cluster, err);
+            auto go = [&](auto kernel, auto adjoint) {
+                if (two) {
+                    adjoint<<<(unsigned)((units * f.nchunk + 7) / 8), 256, 0, s>>>(f);
+                    gated_carry_kernel<<<dim3((unsigned)((a->D + 31) / 32), (unsigned)a->B), dim3(32, 16), 0, s>>>(f);
+                    count_launches(2);
+                    const cudaError_t e = cudaGetLastError();
+                    if (e != cudaSuccess) return e;
+                }
+                return launch_cluster(kernel, units * (two ? splits : 1), sp, smem, s, t[0].map, t[1].map, t[2].map,
+                                      t[3].map, t[4].map, f, splits, err);
             };
-            if (wide) return go(gated_bwd_kernel<T, S, kTma>);
-            if (words) return go(gated_bwd_kernel<T, S, kAsync>);
-            if constexpr (sizeof(T) == 2) return go(gated_bwd_kernel<T, S, kPlain>);
+            if (wide) return go(gated_bwd_kernel<T, S, kTma>, gated_adjoint_kernel<T, kTma>);
+            if (words) return go(gated_bwd_kernel<T, S, kAsync>, gated_adjoint_kernel<T, kAsync>);
+            if constexpr (sizeof(T) == 2) return go(gated_bwd_kernel<T, S, kPlain>, gated_adjoint_kernel<T, kPlain>);
             return cudaErrorInvalidValue;          // not reached: fp32 rows are words
         });
     }

@@ -187,6 +187,13 @@ def test_long_and_wide(hm):
     _check(hm, _inputs(17, 40, 33, 260, "f32"), "f32", around.PLAIN)
 
 
+@pytest.mark.parametrize("io,scale,D,pad", [("bf16", 2, 64, 0), ("f32", 1, 72, 0), ("bf16", 1, 33, 0),
+                                            ("bf16", 0, 34, 2)])
+def test_few_channels_of_a_long_sequence(hm, io, scale, D, pad):
+    """Clusters of 16, and the backward in two passes; sequences that end early, one of them at once."""
+    _check(hm, _inputs(24, 3, 8300, D, io), io, scale, lengths=[8300, 0, 8193], pad=pad)
+
+
 def test_no_tokens(hm):
     """L = 0 hands the state on and gives zero parameter gradients; B = 0 does nothing."""
     import torch
