@@ -25,6 +25,7 @@ namespace hm {
 namespace {
 
 constexpr int kChunk = 64;   // tokens between two stored states
+constexpr int kCols = 64;    // channels of a warp
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ int64_t clamped_len(const int32_t *lengths, int64_t b, int64_t L) {
@@ -150,14 +151,17 @@ __device__ __forceinline__ void st_pair(float *p, F2 v) { *reinterpret_cast<floa
 // How a block's tiles come and go.  kTma: boxes by TMA, where rows start on
 // 16-byte boundaries.  kAsync: each thread's own elements by cp.async, ahead
 // by the same number of windows: fp32 rows at any offset, bf16 rows on 4-byte
-// boundaries.  kPlain: element loads (bf16 rows at odd offsets).
-enum Mode { kPlain = 0, kAsync = 1, kTma = 2 };
+// boundaries.  kOdd (bf16 rows at odd offsets): the aligned words that hold a
+// warp's 64 elements of a row, 32 or 33 of them, by cp.async from its lanes
+// together; an aligned word with an element of the row in it is always readable.
+enum Mode { kOdd = 0, kAsync = 1, kTma = 2 };
 
 // A lane's two channels: neighbours where they move as one word or box; else
 // 32 apart, so that a warp's single elements are neighbours in memory.
 template <typename T, int MODE>
 struct Lanes {
-    static constexpr bool kSplit = MODE == kPlain || (MODE == kAsync && sizeof(T) == 4);
+    static constexpr bool kSplit = MODE == kOdd || (MODE == kAsync && sizeof(T) == 4);
+    static constexpr int kPitch = MODE == kOdd ? kCols + 2 : kCols;              // of a tile's rows
     static constexpr int kFirst = kSplit ? 1 : 2, kSecond = kSplit ? 32 : 1;     // 1st: lane * kFirst; 2nd: that + kSecond
     static __device__ __forceinline__ Raw<T> load(const T *p) {
         Raw<T> r;
@@ -184,6 +188,17 @@ __device__ __forceinline__ void own_pair(T *dst, const T *src, bool in1) {
     } else {
         cp_async4(dst, src, in1 ? 4 : 2);
     }
+}
+
+// whether a bf16 row starts in the upper half of a word
+__device__ __forceinline__ int odd_half(const void *p) { return (int)((uintptr_t)p >> 1) & 1; }
+// kOdd: the words of a row's elements [0, min(left, 64)) from `src` on
+template <typename T>
+__device__ __forceinline__ void own_words(T *dst, const T *src, int lane, int64_t left) {
+    const int off = odd_half(src);
+    src -= off;
+    if (2 * lane - off < left) cp_async4(dst + 2 * lane, src + 2 * lane, 4);
+    if (lane == 0 && off && left >= kCols) cp_async4(dst + kCols, src + kCols, 4);
 }
 
 // ------------------------------------------------------------------ exchange
@@ -243,7 +258,6 @@ struct Exchange {
 };
 
 constexpr int kR = 16;        // tokens of a warp's run
-constexpr int kCols = 64;     // channels of a warp
 constexpr int kStages = 2;
 
 // Bounded wait of every thread of the block.  After a timeout the kernel keeps
@@ -339,8 +353,9 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     __shared__ int abort_flag;
     constexpr bool WIDE = MODE == kTma;
     constexpr int kFirst = Lanes<T, MODE>::kFirst, kSecond = Lanes<T, MODE>::kSecond;
+    constexpr int kPitch = Lanes<T, MODE>::kPitch;
     constexpr int kRows = W * kR;                  // tokens of a block's window
-    constexpr int kTile = kRows * kCols;           // elements of a tile
+    constexpr int kTile = kRows * kPitch;          // elements of a tile
     constexpr uint32_t kBytes = kTile * sizeof(T);
     const hm_gated_scan_args &p = f.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -353,7 +368,7 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     const int iters = (int)(((unsigned)n + (unsigned)window - 1u) / (unsigned)window);
     T *stage0 = reinterpret_cast<T *>(smem), *out = stage0 + 2 * kStages * kTile + warp * kR * kCols;
     Exchange x;
-    x.agg = reinterpret_cast<Map2 *>(smem + (WIDE ? 2 * kStages + 1 : MODE == kAsync ? 2 * kStages : 0) * kBytes);
+    x.agg = reinterpret_cast<Map2 *>(smem + (WIDE ? 2 * kStages + 1 : 2 * kStages) * kBytes);
     x.ctas = x.agg + 2 * W * 32;
     x.low = low;
     x.high = high;
@@ -386,19 +401,27 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     if (p.h0) h = pk(in0 ? p.h0[b * p.D + c] : 0.f, in1 ? p.h0[b * p.D + c + kSecond] : 0.f);
     const T *dtp = (const T *)p.dt + b * p.dt_stride_b + c, *xp = (const T *)p.x + b * p.x_stride_b + c;
     T *yp = (T *)p.y + b * p.y_stride_b + c;
-    auto fetch_own = [&](int it) {                 // this thread's elements of window `it`
-        const int t = it * window + rank * kRows + warp * kR, m = in0 ? min(n - t, kR) : 0;
-        T *dst = stage0 + (it % kStages) * 2 * kTile + warp * kR * kCols + kFirst * lane;
+    auto fetch_own = [&](int it) {                 // this thread's elements (kOdd: words) of window `it`
+        const int t = it * window + rank * kRows + warp * kR, m = in0 || MODE == kOdd ? min(n - t, kR) : 0;
+        T *dst = stage0 + (it % kStages) * 2 * kTile + warp * kR * kPitch + (MODE == kOdd ? 0 : kFirst * lane);
         const T *pd = dtp + t * p.dt_stride_t, *px = xp + t * p.x_stride_t;
 #pragma unroll 4
-        for (int i = 0; i < m; ++i, dst += kCols, pd += p.dt_stride_t, px += p.x_stride_t) {
+        for (int i = 0; i < m; ++i, dst += kPitch, pd += p.dt_stride_t, px += p.x_stride_t) {
+            if (MODE == kOdd) {
+                own_words(dst, pd - lane, lane, p.D - c0);
+                own_words(dst + kTile, px - lane, lane, p.D - c0);
+                continue;
+            }
             own_pair<T, MODE>(dst, pd, in1);
             own_pair<T, MODE>(dst + kTile, px, in1);
         }
         cp_async_commit();
     };
-    if (MODE == kAsync)
+    if (!WIDE)
         for (int s = 0; s < kStages; ++s) fetch_own(s);
+    // kOdd: the half word a row starts in; a run's first token is even
+    const int hd = MODE == kOdd ? odd_half(dtp - lane) : 0, hx = MODE == kOdd ? odd_half(xp - lane) : 0;
+    const int sd = MODE == kOdd ? (int)p.dt_stride_t & 1 : 0, sx = MODE == kOdd ? (int)p.x_stride_t & 1 : 0;
 
     int t0 = rank * kRows + warp * kR;             // the run's first token
     for (int it = 0; it < iters; ++it, t0 += window) {
@@ -406,28 +429,15 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         Map2 run[kR];                              // the run's composition up to each token
         Map2 all = {splat(1.f), splat(0.f)};
         if (WIDE) wait_bar(&full[it % kStages], (it / kStages) & 1, &abort_flag, err, 0);
-        if (MODE == kAsync) cp_async_wait<kStages - 1>();
+        if (!WIDE) cp_async_wait<kStages - 1>();
+        if (MODE == kOdd) __syncwarp();            // the other lanes' words
         if (m > 0) {
             Raw<T> dv[kR], xv[kR];
-            const T *sdt = stage0 + (it % kStages) * 2 * kTile + (warp * kR) * kCols + kFirst * lane;
-            if (MODE != kPlain) {
+            const T *sdt = stage0 + (it % kStages) * 2 * kTile + (warp * kR) * kPitch + kFirst * lane;
 #pragma unroll
-                for (int i = 0; i < kR; ++i) {
-                    dv[i] = Lanes<T, MODE>::load(sdt + i * kCols);
-                    xv[i] = Lanes<T, MODE>::load(sdt + kTile + i * kCols);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kR; ++i) {
-                    float d0 = 0.f, d1 = 0.f, x0 = 0.f, x1 = 0.f;
-                    if (i < m) {
-                        const int64_t od = (int64_t)(t0 + i) * p.dt_stride_t, ox = (int64_t)(t0 + i) * p.x_stride_t;
-                        if (in0) d0 = hm_ld(dtp, od), x0 = hm_ld(xp, ox);
-                        if (in1) d1 = hm_ld(dtp, od + kSecond), x1 = hm_ld(xp, ox + kSecond);
-                    }
-                    dv[i].set(d0, d1);
-                    xv[i].set(x0, x1);
-                }
+            for (int i = 0; i < kR; ++i) {
+                dv[i] = Lanes<T, MODE>::load(sdt + i * kPitch + (hd ^ (i & sd)));
+                xv[i] = Lanes<T, MODE>::load(sdt + kTile + i * kPitch + (hx ^ (i & sx)));
             }
             if (m < kR) {        // tokens behind the end change nothing: a step of zero, no input
 #pragma unroll
@@ -451,7 +461,7 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         if (cluster > 1 && it > 0) h = finish_window(x, it, h);
         __syncthreads();         // maps written; this window's tiles, and the window before's maps, read
         if (WIDE && threadIdx.x == 0 && it + kStages < iters) fetch(it + kStages);
-        if (MODE == kAsync) fetch_own(it + kStages);
+        if (!WIDE) fetch_own(it + kStages);
         const F2 hin = enter_run<W>(x, it, warp, h);
         if (m > 0) {
             if (p.states && t0 % kChunk == 0 && in0) {
@@ -545,7 +555,8 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     __shared__ int abort_flag;
     constexpr bool WIDE = MODE == kTma;
     constexpr int kFirst = Lanes<T, MODE>::kFirst, kSecond = Lanes<T, MODE>::kSecond;
-    constexpr int kTile = kChunk * kCols;
+    constexpr int kPitch = Lanes<T, MODE>::kPitch;
+    constexpr int kTile = kChunk * kPitch;
     constexpr uint32_t kBytes = kTile * sizeof(T);
     const hm_gated_scan_bwd_args &p = f.p;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -597,19 +608,29 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     const T *dyp = (const T *)p.dy + b * p.dy_stride_b + c;
     T *dxp = (T *)p.dx + b * p.dx_stride_b + c, *ddtp = (T *)p.ddt + b * p.ddt_stride_b + c;
     auto fetch_own = [&](int it) {
-        const int t = chunk_of(it) * kChunk + warp * kRb, m = in0 && t >= 0 ? min(n - t, kRb) : 0;
-        T *dst = stage0 + it % kBwdStages * 3 * kTile + warp * kRb * kCols + kFirst * lane;
+        const int t = chunk_of(it) * kChunk + warp * kRb, m = (in0 || MODE == kOdd) && t >= 0 ? min(n - t, kRb) : 0;
+        T *dst = stage0 + it % kBwdStages * 3 * kTile + warp * kRb * kPitch + (MODE == kOdd ? 0 : kFirst * lane);
         const T *pd = dtp + t * p.dt_stride_t, *px = xp + t * p.x_stride_t, *py = dyp + t * p.dy_stride_t;
 #pragma unroll 4
-        for (int i = 0; i < m; ++i, dst += kCols) {
+        for (int i = 0; i < m; ++i, dst += kPitch) {
+            if (MODE == kOdd) {
+                own_words(dst, pd - lane + i * p.dt_stride_t, lane, p.D - c0);
+                own_words(dst + kTile, px - lane + i * p.x_stride_t, lane, p.D - c0);
+                own_words(dst + 2 * kTile, py - lane + i * p.dy_stride_t, lane, p.D - c0);
+                continue;
+            }
             own_pair<T, MODE>(dst, pd + i * p.dt_stride_t, in1);
             own_pair<T, MODE>(dst + kTile, px + i * p.x_stride_t, in1);
             own_pair<T, MODE>(dst + 2 * kTile, py + i * p.dy_stride_t, in1);
         }
         cp_async_commit();
     };
-    if (MODE == kAsync)
+    if (!WIDE)
         for (int s = 0; s < kBwdStages - 1; ++s) fetch_own(s);
+    // kOdd: the half word a row starts in; a run's first token is even
+    const int hd = MODE == kOdd ? odd_half(dtp - lane) : 0, sd = MODE == kOdd ? (int)p.dt_stride_t & 1 : 0;
+    const int hx = MODE == kOdd ? odd_half(xp - lane) : 0, sx = MODE == kOdd ? (int)p.x_stride_t & 1 : 0;
+    const int hy = MODE == kOdd ? odd_half(dyp - lane) : 0, sy = MODE == kOdd ? (int)p.dy_stride_t & 1 : 0;
     F2 sumA = splat(0.f), sumb = splat(0.f);
     int stage = 0;
     uint32_t phase = 0;
@@ -617,7 +638,7 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     for (int it = 0; it < iters; ++it) {
         const int chunk = chunk_of(it), t0 = chunk * kChunk + warp * kRb;
         const int m = chunk < 0 ? 0 : min(max(n - t0, 0), kRb);
-        T *tile = stage0 + stage * 3 * kTile + (warp * kRb) * kCols + kFirst * lane;
+        T *tile = stage0 + stage * 3 * kTile + (warp * kRb) * kPitch + kFirst * lane;
         F2 a[kRb], h[kRb], step[kRb], sig[kRb], beta[kRb];
         Map2 mf = {splat(1.f), splat(0.f)}, mr = {splat(1.f), splat(0.f)};
         F2 hin = splat(0.f);
@@ -630,32 +651,27 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
             }
         }
         if (WIDE && chunk >= 0) wait_bar(&full[stage], phase, &abort_flag, err, 3);
-        if (MODE == kAsync) {
-            fetch_own(it + kBwdStages - 1);                // over what this thread used one window ago
+        if (!WIDE) {
+            if (MODE == kOdd) __syncwarp();
+            fetch_own(it + kBwdStages - 1);                // over what this thread (kOdd: warp) used one window ago
             cp_async_wait<kBwdStages - 1>();
+            if (MODE == kOdd) __syncwarp();                // the other lanes' words
         }
         if (m > 0) {
-            // a thread's own elements of the tile: element loads put them there, and tokens behind
-            // the end become a step of zero, no input, no gradient of their own
-            if (MODE == kPlain || m < kRb) {
-                for (int i = MODE == kPlain ? 0 : m; i < kRb; ++i) {
-                    float d0 = -INFINITY, d1 = -INFINITY, x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
-                    if (i < m) {
-                        const int64_t t = t0 + i, od = t * p.dt_stride_t, ox = t * p.x_stride_t, oy = t * p.dy_stride_t;
-                        if (in0) d0 = hm_ld(dtp, od), x0 = hm_ld(xp, ox), y0 = hm_ld(dyp, oy);
-                        if (in1) d1 = hm_ld(dtp, od + kSecond), x1 = hm_ld(xp, ox + kSecond), y1 = hm_ld(dyp, oy + kSecond);
-                    }
-                    T *q = tile + i * kCols;
-                    hm_st(q, 0, d0), hm_st(q, kSecond, d1);
-                    hm_st(q, kTile, x0), hm_st(q, kTile + kSecond, x1);
-                    hm_st(q, 2 * kTile, y0), hm_st(q, 2 * kTile + kSecond, y1);
-                }
+            auto at_dt = [&](int i) { return tile + i * kPitch + (hd ^ (i & sd)); };
+            auto at_x = [&](int i) { return tile + kTile + i * kPitch + (hx ^ (i & sx)); };
+            auto at_dy = [&](int i) { return tile + 2 * kTile + i * kPitch + (hy ^ (i & sy)); };
+            // tokens behind the end: a step of zero, no input, no gradient of their own
+            for (int i = m; i < kRb; ++i) {
+                hm_st(at_dt(i), 0, -INFINITY), hm_st(at_dt(i), kSecond, -INFINITY);
+                hm_st(at_x(i), 0, 0.f), hm_st(at_x(i), kSecond, 0.f);
+                hm_st(at_dy(i), 0, 0.f), hm_st(at_dy(i), kSecond, 0.f);
             }
             Raw<T> dv[kRb], xr[kRb];
 #pragma unroll
             for (int i = 0; i < kRb; ++i) {
-                dv[i] = Lanes<T, MODE>::load(tile + i * kCols);
-                xr[i] = Lanes<T, MODE>::load(tile + kTile + i * kCols);
+                dv[i] = Lanes<T, MODE>::load(at_dt(i));
+                xr[i] = Lanes<T, MODE>::load(at_x(i));
             }
             F2 sum = splat(0.f);
 #pragma unroll
@@ -679,7 +695,7 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
             }
 #pragma unroll
             for (int i = kRb - 1; i >= 0; --i) {
-                const Raw<T> dy = Lanes<T, MODE>::load(tile + 2 * kTile + i * kCols);
+                const Raw<T> dy = Lanes<T, MODE>::load(at_dy(i));
                 mr.B = a[i] * (dy.pair() + mr.B);
             }
             mf.A = mr.A = ex2(sum);
@@ -702,8 +718,8 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
             }
 #pragma unroll
             for (int i = kRb - 1; i >= 0; --i) {
-                const Raw<T> rx = Lanes<T, MODE>::load(tile + kTile + i * kCols);
-                const Raw<T> rdy = Lanes<T, MODE>::load(tile + 2 * kTile + i * kCols);
+                const Raw<T> rx = Lanes<T, MODE>::load(tile + kTile + i * kPitch + (hx ^ (i & sx)));
+                const Raw<T> rdy = Lanes<T, MODE>::load(tile + 2 * kTile + i * kPitch + (hy ^ (i & sy)));
                 const F2 xv = rx.pair(), g = rdy.pair() + cin;
                 cin = a[i] * g;
                 F2 dla = cin * h[i];
@@ -1205,8 +1221,8 @@ extern "C" hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t 
     const cudaError_t e = by_type(a->io_dtype, a->input_scale, [&](auto *t, auto sc) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int S = decltype(sc)::value;
-        auto go = [&](auto kernel, int tiles) {
-            const size_t smem = (size_t)tiles * rows * kCols * sizeof(T) +
+        auto go = [&](auto kernel, int tiles, int pitch = kCols) {
+            const size_t smem = (size_t)tiles * rows * pitch * sizeof(T) +
                                 (size_t)2 * (sp.warps + sp.cluster) * 32 * sizeof(Map2);
             return launch_cluster(kernel, units, sp, smem, (cudaStream_t)stream, mdt, mx, my, f, sp.cluster, err);
         };
@@ -1214,7 +1230,7 @@ extern "C" hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t 
             constexpr int W = decltype(w)::value;
             if (wide) return go(gated_fwd_kernel<T, S, kTma, W>, 2 * kStages + 1);
             if (words) return go(gated_fwd_kernel<T, S, kAsync, W>, 2 * kStages);
-            if constexpr (sizeof(T) == 2) return go(gated_fwd_kernel<T, S, kPlain, W>, 0);
+            if constexpr (sizeof(T) == 2) return go(gated_fwd_kernel<T, S, kOdd, W>, 2 * kStages, Lanes<T, kOdd>::kPitch);
             return cudaErrorInvalidValue;          // not reached: fp32 rows are words
         };
         if constexpr (sizeof(T) == 2)
@@ -1270,7 +1286,8 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
         e = by_type(a->io_dtype, a->input_scale, [&](auto *tp, auto sc) {
             using T = std::remove_pointer_t<decltype(tp)>;
             constexpr int S = decltype(sc)::value;
-            const size_t smem = (size_t)kBwdStages * 3 * kChunk * kCols * sizeof(T) +
+            const int pitch = !wide && !words ? Lanes<__nv_bfloat16, kOdd>::kPitch : kCols;
+            const size_t smem = (size_t)kBwdStages * 3 * kChunk * pitch * sizeof(T) +
                                 (size_t)2 * (2 * kWb + sp.cluster) * 32 * sizeof(Map2);
             auto go = [&](auto kernel, auto adjoint) {
                 if (two) {
@@ -1285,7 +1302,7 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
             };
             if (wide) return go(gated_bwd_kernel<T, S, kTma>, gated_adjoint_kernel<T, kTma>);
             if (words) return go(gated_bwd_kernel<T, S, kAsync>, gated_adjoint_kernel<T, kAsync>);
-            if constexpr (sizeof(T) == 2) return go(gated_bwd_kernel<T, S, kPlain>, gated_adjoint_kernel<T, kPlain>);
+            if constexpr (sizeof(T) == 2) return go(gated_bwd_kernel<T, S, kOdd>, gated_adjoint_kernel<T, kOdd>);
             return cudaErrorInvalidValue;          // not reached: fp32 rows are words
         });
     }
