@@ -320,3 +320,61 @@ def test_same_bits_on_streams_and_in_a_graph(hm):
     for k, t in (("y", y), ("h_out", h_out), ("dx", dx), ("ddt", ddt), ("dA_log", dA), ("d_dt_bias", db),
                  ("dh0", dh0)):
         assert np.array_equal(to_np(t), one[k]), k
+
+
+@pytest.mark.parametrize("B,L,D", [(1, 5000, 64), (40, 90, 128), (1, 9000, 130), (2, 0, 24)])
+def test_states_in_place(hm, B, L, D):
+    """h_out over h0 and dh0 over dh_out with one block a sequence, clusters and two passes."""
+    import torch
+    c = _inputs(25, B, L, D, "bf16")
+    x, dt, dy = (dev_tensor(c[k], "bf16") for k in ("x", "dt", "dy"))
+    A, bias, h0, dh = (dev_tensor(c[k], "f32") for k in ("A_log", "dt_bias", "h0", "dh_out"))
+    got = []
+    for place in (False, True):
+        h, g = h0.clone(), dh.clone()
+        ho, go = (h, g) if place else (torch.zeros_like(h), torch.zeros_like(g))
+        y, dx, ddt, dA = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(A)
+        a = hm.gated_scan_args(x, dt, y, A, dt_bias=bias, h0=h, h_out=ho, input_scale=around.STEP)
+        st = hm.alloc_workspace(hm.hm_gated_scan_states_size(a))
+        a.states, a.states_bytes = st.data_ptr(), st.numel()
+        hm.hm_gated_scan_fwd(a)
+        b = hm.gated_scan_bwd_args(x, dt, dy, dx, ddt, A, dA, st, dt_bias=bias, dh_out=g, dh0=go,
+                                   input_scale=around.STEP)
+        ws = hm.alloc_workspace(hm.hm_gated_scan_bwd_workspace_size(b))
+        b.workspace, b.workspace_bytes = ws.data_ptr(), ws.numel()
+        hm.hm_gated_scan_bwd(b)
+        got.append((y, ho, dx, ddt, dA, go))
+    for u, v in zip(*got):
+        assert torch.equal(u, v)
+
+
+def test_two_passes_captured(hm):
+    """A long sequence of few channels, its backward captured and replayed on new data."""
+    import torch
+    c = _inputs(26, 1, 8500, 40, "bf16")
+    one = _run(hm, c, "bf16", around.UNIT)
+    x, dt, dy = (dev_tensor(c[k], "bf16") for k in ("x", "dt", "dy"))
+    A, bias, h0, dh = (dev_tensor(c[k], "f32") for k in ("A_log", "dt_bias", "h0", "dh_out"))
+    s = [torch.zeros_like(x) for _ in range(3)]
+    y, dx, ddt, dh0, dA = torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(x), torch.zeros_like(dh), \
+        torch.zeros_like(A)
+    a = hm.gated_scan_args(s[0], s[1], y, A, dt_bias=bias, h0=h0, input_scale=around.UNIT)
+    st = hm.alloc_workspace(hm.hm_gated_scan_states_size(a))
+    a.states, a.states_bytes = st.data_ptr(), st.numel()
+    b = hm.gated_scan_bwd_args(s[0], s[1], s[2], dx, ddt, A, dA, st, dt_bias=bias, dh_out=dh, dh0=dh0,
+                               input_scale=around.UNIT)
+    ws = hm.alloc_workspace(hm.hm_gated_scan_bwd_workspace_size(b))
+    b.workspace, b.workspace_bytes = ws.data_ptr(), ws.numel()
+    hm.hm_gated_scan_fwd(a)
+    hm.hm_gated_scan_bwd(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hm.hm_gated_scan_fwd(a)
+        hm.hm_gated_scan_bwd(b)
+    for t, v in zip(s, (x, dt, dy)):
+        t.copy_(v)
+    graph.replay()
+    torch.cuda.synchronize()
+    for k, t in (("y", y), ("dx", dx), ("ddt", ddt), ("dA_log", dA), ("dh0", dh0)):
+        assert np.array_equal(to_np(t), one[k]), k

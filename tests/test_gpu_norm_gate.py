@@ -327,3 +327,25 @@ def test_captured(hm):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("io,n,D", [("bf16", 37, 64), ("f32", 9, 128), ("bf16", 301, 2048), ("bf16", 150, 6000),
+                                    ("f32", 7, 8192)])
+def test_backward_in_place(hm, io, n, D):
+    """dy over y, dgate over gate, dr over dxn: the same bits, in each form of the backward."""
+    import torch
+    c = _inputs(39, n, D, io)
+    y, r, gate, r_out, dr_out, dxn = (_dev(c[k], io) for k in ROWS)
+    kw = _gpu_kw(hm, c, True, True, 1e-5, 0.7)
+
+    def back(y, gate, dxn, dy, dr, dgate):
+        b = hm.norm_gate_bwd_args(y, r_out, dr_out, dxn, dy, dr, gate=gate, dgate=dgate, **kw)
+        ws = hm.alloc_workspace(hm.hm_norm_gate_bwd_workspace_size(b))
+        b.workspace, b.workspace_bytes = ws.data_ptr(), ws.numel()
+        hm.hm_norm_gate_bwd(b)
+        torch.cuda.synchronize()
+    outs = [torch.empty_like(y) for _ in range(3)]
+    back(y, gate, dxn, *outs)
+    yc, gc, dc = y.clone(), gate.clone(), dxn.clone()
+    back(yc, gc, dc, yc, dc, gc)
+    assert all(torch.equal(a, b) for a, b in zip(outs, (yc, dc, gc)))
