@@ -631,6 +631,21 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
     const int hd = MODE == kOdd ? odd_half(dtp - lane) : 0, sd = MODE == kOdd ? (int)p.dt_stride_t & 1 : 0;
     const int hx = MODE == kOdd ? odd_half(xp - lane) : 0, sx = MODE == kOdd ? (int)p.x_stride_t & 1 : 0;
     const int hy = MODE == kOdd ? odd_half(dyp - lane) : 0, sy = MODE == kOdd ? (int)p.dy_stride_t & 1 : 0;
+    // h entering the next window's chunk (with maps also c entering it from behind), a window ahead
+    float h0 = 0.f, h1 = 0.f, g0 = 0.f, g1 = 0.f;
+    auto fetch_state = [&](int it) {
+        const int chunk = chunk_of(it);
+        if (chunk < 0) return;
+        const float *st = (const float *)p.states + (b * f.nchunk + chunk) * p.D + c;
+        if (in0) h0 = st[0];
+        if (in1) h1 = st[kSecond];
+        if (f.maps) {
+            const float *q = f.maps + ((2 * p.B + b) * f.nchunk + chunk) * p.D + c;
+            if (in0) g0 = q[0];
+            if (in1) g1 = q[kSecond];
+        }
+    };
+    if (iters > 0) fetch_state(0);
     F2 sumA = splat(0.f), sumb = splat(0.f);
     int stage = 0;
     uint32_t phase = 0;
@@ -641,15 +656,6 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         T *tile = stage0 + stage * 3 * kTile + (warp * kRb) * kPitch + kFirst * lane;
         F2 a[kRb], h[kRb], step[kRb], sig[kRb], beta[kRb];
         Map2 mf = {splat(1.f), splat(0.f)}, mr = {splat(1.f), splat(0.f)};
-        F2 hin = splat(0.f);
-        if (chunk >= 0 && in0) {
-            const float *st = (const float *)p.states + (b * f.nchunk + chunk) * p.D + c;
-            hin = pk(st[0], in1 ? st[kSecond] : 0.f);
-            if (f.maps) {
-                const float *q = f.maps + ((2 * p.B + b) * f.nchunk + chunk) * p.D + c;
-                carry = pk(q[0], in1 ? q[kSecond] : 0.f);
-            }
-        }
         if (WIDE && chunk >= 0) wait_bar(&full[stage], phase, &abort_flag, err, 3);
         if (!WIDE) {
             if (MODE == kOdd) __syncwarp();
@@ -706,7 +712,10 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         if (WIDE && lane == 0) tc::bulk_wait_read_all();   // this warp's rows of the last window have left
         __syncthreads();           // maps written; the last window's tiles free
         if (WIDE && threadIdx.x == 0 && it > 0 && it - 1 + kBwdStages < iters) fetch(it - 1 + kBwdStages);
+        F2 hin = pk(h0, h1);
+        if (f.maps) carry = pk(g0, g1);
         F2 cin = enter_run<kWb>(x, it, kWb - 1 - warp, carry);
+        if (it + 1 < iters) fetch_state(it + 1);
         if (m > 0) {
             const Map2 *mw = fwd + (it & 1) * kWb * 32 + lane;
             for (int w = 0; w < warp; ++w, mw += 32) hin = apply(*mw, hin);
@@ -798,66 +807,75 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
 
 // A warp per chunk and 64 channels: the chunk's adjoint map c -> A c + R, R from
 // its last token to its first, A = 2^(sum of the exponents).  Nothing is kept of
-// the tokens, so many warps fit and HBM bounds it (two reads, of dt and dy).
+// the tokens, so many warps fit: 32768 x 1024 bf16 in about 40 us, bound by the
+// latency of 8 rows in flight per warp (16 rows, fewer warps: the same).
 template <typename T, int MODE>
-__global__ void __launch_bounds__(256) gated_adjoint_kernel(BwdArgs f) {
+__global__ void __launch_bounds__(128, 8) gated_adjoint_kernel(BwdArgs f) {
     constexpr int kFirst = Lanes<T, MODE>::kFirst, kSecond = Lanes<T, MODE>::kSecond, U = 8;
     const hm_gated_scan_bwd_args &p = f.p;
     const int lane = threadIdx.x & 31;
-    const int64_t warp = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t warp = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int64_t at = warp / f.groups, b = at / f.nchunk;      // neighbours in memory: groups of a chunk
     if (b >= p.B) return;
     const int chunk = (int)(at - b * f.nchunk), n = (int)clamped_len(p.lengths, b, p.L);
     const int64_t c = (warp - at * f.groups) * kCols + kFirst * lane;
     const bool in0 = c < p.D, in1 = c + kSecond < p.D;
     const int t0 = chunk * kChunk, t1 = min(n, t0 + kChunk);
-    if (t0 >= n || !in0) return;
+    if (t0 >= n) return;                           // the whole warp
     const ChanParams par = chan_params(p.A_log, p.dt_bias, c, c + kSecond, p.D);
     const T *dtp = (const T *)p.dt + b * p.dt_stride_b + c, *dyp = (const T *)p.dy + b * p.dy_stride_b + c;
-    auto own = [&](const T *q) {
-        if (in1) return Lanes<T, MODE>::load(q);
-        Raw<T> r;
-        r.set(hm_ld(q, 0), 0.f);
-        return r;
-    };
     F2 R = splat(0.f), sum = splat(0.f);
-    int t = t1;
-    for (; t - t0 >= U; t -= U) {
-        Raw<T> d[U], y[U];
+    auto walk = [&](auto whole) {                  // whole: every lane has both channels, so no load waits for a branch
+        auto own = [&](const T *q) {
+            if (decltype(whole)::value) return Lanes<T, MODE>::load(q);
+            Raw<T> r;
+            r.set(in0 ? hm_ld(q, 0) : 0.f, in1 ? hm_ld(q, kSecond) : 0.f);
+            return r;
+        };
+        int t = t1;
+        for (; t - t0 >= U; t -= U) {
+            Raw<T> d[U], y[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            d[i] = own(dtp + (int64_t)(t - 1 - i) * p.dt_stride_t);
-            y[i] = own(dyp + (int64_t)(t - 1 - i) * p.dy_stride_t);
+            for (int i = 0; i < U; ++i) {
+                d[i] = own(dtp + (int64_t)(t - 1 - i) * p.dt_stride_t);
+                y[i] = own(dyp + (int64_t)(t - 1 - i) * p.dy_stride_t);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const Gate2 g = gates2(d[i].pair(), par);
+                sum = sum + g.la;
+                R = g.a * (y[i].pair() + R);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const Gate2 g = gates2(d[i].pair(), par);
+        for (; t > t0; --t) {
+            const Gate2 g = gates2(own(dtp + (int64_t)(t - 1) * p.dt_stride_t).pair(), par);
             sum = sum + g.la;
-            R = g.a * (y[i].pair() + R);
+            R = g.a * (own(dyp + (int64_t)(t - 1) * p.dy_stride_t).pair() + R);
         }
-    }
-    for (; t > t0; --t) {
-        const Gate2 g = gates2(own(dtp + (int64_t)(t - 1) * p.dt_stride_t).pair(), par);
-        sum = sum + g.la;
-        R = g.a * (own(dyp + (int64_t)(t - 1) * p.dy_stride_t).pair() + R);
-    }
+    };
+    if (__all_sync(0xffffffffu, in1)) walk(std::true_type());
+    else walk(std::false_type());
     const float2 A = un(ex2(sum)), r = un(R);
     float *o = f.maps + at * p.D + c;
     const int64_t plane = p.B * f.nchunk * p.D;
-    o[0] = A.x, o[plane] = r.x;
+    if (in0) o[0] = A.x, o[plane] = r.x;
     if (in1) o[kSecond] = A.y, o[plane + kSecond] = r.y;
 }
 
-// c at the end of every chunk (third plane) and before the first (dh0): 16
+// c at the end of every chunk (third plane) and before the first (dh0): 64
 // segments of a sequence's chunks, each composed, then walked from the c that
-// enters it; 32 channels a block.
-__global__ void __launch_bounds__(512) gated_carry_kernel(BwdArgs f) {
-    __shared__ float2 seg[16][32];
+// enters it; 16 channels a block, so that there are blocks for half of the SMs
+// and a thread's loads are in flight together (512 chunks of 1024: 7.7 us, with 32
+// channels and 16 segments 10.6).
+__global__ void __launch_bounds__(1024) gated_carry_kernel(BwdArgs f) {
+    constexpr int kSegs = 64, kChan = 16;
+    __shared__ float2 seg[kSegs][kChan];
     const hm_gated_scan_bwd_args &p = f.p;
-    const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x, b = blockIdx.y, plane = p.B * f.nchunk * p.D;
+    const int x = threadIdx.x % kChan, s = threadIdx.x / kChan;
+    const int64_t c = (int64_t)blockIdx.x * kChan + x, b = blockIdx.y, plane = p.B * f.nchunk * p.D;
     const bool on = c < p.D;
     const int n = (int)clamped_len(p.lengths, b, p.L), chunks = (n + kChunk - 1) / kChunk;
-    const int s = threadIdx.y, S = (chunks + 15) / 16, lo = s * S, hi = min(lo + S, chunks);
+    const int S = (chunks + kSegs - 1) / kSegs, lo = min(s * S, chunks), hi = min(lo + S, chunks);
     const float *__restrict__ A = f.maps + b * f.nchunk * p.D + c;
     const float *__restrict__ R = A + plane;
     float *__restrict__ out = f.maps + 2 * plane + b * f.nchunk * p.D + c;
@@ -870,10 +888,11 @@ __global__ void __launch_bounds__(512) gated_carry_kernel(BwdArgs f) {
             a *= m;
         }
     }
-    seg[s][threadIdx.x] = make_float2(a, r);
+    seg[s][x] = make_float2(a, r);
     float v = on && p.dh_out ? p.dh_out[b * p.D + c] : 0.f;
     __syncthreads();
-    for (int k = 15; k > s; --k) v = fmaf(seg[k][threadIdx.x].x, v, seg[k][threadIdx.x].y);
+#pragma unroll 4
+    for (int k = kSegs - 1; k > s; --k) v = fmaf(seg[k][x].x, v, seg[k][x].y);
     if (!on) return;
 #pragma unroll 8
     for (int k = hi - 1; k >= lo; --k) {
@@ -1047,16 +1066,18 @@ struct Split {
 // 4 x 2, 4, 8: 52, 38, 46.  Padded batches count half their tokens (fp32 5 x
 // up to 1531 x 1001: 4 x 2, 4, 8: 121, 64, 39).
 //
-// Clusters are of at most 8 blocks, or 16 where even those leave SMs idle
-// (fp32 1 x 16384 x 512: 57 -> 42 us; bf16 1 x 32768 x 300: 105 -> 60, 1 x 4096 x 512:
-// 14.8 -> 12.8); with more channels 16 do not find room (32768 x 2048, above).
-int most_blocks(int64_t units) { return units * 16 <= 148 ? 16 : 8; }
+// Clusters are of at most 8 blocks, or 16 where 8 leave SMs idle or half used and
+// 16 find room (fp32 1 x 16384 x 512: 57 -> 42 us, 1 x 4096 x 700: 18.9 -> 14.8, but 1 x
+// 16384 x 1024: 68 -> 75; bf16 1 x 32768 x 300: 105 -> 60, 1 x 32768 x 1024: 102 -> 97, 1 x
+// 2048 x 1024: 12.7 -> 10.6, but 2 x 8192 x 512: 29 -> 31; with more channels,
+// 32768 x 2048 above).
+int most_blocks(int64_t units, hm_dtype t) { return units * 16 <= (t == HM_BF16 ? 296 : 192) ? 16 : 8; }
 
 Split split_of(int64_t units, int64_t L, hm_dtype t, bool padded) {
     const int64_t runs = (L + kR - 1) / kR, warps = t == HM_BF16 && L > 2048 ? 8 : 4;
     const int64_t most = (t == HM_BF16 ? 148 * 16 : 148 * 12) * (padded ? 2 : 1);
     Split s{(int)warps, 1};
-    const int lim = most_blocks(units);
+    const int lim = most_blocks(units, t);
     while (s.cluster < lim && units * s.cluster * 2 * warps <= most && warps * s.cluster < runs &&
            (runs >= 2 * warps * s.cluster * 2 || units * s.cluster * 2 <= 148))
         s.cluster *= 2;
@@ -1069,17 +1090,16 @@ Split split_of(int64_t units, int64_t L, hm_dtype t, bool padded) {
 // 4096 x 512: 42 -> 38); fp32 4 x 2885 x 128: 38 -> 42.
 Split bwd_split(int64_t units, int64_t L, hm_dtype t) {
     const int64_t chunks = (L + kChunk - 1) / kChunk;
-    const int lim = t == HM_BF16 ? most_blocks(units) : 8;
+    const int lim = t == HM_BF16 ? most_blocks(units, t) : 8;
     Split s{kWb, 1};
     while (s.cluster < lim && units * s.cluster * 2 <= 148 * 2 && s.cluster < chunks) s.cluster *= 2;
     return s;
 }
 // Two passes, for long sequences of so few channels that clusters of 8 leave
 // SMs idle; a sequence's chunks then go to two blocks on every SM.  Forward and
-// backward, one pass and two: fp32 1 x 16384 x 1024: 236, 202 us; bf16 1 x 32768 x
-// 512: 185, 165; 1 x 16384 x 64: 77, 59; but 1 x 8192 x 1024: 93, 91; 1 x 4096 x
-// 512: 38, 45; 1 x 32768 x 2048: 388, 463 (what is read twice costs more than the
-// waits).
+// backward, one pass and two: fp32 1 x 16384 x 1024: 236, 178 us; bf16 1 x 32768 x
+// 1024: 316, 229; 1 x 32768 x 512: 185, 138; 1 x 16384 x 64: 77, 55; but 1 x 4096 x 512:
+// 38, 45; 1 x 32768 x 2048: 388, 463 (what is read twice costs more than the waits).
 bool two_passes(int64_t units, int64_t L) { return units * 8 <= 148 && L > 8192; }
 int bwd_blocks(int64_t units, int64_t L, hm_dtype t) {
     if (!two_passes(units, L)) return bwd_split(units, L, t).cluster;
@@ -1291,8 +1311,8 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
                                 (size_t)2 * (2 * kWb + sp.cluster) * 32 * sizeof(Map2);
             auto go = [&](auto kernel, auto adjoint) {
                 if (two) {
-                    adjoint<<<(unsigned)((units * f.nchunk + 7) / 8), 256, 0, s>>>(f);
-                    gated_carry_kernel<<<dim3((unsigned)((a->D + 31) / 32), (unsigned)a->B), dim3(32, 16), 0, s>>>(f);
+                    adjoint<<<(unsigned)((units * f.nchunk + 3) / 4), 128, 0, s>>>(f);
+                    gated_carry_kernel<<<dim3((unsigned)((a->D + 15) / 16), (unsigned)a->B), 1024, 0, s>>>(f);
                     count_launches(2);
                     const cudaError_t e = cudaGetLastError();
                     if (e != cudaSuccess) return e;
