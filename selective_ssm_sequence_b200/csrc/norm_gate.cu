@@ -20,21 +20,20 @@ namespace hm {
 
 namespace {
 
-constexpr int kE = 8;       // elements of a thread per piece
-constexpr int kP = kE / 2;  // pairs
-
-// Columns of thread `tid` of a team of nthr: with VEC pieces of 8 consecutive
-// elements, else single elements a team's width apart (both coalesced).
-template <bool VEC>
+// A thread's piece of a row is E elements, 16 bytes (fp32 pieces of 32 bytes
+// would leave a warp's loads half of every sector apart).  Columns of thread
+// `tid` of a team of nthr: with VEC E consecutive elements, else single ones a
+// team's width apart (both coalesced).
+template <bool VEC, int kE>
 __device__ __forceinline__ int col_of(int piece, int j, int tid, int nthr) {
     return VEC ? (piece * nthr + tid) * kE + j : (piece * kE + j) * nthr + tid;
 }
 
-// 8 elements as loaded
-template <typename T>
+// E elements as loaded
+template <typename T, int E>
 struct Raw8;
 template <>
-struct Raw8<__nv_bfloat16> {
+struct Raw8<__nv_bfloat16, 8> {
     uint4 w;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
         asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -54,7 +53,26 @@ struct Raw8<__nv_bfloat16> {
     __device__ __forceinline__ void store(__nv_bfloat16 *p) const { __stcs(reinterpret_cast<uint4 *>(p), w); }
 };
 template <>
-struct Raw8<float> {
+struct Raw8<float, 4> {
+    float4 a;
+    __device__ __forceinline__ void load(const float *p) {
+        asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w)
+                     : "l"(p));
+    }
+    __device__ __forceinline__ void zero() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void set(const F2 *f) {
+        const float2 u0 = un(f[0]), u1 = un(f[1]);
+        a = make_float4(u0.x, u0.y, u1.x, u1.y);
+    }
+    __device__ __forceinline__ void get(F2 *f) const {
+        f[0] = pk(a.x, a.y);
+        f[1] = pk(a.z, a.w);
+    }
+    __device__ __forceinline__ void store(float *p) const { __stcs(reinterpret_cast<float4 *>(p), a); }
+};
+template <>
+struct Raw8<float, 8> {
     float4 a, b;
     __device__ __forceinline__ void load(const float *p) {
         asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -83,39 +101,41 @@ struct Raw8<float> {
 };
 
 // a piece of a row; columns behind D are zero
-template <bool VEC, typename T>
-__device__ __forceinline__ Raw8<T> load8(const T *row, int piece, int tid, int nthr, int D) {
-    Raw8<T> r;
+template <bool VEC, int kE, typename T>
+__device__ __forceinline__ Raw8<T, kE> load8(const T *row, int piece, int tid, int nthr, int D) {
+    Raw8<T, kE> r;
     if (VEC) {
-        const int c = col_of<true>(piece, 0, tid, nthr);
+        const int c = col_of<true, kE>(piece, 0, tid, nthr);
         if (c < D) r.load(row + c);
         else r.zero();
     } else {
         float f[kE];
 #pragma unroll
         for (int j = 0; j < kE; ++j) {
-            const int c = col_of<false>(piece, j, tid, nthr);
+            const int c = col_of<false, kE>(piece, j, tid, nthr);
             f[j] = c < D ? hm_ld(row, c) : 0.f;
         }
-        const F2 g[kP] = {pk(f[0], f[1]), pk(f[2], f[3]), pk(f[4], f[5]), pk(f[6], f[7])};
+        F2 g[kE / 2];
+#pragma unroll
+        for (int j = 0; j < kE / 2; ++j) g[j] = pk(f[2 * j], f[2 * j + 1]);
         r.set(g);
     }
     return r;
 }
 
-template <bool VEC, typename T>
+template <bool VEC, int kE, typename T>
 __device__ __forceinline__ void store8(T *row, int piece, int tid, int nthr, int D, const F2 *f) {
     if (VEC) {
-        const int c = col_of<true>(piece, 0, tid, nthr);
+        const int c = col_of<true, kE>(piece, 0, tid, nthr);
         if (c < D) {
-            Raw8<T> r;
+            Raw8<T, kE> r;
             r.set(f);
             r.store(row + c);
         }
     } else {
 #pragma unroll
         for (int j = 0; j < kE; ++j) {
-            const int c = col_of<false>(piece, j, tid, nthr);
+            const int c = col_of<false, kE>(piece, j, tid, nthr);
             if (c < D) hm_st(row, c, j & 1 ? un(f[j / 2]).y : un(f[j / 2]).x);
         }
     }
@@ -123,58 +143,58 @@ __device__ __forceinline__ void store8(T *row, int piece, int tid, int nthr, int
 
 // fp32 parameters of a thread's columns, of a piece that it has().  The same
 // for every row, so they stay in L1, which the rows themselves pass by.
-template <bool VEC>
+template <bool VEC, int kE>
 __device__ __forceinline__ void param8(const float *p, int piece, int tid, int nthr, int D, F2 *f) {
     if (VEC) {
-        const int c = col_of<true>(piece, 0, tid, nthr);
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p + c));
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(p + c + 4));
-        f[0] = pk(a.x, a.y);
-        f[1] = pk(a.z, a.w);
-        f[2] = pk(b.x, b.y);
-        f[3] = pk(b.z, b.w);
+        const float *q = p + col_of<true, kE>(piece, 0, tid, nthr);
+#pragma unroll
+        for (int j = 0; j < kE / 4; ++j) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(q) + j);
+            f[2 * j] = pk(a.x, a.y);
+            f[2 * j + 1] = pk(a.z, a.w);
+        }
     } else {
         float v[kE];
 #pragma unroll
         for (int j = 0; j < kE; ++j) {
-            const int c = col_of<VEC>(piece, j, tid, nthr);
+            const int c = col_of<false, kE>(piece, j, tid, nthr);
             v[j] = c < D ? __ldg(p + c) : 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < kP; ++j) f[j] = pk(v[2 * j], v[2 * j + 1]);
+        for (int j = 0; j < kE / 2; ++j) f[j] = pk(v[2 * j], v[2 * j + 1]);
     }
 }
 
 // u * p, u + p; a NULL p leaves u
-template <bool VEC>
+template <bool VEC, int kE>
 __device__ __forceinline__ void times(F2 *u, const float *p, int piece, int tid, int nthr, int D) {
     if (!p) return;
-    F2 w[kP];
-    param8<VEC>(p, piece, tid, nthr, D, w);
+    F2 w[kE / 2];
+    param8<VEC, kE>(p, piece, tid, nthr, D, w);
 #pragma unroll
-    for (int j = 0; j < kP; ++j) u[j] = u[j] * w[j];
+    for (int j = 0; j < kE / 2; ++j) u[j] = u[j] * w[j];
 }
-template <bool VEC>
+template <bool VEC, int kE>
 __device__ __forceinline__ void plus(F2 *u, const float *p, int piece, int tid, int nthr, int D) {
     if (!p) return;
-    F2 w[kP];
-    param8<VEC>(p, piece, tid, nthr, D, w);
+    F2 w[kE / 2];
+    param8<VEC, kE>(p, piece, tid, nthr, D, w);
 #pragma unroll
-    for (int j = 0; j < kP; ++j) u[j] = u[j] + w[j];
+    for (int j = 0; j < kE / 2; ++j) u[j] = u[j] + w[j];
 }
 
-// whether a thread has any element of the piece; with VEC (D a multiple of 8) all or none
-template <bool VEC>
+// whether a thread has any element of the piece; with VEC (D a multiple of E) all or none
+template <bool VEC, int kE>
 __device__ __forceinline__ bool has(int piece, int tid, int nthr, int D) {
-    return col_of<VEC>(piece, 0, tid, nthr) < D;
+    return col_of<VEC, kE>(piece, 0, tid, nthr) < D;
 }
 // f with the elements behind D set to zero (VEC: for a piece that has(); nothing to do)
-template <bool VEC>
+template <bool VEC, int kE>
 __device__ __forceinline__ F2 in_row(F2 f, int piece, int j, int tid, int nthr, int D) {
     if (VEC) return f;
     const float2 u = un(f);
-    return pk(col_of<false>(piece, 2 * j, tid, nthr) < D ? u.x : 0.f,
-              col_of<false>(piece, 2 * j + 1, tid, nthr) < D ? u.y : 0.f);
+    return pk(col_of<false, kE>(piece, 2 * j, tid, nthr) < D ? u.x : 0.f,
+              col_of<false, kE>(piece, 2 * j + 1, tid, nthr) < D ? u.y : 0.f);
 }
 
 __device__ __forceinline__ float sum2(F2 f) {
@@ -253,18 +273,19 @@ template <typename T, bool VEC, int NV, int TEAM, bool LAYER>
 __global__ void __launch_bounds__(TEAM ? 128 : 512, 1) norm_gate_fwd_kernel(hm_norm_gate_args p) {
     __shared__ float red[2][kMaxWarps][4];
     int turn = 0;
+    constexpr int kE = 16 / (int)sizeof(T), kP = kE / 2;
     constexpr int kTeam = TEAM ? TEAM : 1;
     const int tid = TEAM ? threadIdx.x % kTeam : threadIdx.x, nthr = TEAM ? TEAM : blockDim.x;
     const float inv = 1.f / (float)p.D;
     const int64_t row = TEAM ? (int64_t)blockIdx.x * (128 / kTeam) + threadIdx.x / kTeam : (int64_t)blockIdx.x;
     if (row >= p.rows && (TEAM == 0 || TEAM == 32)) return;         // whole teams
     const int D = row < p.rows ? (int)p.D : 0;
-    Raw8<T> ry[NV], rg[NV], rr[NV];
+    Raw8<T, kE> ry[NV], rg[NV], rr[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        ry[k] = load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
-        if (p.gate) rg[k] = load8<VEC>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D);
-        if (p.r) rr[k] = load8<VEC>((const T *)p.r + row * p.r_stride, k, tid, nthr, D);
+        ry[k] = load8<VEC, kE>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
+        if (p.gate) rg[k] = load8<VEC, kE>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D);
+        if (p.r) rr[k] = load8<VEC, kE>((const T *)p.r + row * p.r_stride, k, tid, nthr, D);
         else rr[k].zero();
     }
     float mean = 0.f, rstd = 1.f;
@@ -282,11 +303,11 @@ __global__ void __launch_bounds__(TEAM ? 128 : 512, 1) norm_gate_fwd_kernel(hm_n
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (LAYER && !has<VEC>(k, tid, nthr, D)) break;
+            if (LAYER && !has<VEC, kE>(k, tid, nthr, D)) break;
             ry[k].get(f);
 #pragma unroll
             for (int j = 0; j < kP; ++j) {
-                const F2 d = LAYER ? in_row<VEC>(f[j] + splat(-mean), k, j, tid, nthr, D) : f[j];
+                const F2 d = LAYER ? in_row<VEC, kE>(f[j] + splat(-mean), k, j, tid, nthr, D) : f[j];
                 v = fma(d, d, v);
             }
         }
@@ -295,29 +316,29 @@ __global__ void __launch_bounds__(TEAM ? 128 : 512, 1) norm_gate_fwd_kernel(hm_n
     F2 r[NV][kP], v = splat(0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        if (!has<VEC>(k, tid, nthr, D)) break;
+        if (!has<VEC, kE>(k, tid, nthr, D)) break;
         F2 u[kP], c[kP];
         ry[k].get(u);
         rr[k].get(r[k]);
         if (p.post) {
 #pragma unroll
             for (int j = 0; j < kP; ++j) u[j] = (LAYER ? u[j] + splat(-mean) : u[j]) * splat(rstd);
-            times<VEC>(u, p.post_w, k, tid, nthr, D);
-            plus<VEC>(u, p.post_b, k, tid, nthr, D);
+            times<VEC, kE>(u, p.post_w, k, tid, nthr, D);
+            plus<VEC, kE>(u, p.post_b, k, tid, nthr, D);
         }
         if (p.gate) {
             rg[k].get(c);
 #pragma unroll
             for (int j = 0; j < kP; ++j) u[j] = u[j] * (c[j] * sigmoid(c[j]));
         }
-        times<VEC>(u, p.scale, k, tid, nthr, D);
+        times<VEC, kE>(u, p.scale, k, tid, nthr, D);
 #pragma unroll
         for (int j = 0; j < kP; ++j) {
             // columns behind D hold zero, for the sums below
-            r[k][j] = in_row<VEC>(fma(splat(p.alpha), u[j], r[k][j]), k, j, tid, nthr, D);
+            r[k][j] = in_row<VEC, kE>(fma(splat(p.alpha), u[j], r[k][j]), k, j, tid, nthr, D);
             v = LAYER ? v + r[k][j] : fma(r[k][j], r[k][j], v);
         }
-        if (p.r_out) store8<VEC>((T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D, r[k]);
+        if (p.r_out) store8<VEC, kE>((T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D, r[k]);
     }
     if (!p.xn) return;
     float q = team_sum<TEAM>(sum2(v), red, turn);
@@ -327,10 +348,10 @@ __global__ void __launch_bounds__(TEAM ? 128 : 512, 1) norm_gate_fwd_kernel(hm_n
         v = splat(0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (!has<VEC>(k, tid, nthr, D)) break;
+            if (!has<VEC, kE>(k, tid, nthr, D)) break;
 #pragma unroll
             for (int j = 0; j < kP; ++j) {
-                const F2 d = in_row<VEC>(r[k][j] + splat(-mean), k, j, tid, nthr, D);
+                const F2 d = in_row<VEC, kE>(r[k][j] + splat(-mean), k, j, tid, nthr, D);
                 v = fma(d, d, v);
             }
         }
@@ -339,12 +360,12 @@ __global__ void __launch_bounds__(TEAM ? 128 : 512, 1) norm_gate_fwd_kernel(hm_n
     rstd = rsqrtf(q * inv + p.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        if (!has<VEC>(k, tid, nthr, D)) break;
+        if (!has<VEC, kE>(k, tid, nthr, D)) break;
 #pragma unroll
         for (int j = 0; j < kP; ++j) r[k][j] = (LAYER ? r[k][j] + splat(-mean) : r[k][j]) * splat(rstd);
-        times<VEC>(r[k], p.pre_w, k, tid, nthr, D);
-        plus<VEC>(r[k], p.pre_b, k, tid, nthr, D);
-        store8<VEC>((T *)p.xn + row * p.xn_stride, k, tid, nthr, D, r[k]);
+        times<VEC, kE>(r[k], p.pre_w, k, tid, nthr, D);
+        plus<VEC, kE>(r[k], p.pre_b, k, tid, nthr, D);
+        store8<VEC, kE>((T *)p.xn + row * p.xn_stride, k, tid, nthr, D, r[k]);
     }
 }
 
@@ -360,6 +381,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1)
 norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
     __shared__ float red[2][kMaxWarps][4];
     int turn = 0;
+    constexpr int kE = 16 / (int)sizeof(T), kP = kE / 2;
     constexpr int kTeam = TEAM ? TEAM : 1, kRows = TEAM ? 32 / kTeam : 1;       // rows of a warp, or block
     const bool gate = FULL || p.gate, post = FULL || p.post, pre = FULL || p.dxn;
     const int tid = TEAM ? threadIdx.x % kTeam : threadIdx.x, nthr = TEAM ? TEAM : blockDim.x;
@@ -374,18 +396,18 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int j = 0; j < kP; ++j) acc[i][k][j] = splat(0.f);
-    Raw8<T> ry[NV], rg[NV], rr[NV], rd[NV], re[NV];
+    Raw8<T, kE> ry[NV], rg[NV], rr[NV], rd[NV], re[NV];
     auto fetch = [&](int64_t row) {
         const int D = row < p.rows ? (int)p.D : 0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            ry[k] = load8<VEC>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
-            if (gate) rg[k] = load8<VEC>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D);
+            ry[k] = load8<VEC, kE>((const T *)p.y + row * p.y_stride, k, tid, nthr, D);
+            if (gate) rg[k] = load8<VEC, kE>((const T *)p.gate + row * p.gate_stride, k, tid, nthr, D);
             if (pre) {
-                rr[k] = load8<VEC>((const T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D);
-                re[k] = load8<VEC>((const T *)p.dxn + row * p.dxn_stride, k, tid, nthr, D);
+                rr[k] = load8<VEC, kE>((const T *)p.r_out + row * p.r_out_stride, k, tid, nthr, D);
+                re[k] = load8<VEC, kE>((const T *)p.dxn + row * p.dxn_stride, k, tid, nthr, D);
             }
-            if (FULL || p.dr_out) rd[k] = load8<VEC>((const T *)p.dr_out + row * p.dr_out_stride, k, tid, nthr, D);
+            if (FULL || p.dr_out) rd[k] = load8<VEC, kE>((const T *)p.dr_out + row * p.dr_out_stride, k, tid, nthr, D);
             else rd[k].zero();
         }
     };
@@ -416,11 +438,11 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
             const F2 my = splat(post ? -v.x * inv : 0.f), mr = splat(-v.y * inv);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                if (!has<VEC>(k, tid, nthr, D)) break;
+                if (!has<VEC, kE>(k, tid, nthr, D)) break;
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
-                    y[k][j] = in_row<VEC>(y[k][j] + my, k, j, tid, nthr, D);
-                    if (pre) r[k][j] = in_row<VEC>(r[k][j] + mr, k, j, tid, nthr, D);
+                    y[k][j] = in_row<VEC, kE>(y[k][j] + my, k, j, tid, nthr, D);
+                    if (pre) r[k][j] = in_row<VEC, kE>(r[k][j] + mr, k, j, tid, nthr, D);
                 }
             }
         }
@@ -430,12 +452,12 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
         v0 = v1 = splat(0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (!has<VEC>(k, tid, nthr, D)) break;
+            if (!has<VEC, kE>(k, tid, nthr, D)) break;
             if (pre) {
                 F2 we[kP];
 #pragma unroll
                 for (int j = 0; j < kP; ++j) we[j] = e[k][j];
-                times<VEC>(we, p.pre_w, k, tid, nthr, D);        // zero behind D
+                times<VEC, kE>(we, p.pre_w, k, tid, nthr, D);        // zero behind D
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
                     v1 = fma(r[k][j], r[k][j], v1);
@@ -452,7 +474,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
         v0 = v1 = splat(0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (!has<VEC>(k, tid, nthr, D)) break;
+            if (!has<VEC, kE>(k, tid, nthr, D)) break;
             if (pre) {
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
@@ -461,23 +483,23 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
                     acc[4][k][j] = acc[4][k][j] + e[k][j];
                     d[k][j] = fma(u, splat(r1), LAYER ? d[k][j] + splat(r0) : d[k][j]);
                 }
-                times<VEC>(e[k], p.pre_w, k, tid, nthr, D);
+                times<VEC, kE>(e[k], p.pre_w, k, tid, nthr, D);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) d[k][j] = fma(e[k][j], splat(rsr), d[k][j]);
             }
-            if (FULL || p.dr) store8<VEC>((T *)p.dr + row * p.dr_stride, k, tid, nthr, D, d[k]);
+            if (FULL || p.dr) store8<VEC, kE>((T *)p.dr + row * p.dr_stride, k, tid, nthr, D, d[k]);
             F2 n[kP], dm[kP];
 #pragma unroll
             for (int j = 0; j < kP; ++j) {
                 if (post) y[k][j] = y[k][j] * splat(rsy);
                 n[j] = y[k][j];
-                d[k][j] = dm[j] = in_row<VEC>(d[k][j], k, j, tid, nthr, D) * splat(p.alpha);
+                d[k][j] = dm[j] = in_row<VEC, kE>(d[k][j], k, j, tid, nthr, D) * splat(p.alpha);
             }
             if (post) {
-                times<VEC>(n, p.post_w, k, tid, nthr, D);
-                plus<VEC>(n, p.post_b, k, tid, nthr, D);
+                times<VEC, kE>(n, p.post_w, k, tid, nthr, D);
+                plus<VEC, kE>(n, p.post_b, k, tid, nthr, D);
             }
-            times<VEC>(dm, p.scale, k, tid, nthr, D);
+            times<VEC, kE>(dm, p.scale, k, tid, nthr, D);
             if (gate) {
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
@@ -487,7 +509,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
                     g[k][j] = dm[j] * n[j] * fma(si, splat(1.f) - sg, sg);
                     d[k][j] = dm[j] * si;
                 }
-                store8<VEC>((T *)p.dgate + row * p.dgate_stride, k, tid, nthr, D, g[k]);
+                store8<VEC, kE>((T *)p.dgate + row * p.dgate_stride, k, tid, nthr, D, g[k]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
@@ -502,7 +524,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
                     acc[1][k][j] = fma(d[k][j], y[k][j], acc[1][k][j]);
                     acc[2][k][j] = acc[2][k][j] + d[k][j];
                 }
-                times<VEC>(d[k], p.post_w, k, tid, nthr, D);
+                times<VEC, kE>(d[k], p.post_w, k, tid, nthr, D);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
                     if (LAYER) v0 = v0 + d[k][j];
@@ -528,7 +550,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
                 }
         }
 #pragma unroll
-        for (int k = 0; k < NV; ++k) store8<VEC>((T *)p.dy + row * p.dy_stride, k, tid, nthr, D, d[k]);
+        for (int k = 0; k < NV; ++k) store8<VEC, kE>((T *)p.dy + row * p.dy_stride, k, tid, nthr, D, d[k]);
     }
     const int D = (int)p.D;
 #pragma unroll
@@ -537,7 +559,7 @@ norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int j = 0; j < kE; ++j) {
-                const int c = col_of<VEC>(k, j, tid, nthr);
+                const int c = col_of<VEC, kE>(k, j, tid, nthr);
                 float v = j & 1 ? un(acc[i][k][j / 2]).y : un(acc[i][k][j / 2]).x;
                 if (TEAM)
 #pragma unroll
@@ -606,7 +628,7 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
     extern __shared__ __align__(16) uint4 tile[];
     __shared__ float red[2][THREADS / 32][8];
     float4 *sums = reinterpret_cast<float4 *>(tile);       // FAR: [5][2][threads]
-    constexpr int Q = kE * (int)sizeof(T) / 16;
+    constexpr int kE = 8, kP = kE / 2, Q = kE * (int)sizeof(T) / 16;
     int turn = 0;
     const int tid = threadIdx.x, nthr = blockDim.x, D = (int)p.D, c = tid * kE;
     const bool live = c < D;
@@ -666,14 +688,14 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
         if (!FAR) asm volatile("cp.async.wait_group 1;" ::: "memory");
         auto get = [&](int k, int a, F2 *f) {
             if (FAR) {
-                Raw8<T> r;
+                Raw8<T, kE> r;
                 if (live) r.load(base[a] + g * strides[a] + c);
                 else r.zero();
                 r.get(f);
                 return;
             }
             const uint4 *q = &tile[((s * R + k) * 5 + a) * Q * nthr + tid];
-            Raw8<T> r;
+            Raw8<T, kE> r;
             if constexpr (Q == 1) {
                 r.w = q[0];
             } else {
@@ -707,7 +729,7 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
                     get(k, 0, y);
                     get(k, 2, r);
                     get(k, 4, e);
-                    times<true>(e, p.pre_w, 0, tid, nthr, D);
+                    times<true, kE>(e, p.pre_w, 0, tid, nthr, D);
 #pragma unroll
                     for (int j = 0; j < kP; ++j) {
                         const F2 yc = LAYER ? y[j] + splat(my[k]) : y[j], rc = LAYER ? r[j] + splat(mr[k]) : r[j];
@@ -745,10 +767,10 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
                 }
                 add(3, e, u);
                 add(4, e, one);
-                times<true>(e, p.pre_w, 0, tid, nthr, D);
+                times<true, kE>(e, p.pre_w, 0, tid, nthr, D);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) d[j] = fma(e[j], splat(rsr[k]), d[j]);
-                if (row < p.rows) store8<true>((T *)p.dr + row * p.dr_stride, 0, tid, nthr, D, d);
+                if (row < p.rows) store8<true, kE>((T *)p.dr + row * p.dr_stride, 0, tid, nthr, D, d);
                 F2 y[kP], n[kP], gt[kP];
                 get(k, 0, y);
                 get(k, 1, gt);
@@ -759,9 +781,9 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
                     d[j] = d[j] * splat(p.alpha);
                     dn[k][j] = d[j];
                 }
-                times<true>(n, p.post_w, 0, tid, nthr, D);
-                plus<true>(n, p.post_b, 0, tid, nthr, D);
-                times<true>(dn[k], p.scale, 0, tid, nthr, D);
+                times<true, kE>(n, p.post_w, 0, tid, nthr, D);
+                plus<true, kE>(n, p.post_b, 0, tid, nthr, D);
+                times<true, kE>(dn[k], p.scale, 0, tid, nthr, D);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
                     const F2 sg = sigmoid(gt[j]), si = gt[j] * sg;
@@ -772,8 +794,8 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
                 add(0, d, n);
                 add(1, dn[k], y);
                 add(2, dn[k], one);
-                if (row < p.rows) store8<true>((T *)p.dgate + row * p.dgate_stride, 0, tid, nthr, D, gt);
-                times<true>(dn[k], p.post_w, 0, tid, nthr, D);
+                if (row < p.rows) store8<true, kE>((T *)p.dgate + row * p.dgate_stride, 0, tid, nthr, D, gt);
+                times<true, kE>(dn[k], p.post_w, 0, tid, nthr, D);
                 F2 v0 = splat(0.f), v1 = v0;
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
@@ -798,7 +820,7 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
                     const F2 q = fma(y[j], y1, dn[k][j]);
                     y[j] = splat(rsy[k]) * (LAYER ? q + y0 : q);
                 }
-                if (row < p.rows) store8<true>((T *)p.dy + row * p.dy_stride, 0, tid, nthr, D, y);
+                if (row < p.rows) store8<true, kE>((T *)p.dy + row * p.dy_stride, 0, tid, nthr, D, y);
             }
         }
         fetch(g + 2 * (int64_t)gridDim.x, s);              // over what this thread has read
@@ -857,6 +879,9 @@ constexpr int64_t kMaxD = 16384;
 
 size_t esize(hm_dtype t) { return t == HM_BF16 ? 2 : 4; }
 
+// smallest number of lanes, 8, 16 or 32, that have a whole row of one piece each
+int lanes_of(int64_t D, size_t es) { return D * es <= 8 * 16 ? 8 : D * es <= 16 * 16 ? 16 : 32; }
+
 hm_status check_seam(const char *who, int64_t rows, int64_t D, hm_dtype t, int norm, float eps, float alpha) {
     if (t != HM_F32 && t != HM_BF16) return fail_args(HM_ERR_INVALID_ARG, "%s: bad io dtype", who);
     if (norm != HM_NORM_RMS && norm != HM_NORM_LAYER) return fail_args(HM_ERR_INVALID_ARG, "%s: bad norm %d", who, norm);
@@ -884,20 +909,21 @@ bool wide(const Row &r, size_t es) {
 }
 
 struct Team {
-    int nthr, nv;        // threads that share a row (up to 32: of one warp), pieces of 8 columns per thread
+    int nthr, nv;        // threads that share a row (up to 32: of one warp), pieces of 16 bytes per thread
     int blocks;          // backward
 };
 
-// Forward: up to 4 pieces a lane (2 of fp32, as many registers): 2048 bf16
-// columns over 2 warps took 117 us for 32768 rows, over 1 warp of 8 pieces 134,
-// over 4 warps 121, over 8 157.  More warps for wider rows, and for so few
-// rows that these would leave most of the GPU idle.
-// Rows of up to 64 or 128 columns share a warp (320719 rows of 64, bf16: 117 -> 37 us).
+// Forward: up to 4 pieces a lane: 2048 bf16 columns over 2 warps took 117 us for
+// 32768 rows, over 1 warp of 8 pieces 134, over 4 warps 121, over 8 157.  More
+// warps for wider rows, and for so few rows that these would leave most of the
+// GPU idle.
+// Rows of up to 256 bytes share a warp (320719 rows of 64, bf16: 117 -> 37 us).
 // Rows that are read element by element get a block with as few pieces as it can.
 Team fwd_team(int64_t rows, int64_t D, size_t es, bool vec) {
-    const int pieces = (int)((D + 32 * kE - 1) / (32 * kE)), most = !vec ? (D > 8192 ? 4 : D > 4096 ? 2 : 1) : es == 2 || D > 8192 ? 4 : 2;
+    const int columns = 32 * 16 / (int)es, pieces = (int)((D + columns - 1) / columns), of8 = es == 2 ? 1 : 2;
+    const int most = !vec ? (D > 8192 ? 4 : D > 4096 ? 2 : 1) * of8 : es == 4 && D > 8192 ? 8 : 4;
     int warps = 1;
-    if (vec && D <= 128) return {D <= 64 ? 8 : 16, 1, 0};
+    if (vec && lanes_of(D, es) < 32) return {lanes_of(D, es), 1, 0};
     while ((pieces + warps - 1) / warps > most) warps *= 2;
     while (warps < 16 && (pieces + warps - 1) / warps > 1 && rows * warps * 2 <= 148 * 16) warps *= 2;
     int nv = 1;
@@ -905,15 +931,15 @@ Team fwd_team(int64_t rows, int64_t D, size_t es, bool vec) {
     return {warps * 32, nv, 0};
 }
 
-// Backward: as many threads as there are pieces in a row, up to 512; blocks
-// (or warps) to fill the SMs once at 512 threads each.
-// Rows of up to 64 or 128 columns share a warp.
-Team bwd_team(int64_t rows, int64_t D) {
-    const int pieces = (int)((D + 32 * kE - 1) / (32 * kE));
-    int nv = 1;
+// Backward: 8 columns a thread (bf16 one piece, fp32 two), up to 512 threads, then
+// more; blocks (or warps) to fill the SMs once at 512 threads each.
+// Rows of up to 256 bytes share a warp.
+Team bwd_team(int64_t rows, int64_t D, size_t es) {
+    const int columns = 32 * 16 / (int)es, pieces = (int)((D + columns - 1) / columns);
+    int nv = es == 4 && pieces > 1 ? 2 : 1;
     while (nv * 16 < pieces) nv *= 2;
-    const int warps = (pieces + nv - 1) / nv;
-    const int lanes = D <= 64 ? 8 : D <= 128 ? 16 : 32, of_block = 8 * 32 / lanes;     // rows of a block of warps
+    const int warps = (pieces + nv - 1) / nv, lanes = lanes_of(D, es);
+    const int of_block = 8 * 32 / lanes;                               // rows of a block of warps
     const int64_t most = warps == 1 ? 148 * 2 : 148 * (16 / warps);
     const int64_t need = warps == 1 ? (rows + of_block - 1) / of_block : rows;
     return {warps == 1 ? lanes : warps * 32, nv, (int)(need < most ? need : most)};
@@ -944,7 +970,7 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
                         {"r", a->r, a->r_stride, false},
                         {"r_out", a->r_out, a->r_out_stride, false},
                         {"xn", a->xn, a->xn_stride, false}};
-    bool vec = a->D % kE == 0;
+    bool vec = a->D * es % 16 == 0;
     for (const Row &r : rows) {
         HM_TRY(check_row(w, r, a->rows, a->D, es));
         vec = vec && wide(r, es);
@@ -975,12 +1001,14 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
         else if (t.nv == 2) HM_FWD_B(__nv_bfloat16, 2);
         else HM_FWD_B(__nv_bfloat16, 4);
     } else {
-        if (!vec) HM_FWD_S(float);
+        if (!vec && t.nv == 8) HM_FWD_Y(float, false, 8, 0);
+        else if (!vec) HM_FWD_S(float);
         else if (t.nthr == 8) HM_FWD_Y(float, true, 1, 8);
         else if (t.nthr == 16) HM_FWD_Y(float, true, 1, 16);
         else if (t.nv == 1) HM_FWD_B(float, 1);
         else if (t.nv == 2) HM_FWD_B(float, 2);
-        else HM_FWD_B(float, 4);
+        else if (t.nv == 4) HM_FWD_B(float, 4);
+        else HM_FWD_B(float, 8);
     }
 #undef HM_FWD
 #undef HM_FWD_Y
@@ -993,7 +1021,7 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
 
 extern "C" size_t hm_norm_gate_bwd_workspace_size(const hm_norm_gate_bwd_args *a) {
     if (!a || check_seam("norm_gate_bwd", a->rows, a->D, a->io_dtype, a->norm, a->eps, a->alpha) != HM_OK) return 0;
-    return (size_t)bwd_shares(bwd_team(a->rows, a->D)) * 5 * a->D * sizeof(float);
+    return (size_t)bwd_shares(bwd_team(a->rows, a->D, esize(a->io_dtype))) * 5 * a->D * sizeof(float);
 }
 
 extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_t stream) {
@@ -1010,7 +1038,7 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
                         {"dy", a->dy, a->dy_stride, true},
                         {"dgate", a->gate ? a->dgate : nullptr, a->dgate_stride, a->gate != nullptr},
                         {"dr", a->dr, a->dr_stride, false}};
-    bool vec = a->D % kE == 0;
+    bool vec = a->D * es % 16 == 0;
     for (const Row &r : rows) {
         HM_TRY(check_row(w, r, a->rows, a->D, es));
         vec = vec && wide(r, es);
@@ -1023,17 +1051,17 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     const size_t need = hm_norm_gate_bwd_workspace_size(a);
     if (need > 0 && (!a->workspace || a->workspace_bytes < need || ((uintptr_t)a->workspace & 255) != 0))
         return fail_args(HM_ERR_INVALID_ARG, "%s: workspace of %zu bytes, 256-byte aligned, is needed", w, need);
-    const Team t = bwd_team(a->rows, a->D);
+    const Team t = bwd_team(a->rows, a->D, es);
     int64_t shares = bwd_shares(t);
     cudaStream_t s = (cudaStream_t)stream;
     float *part = (float *)a->workspace;
     if (t.blocks > 0) {
         const bool full = a->gate && a->post && a->dxn && a->dr_out && a->dr;
-        const bool far = vec && full && a->D > 4096 && a->D <= 8192;
+        const bool far = vec && full && a->D % 8 == 0 && a->D > 4096 && a->D <= 8192;
         const bool tiled = far || (vec && full && es == 2 && a->D > 512 && t.nv == 1);
         auto rows_kernel = [&](auto kernel, int R) {
-            const int nthr = far ? (int)((a->D / kE + 31) / 32 * 32) : t.nthr;
-            const size_t smem = far ? (size_t)10 * sizeof(float4) * nthr : (size_t)2 * R * 5 * kE * es * nthr;
+            const int nthr = far ? (int)((a->D / 8 + 31) / 32 * 32) : t.nthr;
+            const size_t smem = far ? (size_t)10 * sizeof(float4) * nthr : (size_t)2 * R * 5 * 16 * nthr;
             const cudaError_t e = tc::ensure_smem_limit(kernel, (int)smem);
             if (e != cudaSuccess) return e;
             const int64_t groups = (a->rows + R - 1) / R;
@@ -1053,20 +1081,25 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     (V && full ? norm_gate_bwd_kernel<T, V, N, B, Y, V, Z><<<t.blocks, B ? 256 : t.nthr, 0, s>>>(*a, part)      \
                : norm_gate_bwd_kernel<T, V, N, B, Y, false, Z><<<t.blocks, B ? 256 : t.nthr, 0, s>>>(*a, part))
 #define HM_BWD(T, V, N, B, Z) (a->norm == HM_NORM_LAYER ? HM_BWD_F(T, V, N, B, true, Z) : HM_BWD_F(T, V, N, B, false, Z))
-#define HM_BWD_N(T, V)                                                                                      \
-    (t.nthr == 8 ? HM_BWD(T, V, 1, 8, 256)                                                                  \
-     : t.nthr == 16 ? HM_BWD(T, V, 1, 16, 256)                                                              \
-     : t.nthr == 32 ? HM_BWD(T, V, 1, 32, 256)                                                              \
+#define HM_BWD_WARP(T, V) (t.nthr == 8 ? HM_BWD(T, V, 1, 8, 256) : t.nthr == 16 ? HM_BWD(T, V, 1, 16, 256) : HM_BWD(T, V, 1, 32, 256))
+#define HM_BWD_16(T, V)                                                                                     \
+    (t.nthr <= 32 ? HM_BWD_WARP(T, V)                                                                       \
      : t.nv == 1 ? (t.nthr <= 256 ? HM_BWD(T, V, 1, 0, 256) : HM_BWD(T, V, 1, 0, 512))                      \
      : t.nv == 2 ? HM_BWD(T, V, 2, 0, 512) : HM_BWD(T, V, 4, 0, 512))
+#define HM_BWD_32(T, V)                                                                                     \
+    (t.nthr <= 32 ? (t.nv == 1 ? HM_BWD_WARP(T, V) : HM_BWD(T, V, 2, 32, 256))                              \
+     : t.nv == 2 ? (t.nthr <= 256 ? HM_BWD(T, V, 2, 0, 256) : HM_BWD(T, V, 2, 0, 512))                      \
+     : t.nv == 4 ? HM_BWD(T, V, 4, 0, 512) : HM_BWD(T, V, 8, 0, 512))
         if (tiled) {
             const cudaError_t e = a->norm == HM_NORM_LAYER ? rows_by(std::true_type()) : rows_by(std::false_type());
             if (e != cudaSuccess) return fail_args(HM_ERR_CUDA, "%s launch: %s", w, cudaGetErrorString(e));
-        } else if (a->io_dtype == HM_BF16) vec ? HM_BWD_N(__nv_bfloat16, true) : HM_BWD_N(__nv_bfloat16, false);
-        else vec ? HM_BWD_N(float, true) : HM_BWD_N(float, false);
+        } else if (a->io_dtype == HM_BF16) vec ? HM_BWD_16(__nv_bfloat16, true) : HM_BWD_16(__nv_bfloat16, false);
+        else vec ? HM_BWD_32(float, true) : HM_BWD_32(float, false);
 #undef HM_BWD
 #undef HM_BWD_F
-#undef HM_BWD_N
+#undef HM_BWD_WARP
+#undef HM_BWD_16
+#undef HM_BWD_32
         count_launches(1);
     }
     cudaError_t e = cudaGetLastError();

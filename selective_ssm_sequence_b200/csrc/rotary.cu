@@ -331,7 +331,9 @@ extern "C" hm_status hm_rotary(const hm_rotary_args *a, hm_stream_t stream) {
     r.tb = r.per >= kThreads ? 1 : kThreads / r.per;
     // blocks walk the tokens, so that the frequencies are formed once per block
     const unsigned blocks = (r.tokens + r.tb - 1) / r.tb;
-    const unsigned grid = blocks < 148 * 6 ? blocks : 148 * 6;
+    // (one wave where there is little to do, else shorter shares: 8192 tokens, a quarter of 16 heads
+    // of 256: 3, 6, 12 blocks per SM 27.4, 29.0, 29.0 us; 32768 whole heads 101, 94, 88)
+    const unsigned most = 148 * (blocks < 148 * 32 ? 3 : 12), grid = blocks < most ? blocks : most;
     cudaStream_t s = (cudaStream_t)stream;
     const bool inter = a->layout == HM_ROTARY_INTERLEAVED;
 #define HM_ROT(T, N)                                                     \
