@@ -13,8 +13,9 @@
 // the block composes them through shared memory and hands its own to every
 // block of the cluster (st.async into their shared memory, counted by an
 // mbarrier there), and each warp, now knowing its entering state, runs its
-// tokens once more out of registers.  So each input is read once from HBM,
-// there is one launch and no scratch, and every sum has a fixed order.
+// tokens once more out of registers.  So each input is read once from HBM in
+// one launch without scratch (but for the backward of long sequences of few
+// channels), and every sum has a fixed order.
 #include <type_traits>
 
 #include "packed.cuh"
@@ -542,9 +543,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // warps on an SM; x and dy are read again from shared memory.
 //
 // A long sequence of few channels does not fill the GPU with clusters.  There
-// the backward takes two passes (maps given): gated_adjoint_kernel forms every chunk's adjoint map from
-// dt and dy, gated_carry_kernel runs through them to the c that enters each
-// chunk, and here every chunk stands for itself; dt and dy are read twice.
+// the backward takes two passes (maps given): gated_adjoint_kernel forms every
+// chunk's adjoint map from dt and dy, gated_carry_kernel runs through them to
+// the c that enters each chunk, and here every chunk stands for itself; dt and
+// dy are read twice.
+//
+// 4 x 2048 x 2048 bf16: 56 us, 108 instructions per channel pair and token, 45 %
+// of the issue slots: bound by latency at 16 warps per SM.
 template <typename T, int SCALE, int MODE>
 __global__ void __launch_bounds__(kWb * 32, 2)
 gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_constant__ CUtensorMap map_x,

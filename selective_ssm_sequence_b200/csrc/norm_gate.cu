@@ -609,14 +609,15 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes
 }
 
 // The common case of the backward (every row array there, y normalised, rows on
-// 16-byte boundaries), for bf16 rows of 512 to 4096 columns: R rows at a time.
-// Their sums share the exchanges and barriers, and the rows wait in shared
-// memory (each thread's own columns, by cp.async, the next R behind them), which
-// leaves the registers to the parameter gradients.  8192 x 2048 layer norms:
-// 91 us against 95 with a row in registers, 260 x 2752 17.6 against 23.8; fp32
-// rows gain nothing (184 against 160) and narrow ones neither (65536 x 264: 128
-// against 122).  715 instructions per warp and row, half of the issue slots
-// used: latency at 16 warps per SM bounds it.
+// 16-byte boundaries), for bf16 rows of 256 to 4096 columns: R rows at a time.
+// Their sums share the exchanges and barriers, the rows wait in shared memory
+// (each thread's own columns, by cp.async, the next R behind them), which
+// leaves the registers to the parameter gradients, and so do the parameters
+// (from L1, 8 columns a thread, they cost 91 us in place of 77).  8192 x 2048
+// layer norms: 77 us against 95 with a row in registers, RMS 67 against 98, 4096 x
+// 4096 68 against 109, 32768 x 512 77 against 83; fp32 rows, with pieces of their
+// own half as wide, gained nothing.  What is left: issue slots and latency at
+// 16 warps per SM.
 //
 // FAR: rows of 4096 to 8192 columns of either type, one at a time over 1024
 // threads, whose registers have no room for rows nor sums: the parameter
@@ -625,10 +626,11 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes
 template <typename T, bool LAYER, int R, int THREADS, bool FAR>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1)
 norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
+    constexpr int kE = 8, kP = kE / 2, Q = kE * (int)sizeof(T) / 16;
     extern __shared__ __align__(16) uint4 tile[];
     __shared__ float red[2][THREADS / 32][8];
     float4 *sums = reinterpret_cast<float4 *>(tile);       // FAR: [5][2][threads]
-    constexpr int kE = 8, kP = kE / 2, Q = kE * (int)sizeof(T) / 16;
+    float4 *par = sums + 2 * R * 5 * Q * blockDim.x;    // else, behind the rows: [4][2][threads]
     int turn = 0;
     const int tid = threadIdx.x, nthr = blockDim.x, D = (int)p.D, c = tid * kE;
     const bool live = c < D;
@@ -660,6 +662,33 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
         }
     };
     const F2 one[kP] = {splat(1.f), splat(1.f), splat(1.f), splat(1.f)};
+    // the thread's parameters: pre_w, post_w, post_b, scale.  Not FAR: copied once into shared memory,
+    // 16 bytes a lane, since global loads of 8 fp32 columns leave their halves apart
+    const float *const params[4] = {p.pre_w, p.post_w, p.post_b, p.scale};
+    if (!FAR && live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float none = i == 2 ? 0.f : 1.f;
+                par[(i * 2 + h) * nthr + tid] = params[i] ? __ldg(reinterpret_cast<const float4 *>(params[i] + c) + h)
+                                                          : make_float4(none, none, none, none);
+            }
+    }
+    auto get_par = [&](int i, F2 *w) {
+        const float4 a = par[i * 2 * nthr + tid], b = par[(i * 2 + 1) * nthr + tid];
+        w[0] = pk(a.x, a.y), w[1] = pk(a.z, a.w), w[2] = pk(b.x, b.y), w[3] = pk(b.z, b.w);
+    };
+    auto by = [&](F2 *u, int i) {                  // u *= the i-th parameter
+        if (FAR) {
+            times<true, kE>(u, params[i], 0, tid, nthr, D);
+            return;
+        }
+        F2 w[kP];
+        get_par(i, w);
+#pragma unroll
+        for (int j = 0; j < kP; ++j) u[j] = u[j] * w[j];
+    };
     const T *const base[5] = {(const T *)p.y, (const T *)p.gate, (const T *)p.r_out, (const T *)p.dr_out, (const T *)p.dxn};
     const int64_t strides[5] = {p.y_stride, p.gate_stride, p.r_out_stride, p.dr_out_stride, p.dxn_stride};
     auto fetch = [&](int64_t g, int s) {
@@ -729,7 +758,7 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
                     get(k, 0, y);
                     get(k, 2, r);
                     get(k, 4, e);
-                    times<true, kE>(e, p.pre_w, 0, tid, nthr, D);
+                    by(e, 0);
 #pragma unroll
                     for (int j = 0; j < kP; ++j) {
                         const F2 yc = LAYER ? y[j] + splat(my[k]) : y[j], rc = LAYER ? r[j] + splat(mr[k]) : r[j];
@@ -767,7 +796,7 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
                 }
                 add(3, e, u);
                 add(4, e, one);
-                times<true, kE>(e, p.pre_w, 0, tid, nthr, D);
+                by(e, 0);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) d[j] = fma(e[j], splat(rsr[k]), d[j]);
                 if (row < p.rows) store8<true, kE>((T *)p.dr + row * p.dr_stride, 0, tid, nthr, D, d);
@@ -781,9 +810,17 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
                     d[j] = d[j] * splat(p.alpha);
                     dn[k][j] = d[j];
                 }
-                times<true, kE>(n, p.post_w, 0, tid, nthr, D);
-                plus<true, kE>(n, p.post_b, 0, tid, nthr, D);
-                times<true, kE>(dn[k], p.scale, 0, tid, nthr, D);
+                if (FAR) {
+                    times<true, kE>(n, p.post_w, 0, tid, nthr, D);
+                    plus<true, kE>(n, p.post_b, 0, tid, nthr, D);
+                } else {
+                    F2 w[kP], b[kP];
+                    get_par(1, w);
+                    get_par(2, b);
+#pragma unroll
+                    for (int j = 0; j < kP; ++j) n[j] = fma(n[j], w[j], b[j]);
+                }
+                by(dn[k], 3);
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
                     const F2 sg = sigmoid(gt[j]), si = gt[j] * sg;
@@ -795,7 +832,7 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
                 add(1, dn[k], y);
                 add(2, dn[k], one);
                 if (row < p.rows) store8<true, kE>((T *)p.dgate + row * p.dgate_stride, 0, tid, nthr, D, gt);
-                times<true, kE>(dn[k], p.post_w, 0, tid, nthr, D);
+                by(dn[k], 1);
                 F2 v0 = splat(0.f), v1 = v0;
 #pragma unroll
                 for (int j = 0; j < kP; ++j) {
@@ -831,13 +868,13 @@ norm_gate_bwd_rows_kernel(hm_norm_gate_bwd_args p, float *part) {
 #pragma unroll
         for (int i = 0; i < 10; ++i)
             *reinterpret_cast<float4 *>(part + ((int64_t)blockIdx.x * 5 + i / 2) * D + c + i % 2 * 4) = sums[i * nthr + tid];
-        return;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+#pragma unroll
+            for (int j = 0; j < kP; ++j)
+                *reinterpret_cast<float2 *>(part + ((int64_t)blockIdx.x * 5 + i) * D + c + 2 * j) = un(acc[i][j]);
     }
-#pragma unroll
-    for (int i = 0; i < (FAR ? 0 : 5); ++i)
-#pragma unroll
-        for (int j = 0; j < kP; ++j)
-            *reinterpret_cast<float2 *>(part + ((int64_t)blockIdx.x * 5 + i) * D + c + 2 * j) = un(acc[i][j]);
 }
 
 struct GradPtrs {
@@ -1058,14 +1095,16 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     if (t.blocks > 0) {
         const bool full = a->gate && a->post && a->dxn && a->dr_out && a->dr;
         const bool far = vec && full && a->D % 8 == 0 && a->D > 4096 && a->D <= 8192;
-        const bool tiled = far || (vec && full && es == 2 && a->D > 512 && t.nv == 1);
+        const bool tiled = far || (vec && full && es == 2 && a->D > 256 && t.nv == 1);
         auto rows_kernel = [&](auto kernel, int R) {
             const int nthr = far ? (int)((a->D / 8 + 31) / 32 * 32) : t.nthr;
-            const size_t smem = far ? (size_t)10 * sizeof(float4) * nthr : (size_t)2 * R * 5 * 16 * nthr;
+            const size_t smem = far ? (size_t)10 * sizeof(float4) * nthr : ((size_t)2 * R * 5 + 8) * 16 * nthr;
             const cudaError_t e = tc::ensure_smem_limit(kernel, (int)smem);
             if (e != cudaSuccess) return e;
-            const int64_t groups = (a->rows + R - 1) / R;
+            // one wave: what an SM's 228 KB hold of these blocks (1.5 KB: the sums, and what a block costs besides)
+            const int64_t groups = (a->rows + R - 1) / R, of_sm = (228 << 10) / (smem + 1536), wave = 148 * of_sm;
             shares = groups < t.blocks ? groups : t.blocks;
+            if (!far && shares > wave) shares = wave;
             kernel<<<(unsigned)shares, nthr, smem, s>>>(*a, part);
             return cudaGetLastError();
         };
@@ -1082,10 +1121,13 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
                : norm_gate_bwd_kernel<T, V, N, B, Y, false, Z><<<t.blocks, B ? 256 : t.nthr, 0, s>>>(*a, part))
 #define HM_BWD(T, V, N, B, Z) (a->norm == HM_NORM_LAYER ? HM_BWD_F(T, V, N, B, true, Z) : HM_BWD_F(T, V, N, B, false, Z))
 #define HM_BWD_WARP(T, V) (t.nthr == 8 ? HM_BWD(T, V, 1, 8, 256) : t.nthr == 16 ? HM_BWD(T, V, 1, 16, 256) : HM_BWD(T, V, 1, 32, 256))
+#define HM_BWD_P(T, V, N, B, Z)      /* where the full case has gone to the kernel above */                 \
+    (a->norm == HM_NORM_LAYER ? norm_gate_bwd_kernel<T, V, N, B, true, false, Z><<<t.blocks, t.nthr, 0, s>>>(*a, part) \
+                              : norm_gate_bwd_kernel<T, V, N, B, false, false, Z><<<t.blocks, t.nthr, 0, s>>>(*a, part))
 #define HM_BWD_16(T, V)                                                                                     \
     (t.nthr <= 32 ? HM_BWD_WARP(T, V)                                                                       \
-     : t.nv == 1 ? (t.nthr <= 256 ? HM_BWD(T, V, 1, 0, 256) : HM_BWD(T, V, 1, 0, 512))                      \
-     : t.nv == 2 ? HM_BWD(T, V, 2, 0, 512) : HM_BWD(T, V, 4, 0, 512))
+     : t.nv == 1 ? (t.nthr <= 256 ? HM_BWD_P(T, V, 1, 0, 256) : HM_BWD_P(T, V, 1, 0, 512))                  \
+     : t.nv == 2 ? HM_BWD_P(T, V, 2, 0, 512) : HM_BWD(T, V, 4, 0, 512))
 #define HM_BWD_32(T, V)                                                                                     \
     (t.nthr <= 32 ? (t.nv == 1 ? HM_BWD_WARP(T, V) : HM_BWD(T, V, 2, 32, 256))                              \
      : t.nv == 2 ? (t.nthr <= 256 ? HM_BWD(T, V, 2, 0, 256) : HM_BWD(T, V, 2, 0, 512))                      \
@@ -1098,6 +1140,7 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
 #undef HM_BWD
 #undef HM_BWD_F
 #undef HM_BWD_WARP
+#undef HM_BWD_P
 #undef HM_BWD_16
 #undef HM_BWD_32
         count_launches(1);
