@@ -21,7 +21,8 @@ namespace hm {
 namespace {
 
 // A thread's piece of a row is E elements, 16 bytes (fp32 pieces of 32 bytes
-// would leave a warp's loads half of every sector apart).  Columns of thread
+// would leave a warp's loads half of every sector apart), or a pair where rows
+// and widths allow no more.  Columns of thread
 // `tid` of a team of nthr: with VEC E consecutive elements, else single ones a
 // team's width apart (both coalesced).
 template <bool VEC, int kE>
@@ -51,6 +52,28 @@ struct Raw8<__nv_bfloat16, 8> {
         f[3] = pk_bf16(w.w);
     }
     __device__ __forceinline__ void store(__nv_bfloat16 *p) const { __stcs(reinterpret_cast<uint4 *>(p), w); }
+};
+template <>
+struct Raw8<__nv_bfloat16, 2> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(w) : "l"(p));
+    }
+    __device__ __forceinline__ void zero() { w = 0; }
+    __device__ __forceinline__ void set(const F2 *f) { w = bf16_of(f[0]); }
+    __device__ __forceinline__ void get(F2 *f) const { f[0] = pk_bf16(w); }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { __stcs(reinterpret_cast<unsigned *>(p), w); }
+};
+template <>
+struct Raw8<float, 2> {
+    float2 a;
+    __device__ __forceinline__ void load(const float *p) {
+        asm volatile("ld.global.L1::no_allocate.v2.f32 {%0, %1}, [%2];" : "=f"(a.x), "=f"(a.y) : "l"(p));
+    }
+    __device__ __forceinline__ void zero() { a = make_float2(0.f, 0.f); }
+    __device__ __forceinline__ void set(const F2 *f) { a = un(f[0]); }
+    __device__ __forceinline__ void get(F2 *f) const { f[0] = pk(a.x, a.y); }
+    __device__ __forceinline__ void store(float *p) const { __stcs(reinterpret_cast<float2 *>(p), a); }
 };
 template <>
 struct Raw8<float, 4> {
@@ -147,6 +170,10 @@ template <bool VEC, int kE>
 __device__ __forceinline__ void param8(const float *p, int piece, int tid, int nthr, int D, F2 *f) {
     if (VEC) {
         const float *q = p + col_of<true, kE>(piece, 0, tid, nthr);
+        if constexpr (kE == 2) {
+            const float2 a = __ldg(reinterpret_cast<const float2 *>(q));
+            f[0] = pk(a.x, a.y);
+        }
 #pragma unroll
         for (int j = 0; j < kE / 4; ++j) {
             const float4 a = __ldg(reinterpret_cast<const float4 *>(q) + j);
@@ -269,11 +296,11 @@ __device__ __forceinline__ F2 sigmoid(F2 x) {
 // One row per team: a block of 128 threads has several, or is one itself.  Teams
 // of less than a warp (D <= 128) stay to the end when they have no row, with no
 // columns either, since their warp's shuffles need them.
-template <typename T, bool VEC, int NV, int TEAM, bool LAYER>
+template <typename T, bool VEC, int NV, int TEAM, bool LAYER, int kE = 16 / (int)sizeof(T)>
 __global__ void __launch_bounds__(TEAM ? 128 : 512, 1) norm_gate_fwd_kernel(hm_norm_gate_args p) {
     __shared__ float red[2][kMaxWarps][4];
     int turn = 0;
-    constexpr int kE = 16 / (int)sizeof(T), kP = kE / 2;
+    constexpr int kP = kE / 2;
     constexpr int kTeam = TEAM ? TEAM : 1;
     const int tid = TEAM ? threadIdx.x % kTeam : threadIdx.x, nthr = TEAM ? TEAM : blockDim.x;
     const float inv = 1.f / (float)p.D;
@@ -376,12 +403,12 @@ __global__ void __launch_bounds__(TEAM ? 128 : 512, 1) norm_gate_fwd_kernel(hm_n
 // known to the compiler.
 // part[(w * 5 + i) * D + c]: dscale, dpost_w, dpost_b, dpre_w, dpre_b as the
 // w-th block, or warp, has summed them.
-template <typename T, bool VEC, int NV, int TEAM, bool LAYER, bool FULL, int THREADS>
+template <typename T, bool VEC, int NV, int TEAM, bool LAYER, bool FULL, int THREADS, int kE = 16 / (int)sizeof(T)>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1)
 norm_gate_bwd_kernel(hm_norm_gate_bwd_args p, float *part) {
     __shared__ float red[2][kMaxWarps][4];
     int turn = 0;
-    constexpr int kE = 16 / (int)sizeof(T), kP = kE / 2;
+    constexpr int kP = kE / 2;
     constexpr int kTeam = TEAM ? TEAM : 1, kRows = TEAM ? 32 / kTeam : 1;       // rows of a warp, or block
     const bool gate = FULL || p.gate, post = FULL || p.post, pre = FULL || p.dxn;
     const int tid = TEAM ? threadIdx.x % kTeam : threadIdx.x, nthr = TEAM ? TEAM : blockDim.x;
@@ -941,8 +968,9 @@ hm_status check_row(const char *who, const Row &r, int64_t rows, int64_t D, size
     return HM_OK;
 }
 
-bool wide(const Row &r, size_t es) {
-    return !r.p || ((((uintptr_t)r.p) & 15) == 0 && (r.stride * (int64_t)es) % 16 == 0);
+// rows that start on `bytes` boundaries
+bool wide(const Row &r, size_t es, size_t bytes = 16) {
+    return !r.p || ((((uintptr_t)r.p) & (bytes - 1)) == 0 && (r.stride * (int64_t)es) % (int64_t)bytes == 0);
 }
 
 struct Team {
@@ -966,6 +994,28 @@ Team fwd_team(int64_t rows, int64_t D, size_t es, bool vec) {
     int nv = 1;
     while (nv * warps < pieces) nv *= 2;
     return {warps * 32, nv, 0};
+}
+
+// Rows of pairs: an even width up to `most`, every row on a boundary of two
+// elements.  Against element by element: forward, bf16, 60000 x 500 62 us and
+// 127, 4000 x 7002 151 and 230 (fp32, 12000 x 1002: 56 and 50, so not there);
+// backward 20000 x 1530 334 and 681, fp32 12000 x 1002 120 and 257 (100000 x 170, a warp
+// per row: 228 and 214, so only from 256 columns on).
+bool pairs(const Row *rows, int n, int64_t D, int64_t most, size_t es, const void *const *params, int np) {
+    bool ok = D % 2 == 0 && D <= most;
+    for (int i = 0; i < n; ++i) ok = ok && wide(rows[i], es, 2 * es);
+    for (int i = 0; i < np; ++i) ok = ok && ((uintptr_t)params[i] & 7) == 0;
+    return ok;
+}
+
+// Forward of pairs: up to 8 a lane.
+Team pair_team(int64_t rows, int64_t D) {
+    const int pieces = (int)((D + 63) / 64);
+    int warps = 1, nv = 1;
+    while ((pieces + warps - 1) / warps > 8) warps *= 2;
+    while (warps < 16 && (pieces + warps - 1) / warps > 4 && rows * warps * 2 <= 148 * 16) warps *= 2;
+    while (nv * warps < pieces) nv *= 2;
+    return {warps * 32, warps > 1 && nv < 4 ? 4 : nv, 0};
 }
 
 // Backward: 8 columns a thread (bf16 one piece, fp32 two), up to 512 threads, then
@@ -1020,8 +1070,9 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
     if (a->rows == 0) return HM_OK;
     if (!a->r_out && !a->xn) return fail_args(HM_ERR_INVALID_ARG, "%s: r_out and xn are both NULL", w);
     if (a->r_out == a->xn) return fail_args(HM_ERR_INVALID_ARG, "%s: r_out and xn are the same array", w);
-    const Team t = fwd_team(a->rows, a->D, es, vec);
-    const bool block = t.nthr > 32 || !vec;
+    const bool two = !vec && es == 2 && pairs(rows, 5, a->D, 8192, es, params, 5);
+    const Team t = two ? pair_team(a->rows, a->D) : fwd_team(a->rows, a->D, es, vec);
+    const bool block = t.nthr > 32 || !(vec || two);
     const int of_block = block ? 1 : 128 / t.nthr;         // rows
     const int64_t blocks = (a->rows + of_block - 1) / of_block;
     if (blocks > 0x7fffffffLL) return fail_args(HM_ERR_UNSUPPORTED, "%s: too many rows", w);
@@ -1030,7 +1081,17 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
 #define HM_FWD_Y(T, V, N, B) (a->norm == HM_NORM_LAYER ? HM_FWD(T, V, N, B, true) : HM_FWD(T, V, N, B, false))
 #define HM_FWD_B(T, N) (block ? HM_FWD_Y(T, true, N, 0) : HM_FWD_Y(T, true, N, 32))
 #define HM_FWD_S(T) (t.nv == 1 ? HM_FWD_Y(T, false, 1, 0) : t.nv == 2 ? HM_FWD_Y(T, false, 2, 0) : HM_FWD_Y(T, false, 4, 0))
-    if (a->io_dtype == HM_BF16) {
+#define HM_FWD_2(T, N, B)                                                                                            \
+    (a->norm == HM_NORM_LAYER                                                                                        \
+         ? norm_gate_fwd_kernel<T, true, N, B, true, 2><<<(unsigned)blocks, B ? 128 : t.nthr, 0, s>>>(*a)            \
+         : norm_gate_fwd_kernel<T, true, N, B, false, 2><<<(unsigned)blocks, B ? 128 : t.nthr, 0, s>>>(*a))
+#define HM_FWD_PAIRS(T)                                                                                              \
+    (block ? (t.nv == 4 ? HM_FWD_2(T, 4, 0) : HM_FWD_2(T, 8, 0))                                                     \
+     : t.nv == 1 ? HM_FWD_2(T, 1, 32) : t.nv == 2 ? HM_FWD_2(T, 2, 32)                                               \
+     : t.nv == 4 ? HM_FWD_2(T, 4, 32) : HM_FWD_2(T, 8, 32))
+    if (two) {
+        HM_FWD_PAIRS(__nv_bfloat16);
+    } else if (a->io_dtype == HM_BF16) {
         if (!vec) HM_FWD_S(__nv_bfloat16);
         else if (t.nthr == 8) HM_FWD_Y(__nv_bfloat16, true, 1, 8);
         else if (t.nthr == 16) HM_FWD_Y(__nv_bfloat16, true, 1, 16);
@@ -1051,6 +1112,8 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
 #undef HM_FWD_Y
 #undef HM_FWD_B
 #undef HM_FWD_S
+#undef HM_FWD_2
+#undef HM_FWD_PAIRS
     count_launches(1);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? HM_OK : fail_args(HM_ERR_CUDA, "%s launch: %s", w, cudaGetErrorString(e));
@@ -1132,7 +1195,15 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     (t.nthr <= 32 ? (t.nv == 1 ? HM_BWD_WARP(T, V) : HM_BWD(T, V, 2, 32, 256))                              \
      : t.nv == 2 ? (t.nthr <= 256 ? HM_BWD(T, V, 2, 0, 256) : HM_BWD(T, V, 2, 0, 512))                      \
      : t.nv == 4 ? HM_BWD(T, V, 4, 0, 512) : HM_BWD(T, V, 8, 0, 512))
-        if (tiled) {
+        const bool two = !vec && a->D > 256 && pairs(rows, 8, a->D, 4096, es, params, 4);
+#define HM_BWD_2(T, Z)                                                                                               \
+    (a->norm == HM_NORM_LAYER ? norm_gate_bwd_kernel<T, true, 4, 0, true, false, Z, 2><<<t.blocks, t.nthr, 0, s>>>(*a, part) \
+                              : norm_gate_bwd_kernel<T, true, 4, 0, false, false, Z, 2><<<t.blocks, t.nthr, 0, s>>>(*a, part))
+#define HM_BWD_PAIRS(T) (t.nthr > 256 ? HM_BWD_2(T, 512) : HM_BWD_2(T, 256))      /* 8 columns a thread, as bwd_team has them */
+        if (two) {
+            if (a->io_dtype == HM_BF16) HM_BWD_PAIRS(__nv_bfloat16);
+            else HM_BWD_PAIRS(float);
+        } else if (tiled) {
             const cudaError_t e = a->norm == HM_NORM_LAYER ? rows_by(std::true_type()) : rows_by(std::false_type());
             if (e != cudaSuccess) return fail_args(HM_ERR_CUDA, "%s launch: %s", w, cudaGetErrorString(e));
         } else if (a->io_dtype == HM_BF16) vec ? HM_BWD_16(__nv_bfloat16, true) : HM_BWD_16(__nv_bfloat16, false);
@@ -1141,6 +1212,8 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
 #undef HM_BWD_F
 #undef HM_BWD_WARP
 #undef HM_BWD_P
+#undef HM_BWD_2
+#undef HM_BWD_PAIRS
 #undef HM_BWD_16
 #undef HM_BWD_32
         count_launches(1);

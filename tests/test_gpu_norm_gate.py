@@ -349,3 +349,15 @@ def test_backward_in_place(hm, io, n, D):
     yc, gc, dc = y.clone(), gate.clone(), dxn.clone()
     back(yc, gc, dc, yc, dc, gc)
     assert all(torch.equal(a, b) for a, b in zip(outs, (yc, dc, gc)))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("n,D,pad", [(5, 2, 0), (77, 34, 0), (30, 130, 0), (2600, 170, 0), (41, 254, 0), (9, 302, 0),
+                                     (700, 1002, 0), (3, 2050, 2), (6, 4094, 0), (4, 8190, 0), (50, 256, 2)])
+def test_rows_of_pairs(hm, io, layer, n, D, pad):
+    """Even widths and offsets that are no multiples of 16 bytes."""
+    c = _inputs(40, n, D, io, layer)
+    _forward(hm, c, io, layer, True, True, pad=pad)
+    _backward(hm, c, io, layer, True, True, pad=pad)
+    _backward(hm, c, io, layer, False, False, pad=pad)
