@@ -622,26 +622,34 @@ def hm_gated_scan_step(args: GatedStepArgs, stream=None) -> None:
 
 
 def _row_stride(t) -> int:
-    """Elements between the rows of [..., D], whose leading axes must be dense over one another."""
+    """Elements between the rows of [..., D], whose leading axes must be dense over one another.
+    A broadcast axis (stride 0) is refused: its rows are one row, and a single stride that
+    stands for the other axes would count past the tensor's end."""
     if t is None:
         return 0
     if t.dim() == 2:
         return t.stride()[0]
-    step = want = 0
+    if t.numel() == 0:
+        return t.shape[-1]
+    step = want = None
     for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
             continue
-        if not step:
+        if st == 0:
+            raise ValueError("a tensor of shape %s with strides %s repeats its rows along an axis: pass a dense "
+                             "copy (.contiguous())" % (tuple(t.shape), tuple(t.stride())))
+        if step is None:
             step = want = st
         elif st != want:
             raise ValueError("rows of a tensor with strides %s are not equally spaced" % (tuple(t.stride()),))
         want *= n
-    return step or t.shape[-1]
+    return t.shape[-1] if step is None else step
 
 
 def norm_gate_args(y, r, r_out, xn, gate=None, norm: int = 0, post: bool = True, eps: float = 1e-5,
                    alpha: float = 1.0, scale=None, post_w=None, post_b=None, pre_w=None, pre_b=None) -> NormGateArgs:
-    """Fill an hm_norm_gate_args (y, gate, r, r_out, xn: [..., D]; parameters: [D] fp32)."""
+    """Fill an hm_norm_gate_args (y, gate, r, r_out, xn: [..., D], equally spaced rows, no
+    broadcast axes; parameters: [D] fp32)."""
     refs = (y, r, r_out, xn, gate)
     par = (scale, post_w, post_b, pre_w, pre_b)
     raw = _filler().norm_gate(*refs, norm, post, eps, alpha, *par)
@@ -672,7 +680,8 @@ def norm_gate_bwd_args(y, r_out, dr_out, dxn, dy, dr, gate=None, dgate=None, nor
                        dscale=None, dpost_w=None, dpost_b=None, dpre_w=None, dpre_b=None,
                        workspace=None) -> NormGateBwdArgs:
     """Fill an hm_norm_gate_bwd_args (y, gate and the forward's r_out, the gradients of its
-    outputs, the gradient buffers; rows [..., D] of one dtype, parameters and theirs [D] fp32)."""
+    outputs, the gradient buffers; rows [..., D] of one dtype, equally spaced, no broadcast axes;
+    parameters and theirs [D] fp32)."""
     refs = (y, r_out, dr_out, dxn, dy, dr, gate, dgate)
     par = (scale, post_w, post_b, pre_w, dscale, dpost_w, dpost_b, dpre_w, dpre_b, workspace)
     raw = _filler().norm_gate_bwd(*refs, norm, post, eps, alpha, *par)
