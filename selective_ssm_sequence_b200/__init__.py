@@ -511,6 +511,13 @@ def _dense(who: str, shape, dtype, **ts):
                 who, name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
 
 
+def _buffer(who: str, **ts) -> None:
+    """Each given byte buffer is dense: its size is that of the memory behind it."""
+    for name, t in ts.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError("%s: %s must be contiguous, got strides %s" % (who, name, tuple(t.stride())))
+
+
 def _one_device(who: str, *ts) -> None:
     """All tensors on the current CUDA device: the kernels run there, on its stream."""
     torch = _need_torch()
@@ -543,6 +550,7 @@ def gated_scan_args(x, dt, y, A_log, dt_bias=None, h0=None, h_out=None, lengths=
     _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias)
     _dense(who, (B, D), torch.float32, h0=h0, h_out=h_out)
     _dense(who, (B,), torch.int32, lengths=lengths)
+    _buffer(who, states=states)
     _one_device(who, *refs)
     xs, ds, ys = x.stride(), dt.stride(), y.stride() if y is not None else (0, 0)
     a = GatedScanArgs(B, L, D, _dtype_code(x), int(input_scale), _ptr(x), _ptr(dt), _ptr(y), xs[0], xs[1], ds[0],
@@ -577,6 +585,7 @@ def gated_scan_bwd_args(x, dt, dy, dx, ddt, A_log, dA_log, states, dt_bias=None,
     _dense(who, (D,), torch.float32, A_log=A_log, dt_bias=dt_bias, dA_log=dA_log, d_dt_bias=d_dt_bias)
     _dense(who, (B, D), torch.float32, dh_out=dh_out, dh0=dh0)
     _dense(who, (B,), torch.int32, lengths=lengths)
+    _buffer(who, states=states, workspace=workspace)
     _one_device(who, *refs, workspace)
     s = [v for t in (x, dt, dy, dx, ddt) for v in t.stride()[:2]]
     a = GatedScanBwdArgs(B, L, D, _dtype_code(x), int(input_scale), _ptr(x), _ptr(dt), _ptr(dy), _ptr(dx), _ptr(ddt),
@@ -695,6 +704,7 @@ def norm_gate_bwd_args(y, r_out, dr_out, dxn, dy, dr, gate=None, dgate=None, nor
     _io(who, y.shape, y, y=y, gate=gate, r_out=r_out, dr_out=dr_out, dxn=dxn, dy=dy, dgate=dgate, dr=dr)
     _dense(who, (D,), torch.float32, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w, dscale=dscale,
            dpost_w=dpost_w, dpost_b=dpost_b, dpre_w=dpre_w, dpre_b=dpre_b)
+    _buffer(who, workspace=workspace)
     _one_device(who, *refs, *par)
     a = NormGateBwdArgs(y.numel() // D if D else 0, D, _dtype_code(y), int(norm), int(post), eps, alpha, _ptr(y),
                         _ptr(gate), _ptr(r_out), _ptr(dr_out), _ptr(dxn), _ptr(dy), _ptr(dgate), _ptr(dr),

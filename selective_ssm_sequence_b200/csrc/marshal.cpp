@@ -70,12 +70,12 @@ struct Common {
         return t->data_ptr();
     }
     float *f32(PyObject *o, at::IntArrayRef sh) const { return (float *)dense(opt(o), sh); }
-    // a byte buffer of any type
+    // a byte buffer of any type; dense, so that its size is that of the memory behind it
     void *buffer(PyObject *o, size_t &bytes) const {
         bytes = 0;
         const at::Tensor *t = opt(o);
         if (!t) return nullptr;
-        if (t->device() != dev) throw No();
+        if (t->device() != dev || !t->is_contiguous()) throw No();
         bytes = (size_t)t->numel() * t->element_size();
         return t->data_ptr();
     }

@@ -62,3 +62,20 @@ def test_seam_helpers_refuse_broadcast_rows(on_cpu):
                 call()
         a = on_cpu.norm_gate_args(y, b.contiguous(), e[0], e[1])
         assert (a.rows, a.D, a.r_stride) == (24, 8, 8)
+
+
+def test_buffers_are_dense(on_cpu):
+    """A buffer of repeated or spaced bytes has fewer of its own than its count says."""
+    import torch
+    B, L, D = 2, 5, 8
+    x, p, u8 = torch.zeros(B, L, D), torch.zeros(D), torch.uint8
+    dense = torch.zeros(1 << 12, dtype=u8)
+    for bad in (torch.zeros(1, dtype=u8).expand(1 << 12), torch.zeros(1 << 13, dtype=u8)[::2]):
+        for call in (lambda: on_cpu.gated_scan_args(x, x, x, p, states=bad),
+                     lambda: on_cpu.gated_scan_bwd_args(x, x, x, x, x, p, p, bad),
+                     lambda: on_cpu.gated_scan_bwd_args(x, x, x, x, x, p, p, dense, workspace=bad),
+                     lambda: on_cpu.norm_gate_bwd_args(x, x, x, x, x, x, workspace=bad)):
+            with pytest.raises(ValueError, match="must be contiguous"):
+                call()
+    a = on_cpu.gated_scan_bwd_args(x, x, x, x, x, p, p, dense, workspace=dense[256:])
+    assert (a.states_bytes, a.workspace_bytes) == (1 << 12, (1 << 12) - 256)

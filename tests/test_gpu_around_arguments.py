@@ -51,3 +51,17 @@ def test_seam_takes_no_broadcast_rows(hm):
     want = around.norm_gate_bwd(rows(y), rows(o), rows(g), rows(x), None)
     assert np.allclose(rows(dr), want["dr"], rtol=0, atol=2.0 ** -15)
     assert np.allclose(rows(dy), want["dy"], rtol=0, atol=2.0 ** -15)
+
+
+def test_buffers_are_dense(hm):
+    import torch
+    x, p, u8 = torch.zeros(2, 5, 8, device="cuda"), torch.zeros(8, device="cuda"), torch.uint8
+    dense = torch.zeros(1 << 12, dtype=u8, device="cuda")
+    for bad in (torch.zeros(1, dtype=u8, device="cuda").expand(1 << 12), dense[::2]):
+        for call in (lambda: hm.gated_scan_args(x, x, x, p, states=bad),
+                     lambda: hm.gated_scan_bwd_args(x, x, x, x, x, p, p, bad),
+                     lambda: hm.gated_scan_bwd_args(x, x, x, x, x, p, p, dense, workspace=bad),
+                     lambda: hm.norm_gate_bwd_args(x, x, x, x, x, x, workspace=bad)):
+            with pytest.raises(ValueError, match="must be contiguous"):
+                call()
+    assert hm.gated_scan_args(x, x, x, p, states=dense).states_bytes == 1 << 12
