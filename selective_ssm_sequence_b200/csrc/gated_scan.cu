@@ -261,27 +261,51 @@ struct Exchange {
 constexpr int kR = 16;        // tokens of a warp's run
 constexpr int kStages = 2;
 
+// One poll for a phase that other blocks of the cluster complete: their maps come
+// by st.async, whose complete_tx releases at cluster scope, so the wait acquires
+// at that scope (the plain form acquires within the block only, which is enough
+// for the block's own TMA loads).
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, P;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// what a barrier counts: this block's TMA loads, or maps of the cluster's blocks
+enum Source { kOwnLoads, kClusterMaps };
+template <Source S>
+__device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity) {
+    return S == kClusterMaps ? try_wait_cluster(bar, parity) : tc::mbar_try_wait(bar, parity);
+}
+
 // Bounded wait of every thread of the block.  After a timeout the kernel keeps
 // its control flow (its loops are bounded and every block of a cluster must
 // reach the barriers), with short waits that let its own copies land.
+template <Source S>
 __device__ __noinline__ void wait_bar_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, DevErr err,
                                            unsigned site) {
     const uint32_t polls = *abort_flag ? 1u << 10 : tc::kWaitPolls;
     for (uint32_t i = 0; i < polls; ++i)
-        if (tc::mbar_try_wait(bar, parity)) return;
+        if (try_wait<S>(bar, parity)) return;
     *abort_flag = 1;
     report_error(err, HM_ERR_TIMEOUT, KID_GATED_SCAN, site);
 }
+template <Source S>
 __device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag, DevErr err,
                                          unsigned site) {
-    if (!tc::mbar_try_wait(bar, parity)) wait_bar_slow(bar, parity, abort_flag, err, site);
+    if (!try_wait<S>(bar, parity)) wait_bar_slow<S>(bar, parity, abort_flag, err, site);
 }
 
 // State at the start of window `it` from that at this block's runs of the
 // window before (`hb`); it > 0, cluster > 1.
 __device__ __forceinline__ F2 finish_window(const Exchange &x, int it, F2 hb) {
     const int i = it - 1;
-    wait_bar(&x.high[i & 1], (i >> 1) & 1, x.abort_flag, x.err, 1);
+    wait_bar<kClusterMaps>(&x.high[i & 1], (i >> 1) & 1, x.abort_flag, x.err, 1);
     const Map2 *m = x.ctas + ((i & 1) * x.cluster + x.rank) * 32 + (threadIdx.x & 31);
 #pragma unroll 2
     for (int r = x.rank; r < x.cluster; ++r, m += 32) hb = apply(*m, hb);
@@ -323,7 +347,7 @@ __device__ __forceinline__ F2 enter_run(const Exchange &x, int it, int warp, F2 
         for (int r = 0; r < x.cluster; ++r) st_async16(slot, x.rank < r ? lo : hi, (uint32_t)r, q);
     }
     if (x.rank) {
-        wait_bar(&x.low[it & 1], (it >> 1) & 1, x.abort_flag, x.err, 2);
+        wait_bar<kClusterMaps>(&x.low[it & 1], (it >> 1) & 1, x.abort_flag, x.err, 2);
         const Map2 *m = x.ctas + (it & 1) * x.cluster * 32 + lane;
 #pragma unroll 2
         for (int r = 0; r < x.rank; ++r, m += 32) h = apply(*m, h);
@@ -429,7 +453,7 @@ gated_fwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         const int m = min(max(n - t0, 0), kR);     // tokens of this run
         Map2 run[kR];                              // the run's composition up to each token
         Map2 all = {splat(1.f), splat(0.f)};
-        if (WIDE) wait_bar(&full[it % kStages], (it / kStages) & 1, &abort_flag, err, 0);
+        if (WIDE) wait_bar<kOwnLoads>(&full[it % kStages], (it / kStages) & 1, &abort_flag, err, 0);
         if (!WIDE) cp_async_wait<kStages - 1>();
         if (MODE == kOdd) __syncwarp();            // the other lanes' words
         if (m > 0) {
@@ -661,7 +685,7 @@ gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_consta
         T *tile = stage0 + stage * 3 * kTile + (warp * kRb) * kPitch + kFirst * lane;
         F2 a[kRb], h[kRb], step[kRb], sig[kRb], beta[kRb];
         Map2 mf = {splat(1.f), splat(0.f)}, mr = {splat(1.f), splat(0.f)};
-        if (WIDE && chunk >= 0) wait_bar(&full[stage], phase, &abort_flag, err, 3);
+        if (WIDE && chunk >= 0) wait_bar<kOwnLoads>(&full[stage], phase, &abort_flag, err, 3);
         if (!WIDE) {
             if (MODE == kOdd) __syncwarp();
             fetch_own(it + kBwdStages - 1);                // over what this thread (kOdd: warp) used one window ago
