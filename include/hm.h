@@ -515,7 +515,8 @@ HM_API hm_status hm_gated_scan_step(const hm_gated_step_args *a, hm_stream_t str
  * The parameters are fp32 [D]; a NULL weight or scale is 1, a NULL shift 0.
  * xn is formed from the sum before it is rounded to r_out's type.  r NULL is a
  * zero residual; r_out or xn may be NULL when the other alone is wanted;
- * r_out may alias r, and r_out or xn may alias y or gate (same stride).
+ * r_out and xn may each alias y, gate or r, with the same stride (other strides
+ * are refused), but not each other.
  * Pointers need the alignment of their element type; rows on 16-byte
  * boundaries run the wide loads.  1 <= D <= 16384.
  */
@@ -544,7 +545,8 @@ HM_API hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t stream
  * (r_out is then not read and may be NULL); dr_out NULL: r_out was not used
  * after xn; not both.  Parameter gradients are fp32 [D], each nullable, summed
  * over the rows in a fixed order.  dr may alias dr_out or dxn, dy may alias y,
- * dgate may alias gate (same strides).
+ * dgate may alias gate, with the same strides; an output that is another input's
+ * or another output's array, or an input's with another stride, is refused.
  */
 typedef struct {
     int64_t rows, D;

@@ -968,6 +968,17 @@ hm_status check_row(const char *who, const Row &r, int64_t rows, int64_t D, size
     return HM_OK;
 }
 
+// What an output may lie over.  A row is read whole before any of it is
+// written, so an input with the same row stride may be an output's array; with
+// other strides one row's output would fall on another's input.
+hm_status check_over(const char *who, int64_t rows, const Row &out, const Row &in, bool allowed) {
+    if (rows == 0 || !out.p || out.p != in.p) return HM_OK;
+    if (!allowed) return fail_args(HM_ERR_INVALID_ARG, "%s: %s must not be %s", who, out.name, in.name);
+    if (rows > 1 && out.stride != in.stride)
+        return fail_args(HM_ERR_INVALID_ARG, "%s: %s is %s with another stride", who, out.name, in.name);
+    return HM_OK;
+}
+
 // rows that start on `bytes` boundaries
 bool wide(const Row &r, size_t es, size_t bytes = 16) {
     return !r.p || ((((uintptr_t)r.p) & (bytes - 1)) == 0 && (r.stride * (int64_t)es) % (int64_t)bytes == 0);
@@ -1062,6 +1073,8 @@ extern "C" hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t st
         HM_TRY(check_row(w, r, a->rows, a->D, es));
         vec = vec && wide(r, es);
     }
+    for (int o = 3; o < 5; ++o)
+        for (int i = 0; i < 3; ++i) HM_TRY(check_over(w, a->rows, rows[o], rows[i], true));
     const void *params[] = {a->scale, a->post_w, a->post_b, a->pre_w, a->pre_b};
     for (const void *q : params) {
         if (((uintptr_t)q & 3) != 0) return fail_args(HM_ERR_INVALID_ARG, "%s: misaligned parameter", w);
@@ -1142,6 +1155,12 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     for (const Row &r : rows) {
         HM_TRY(check_row(w, r, a->rows, a->D, es));
         vec = vec && wide(r, es);
+    }
+    for (int o = 5; o < 8; ++o) {
+        // dy over y; dgate over gate; dr over dr_out or dxn (wide rows are read again after other outputs)
+        for (int i = 0; i < 5; ++i)
+            HM_TRY(check_over(w, a->rows, rows[o], rows[i], o == 5 ? i == 0 : o == 6 ? i == 1 : i >= 3));
+        for (int i = 5; i < o; ++i) HM_TRY(check_over(w, a->rows, rows[o], rows[i], false));
     }
     const void *params[] = {a->scale, a->post_w, a->post_b, a->pre_w, a->dscale, a->dpost_w, a->dpost_b, a->dpre_w,
                             a->dpre_b};

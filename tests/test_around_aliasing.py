@@ -1,0 +1,61 @@
+"""Which arrays the outputs of the operators around the mixer may lie over, without a GPU: every
+call here is refused on the host (the allowed ones by a later check, of another argument)."""
+import ctypes
+
+import pytest
+
+from test_abi import hm   # noqa: F401  (the fixture that builds and imports the package)
+from test_around_abi import FAKE, _fill, _scan_bwd, _seam
+
+FWD = ("gate", "r", "r_out", "xn")
+BWD = ("gate", "r_out", "dr_out", "dxn", "dy", "dgate", "dr")
+
+
+def _detail(hm, entry, a):      # noqa: F811
+    assert getattr(hm.lib, entry)(ctypes.byref(a), None) == hm.HM_ERR_INVALID_ARG
+    return hm.lib.hm_last_error_detail().decode()
+
+
+def _over(a, out, inp, stride=None):
+    setattr(a, out, getattr(a, inp))
+    if stride:
+        setattr(a, out + "_stride", stride)
+    return a
+
+
+@pytest.mark.parametrize("out", ["r_out", "xn"])
+@pytest.mark.parametrize("inp", ["y", "gate", "r"])
+def test_seam_forward(hm, out, inp):        # noqa: F811
+    def make():
+        return _seam(hm, "NormGateArgs", FWD, pre_w=FAKE + 2)
+    assert "misaligned parameter" in _detail(hm, "hm_norm_gate_fwd", _over(make(), out, inp))
+    assert "%s is %s with another stride" % (out, inp) in _detail(hm, "hm_norm_gate_fwd", _over(make(), out, inp, 520))
+    one = _fill(_over(make(), out, inp, 520), (), rows=1)       # a single row has no stride
+    assert "misaligned parameter" in _detail(hm, "hm_norm_gate_fwd", one)
+
+
+ALLOWED = {("dy", "y"), ("dgate", "gate"), ("dr", "dr_out"), ("dr", "dxn")}
+
+
+@pytest.mark.parametrize("out", ["dy", "dgate", "dr"])
+@pytest.mark.parametrize("inp", ["y", "gate", "r_out", "dr_out", "dxn", "dy", "dgate", "dr"])
+def test_seam_backward(hm, out, inp):       # noqa: F811
+    if out == inp:
+        return
+
+    def make():
+        return _seam(hm, "NormGateBwdArgs", BWD, workspace=None)
+    same = _detail(hm, "hm_norm_gate_bwd", _over(make(), out, inp))
+    other = _detail(hm, "hm_norm_gate_bwd", _over(make(), out, inp, 520))
+    if (out, inp) in ALLOWED:
+        assert "workspace" in same and "%s is %s with another stride" % (out, inp) in other
+    else:
+        assert "must not be" in same and "must not be" in other
+
+
+def test_seam_backward_without_an_array(hm):    # noqa: F811
+    """An input that is not read (r_out without dxn, dgate without a gate) stands in no one's way."""
+    a = _seam(hm, "NormGateBwdArgs", BWD, workspace=None, dxn=None)
+    assert "workspace" in _detail(hm, "hm_norm_gate_bwd", _over(a, "dr", "r_out"))
+    a = _seam(hm, "NormGateBwdArgs", BWD, workspace=None, gate=None)
+    assert "workspace" in _detail(hm, "hm_norm_gate_bwd", _over(a, "dgate", "dy"))

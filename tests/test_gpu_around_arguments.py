@@ -65,3 +65,22 @@ def test_buffers_are_dense(hm):
             with pytest.raises(ValueError, match="must be contiguous"):
                 call()
     assert hm.gated_scan_args(x, x, x, p, states=dense).states_bytes == 1 << 12
+
+
+@pytest.mark.parametrize("io,n,D", [("bf16", 37, 64), ("bf16", 5, 2048), ("bf16", 9, 6000), ("bf16", 11, 302),
+                                    ("f32", 7, 1001), ("f32", 300, 512)])
+def test_seam_forward_in_place(hm, io, n, D):
+    """r_out and xn over any of y, gate and r, in each form of the forward: the same bits."""
+    import torch
+    src = [dev_tensor(_rand(k, (n, D)), io) for k in ("y", "gate", "r")]
+    o, x = torch.empty_like(src[0]), torch.empty_like(src[0])
+
+    def run(y, gate, r, o, x):
+        hm.hm_norm_gate_fwd(hm.norm_gate_args(y, r, o, x, gate=gate, norm=hm.HM_NORM_LAYER, alpha=0.7))
+    run(*src, o, x)
+    for i in range(3):
+        for j in range(3):
+            if i != j:
+                t = [s.clone() for s in src]
+                run(*t, t[i], t[j])
+                assert torch.equal(t[i], o) and torch.equal(t[j], x), (i, j)
