@@ -596,7 +596,7 @@ HM_API hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_t st
  * other strides in elements; Hk = 0 leaves k out.  positions: device int64,
  * that of (b, t) at positions[b * pos_stride_b + t * pos_stride_t]; NULL:
  * pos0 + t.  q_out / k_out may be q / k (same strides) and must not overlap
- * them otherwise.  rot even, 2 <= rot <= d <= 1024.
+ * them, one another or the other's input otherwise.  rot even, 2 <= rot <= d <= 1024.
  */
 typedef enum { HM_ROTARY_HALF = 0, HM_ROTARY_INTERLEAVED = 1 } hm_rotary_layout;
 typedef enum {

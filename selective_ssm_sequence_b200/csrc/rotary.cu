@@ -279,6 +279,8 @@ extern "C" hm_status hm_rotary(const hm_rotary_args *a, hm_stream_t stream) {
     st = check_side("k", a->k, a->k_out, a->Hk, a->B, a->L, a->d, es, is[1], os[1]);
     if (st != HM_OK) return st;
     if (a->B == 0 || a->L == 0 || a->Hq + a->Hk == 0) return HM_OK;
+    if (a->Hq > 0 && a->Hk > 0 && (a->q_out == a->k_out || a->q_out == a->k || a->k_out == a->q))
+        return fail_args(HM_ERR_INVALID_ARG, "rotary: q_out or k_out is the other's array");
 
     RotArgs r{};
     r.s[0] = {a->q, a->q_out, is[0][0], is[0][1], is[0][2], os[0][0], os[0][1], os[0][2]};

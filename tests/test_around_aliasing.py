@@ -59,3 +59,14 @@ def test_seam_backward_without_an_array(hm):    # noqa: F811
     assert "workspace" in _detail(hm, "hm_norm_gate_bwd", _over(a, "dr", "r_out"))
     a = _seam(hm, "NormGateBwdArgs", BWD, workspace=None, gate=None)
     assert "workspace" in _detail(hm, "hm_norm_gate_bwd", _over(a, "dgate", "dy"))
+
+
+@pytest.mark.parametrize("out,inp", [("q_out", "k"), ("k_out", "q"), ("k_out", "q_out")])
+def test_rotary(hm, out, inp):      # noqa: F811
+    B, L, H, d = 2, 100, 8, 128
+    a = _fill(hm.RotaryArgs(), (), B=B, L=L, Hq=H, Hk=H, d=d, rot=64, io_dtype=hm.HM_BF16, base=1e4, factor=1.0,
+              mscale=1.0, q=FAKE, k=2 * FAKE, q_out=3 * FAKE, k_out=4 * FAKE)
+    for n in ("q", "k", "q_out", "k_out"):
+        for ax, st in (("b", L * H * d), ("t", H * d), ("h", d)):
+            setattr(a, "%s_stride_%s" % (n, ax), st)
+    assert "the other's array" in _detail(hm, "hm_rotary", _over(a, out, inp))
