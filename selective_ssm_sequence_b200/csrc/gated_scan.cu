@@ -1160,6 +1160,8 @@ hm_status check_bwd(const hm_gated_scan_bwd_args *a) {
     HM_TRY(check_f32(w, "dh_out", a->dh_out, false));
     HM_TRY(check_f32(w, "dh0", a->dh0, false));
     HM_TRY(check_f32(w, "lengths", a->lengths, false));
+    if (a->dA_log == a->d_dt_bias)
+        return fail_args(HM_ERR_INVALID_ARG, "%s: dA_log and d_dt_bias are the same array", w);
     if (a->B > 0 && a->L > 0) {
         const void *in[] = {a->x, a->dt, a->dy}, *out[] = {a->dx, a->ddt};
         for (const void *o : out)

@@ -1167,6 +1167,10 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
     for (const void *q : params)
         if (((uintptr_t)q & 3) != 0) return fail_args(HM_ERR_INVALID_ARG, "%s: misaligned parameter", w);
     for (int i = 0; i < 4; ++i) vec = vec && ((uintptr_t)params[i] & 15) == 0;    // those that are read
+    for (int o = 4; o < 9; ++o)
+        for (int i = 4; i < o; ++i)
+            if (params[o] && params[o] == params[i])
+                return fail_args(HM_ERR_INVALID_ARG, "%s: two parameter gradients are the same array", w);
     const size_t need = hm_norm_gate_bwd_workspace_size(a);
     if (need > 0 && (!a->workspace || a->workspace_bytes < need || ((uintptr_t)a->workspace & 255) != 0))
         return fail_args(HM_ERR_INVALID_ARG, "%s: workspace of %zu bytes, 256-byte aligned, is needed", w, need);

@@ -61,6 +61,18 @@ def test_seam_backward_without_an_array(hm):    # noqa: F811
     assert "workspace" in _detail(hm, "hm_norm_gate_bwd", _over(a, "dgate", "dy"))
 
 
+def test_parameter_gradients_are_arrays_of_their_own(hm):       # noqa: F811
+    names = ("dscale", "dpost_w", "dpost_b", "dpre_w", "dpre_b")
+    own = {n: (40 + i) * FAKE for i, n in enumerate(names)}
+    assert "workspace" in _detail(hm, "hm_norm_gate_bwd", _seam(hm, "NormGateBwdArgs", BWD, workspace=None, **own))
+    for i, n in enumerate(names):
+        for m in names[:i]:
+            a = _seam(hm, "NormGateBwdArgs", BWD, workspace=None, **dict(own, **{n: own[m]}))
+            assert "parameter gradients are the same" in _detail(hm, "hm_norm_gate_bwd", a)
+    a = _scan_bwd(hm, d_dt_bias=FAKE, workspace=None)
+    assert "dA_log and d_dt_bias" in _detail(hm, "hm_gated_scan_bwd", a)
+
+
 @pytest.mark.parametrize("out,inp", [("q_out", "k"), ("k_out", "q"), ("k_out", "q_out")])
 def test_rotary(hm, out, inp):      # noqa: F811
     B, L, H, d = 2, 100, 8, 128
