@@ -416,6 +416,7 @@ HM_API hm_status hm_step_decode_noalloc(const hm_decode_args *a, hm_stream_t str
  * sequence of a padded batch, read as clamped to [0, L]: rows behind a
  * sequence's end are neither read for its result nor written, the final state
  * is the one after its last token, and a sequence of no tokens hands h0 on.
+ * A dt_bias above 2e38 counts as about 2e38 (a step that forgets all).
  */
 typedef enum { HM_INPUT_PLAIN = 0, HM_INPUT_STEP = 1, HM_INPUT_UNIT = 2 } hm_input_scale;
 

@@ -69,7 +69,9 @@ __device__ __forceinline__ ChanParams params_of(float A0, float A1, float bias0,
     if (r0 > 3e38f) r0 = 3e38f;       // finite, so that a step of zero decays nothing
     if (r1 > 3e38f) r1 = 3e38f;
     p.nrate = pk(-r0, -r1);
-    p.bias = pk(bias0, bias1) * splat(kLog2e);
+    // below infinity: tokens behind a sequence's end enter as dt = -inf, and must come out as z = -inf
+    bias0 *= kLog2e, bias1 *= kLog2e;
+    p.bias = pk(bias0 > 3e38f ? 3e38f : bias0, bias1 > 3e38f ? 3e38f : bias1);
     return p;
 }
 __device__ __forceinline__ ChanParams chan_params(const float *A_log, const float *dt_bias, int64_t c, int64_t c1,
