@@ -6,7 +6,8 @@ without a GPU (its symbols can be inspected on a build host) and needs only
 the driver on a GPU host.
 
 csrc/marshal.cpp becomes the extension module _marshal.so beside it, with the
-host compiler, against torch's headers and libraries.
+host compiler, against torch's headers and libraries.  It only saves the helpers
+time, so where it cannot be built the library stands without it.
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ import glob
 import os
 import shutil
 import subprocess
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -76,8 +78,7 @@ def build_marshal(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile csrc/*.cu and link libhm.so, and build _marshal.so; returns the library's path."""
-    build_marshal(force)
+    """Compile csrc/*.cu and link libhm.so, then build _marshal.so; returns the library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = _sources()
     hdrs = _headers()
@@ -105,6 +106,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
         os.replace(tmp, LIB)
+    try:
+        build_marshal(force)
+    except Exception as e:      # no torch, its headers or Python's, or no host compiler
+        warnings.warn("_marshal.so was not built; the helpers fill their structs in Python: %s" % e, RuntimeWarning)
     return LIB
 
 
