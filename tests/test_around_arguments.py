@@ -79,3 +79,22 @@ def test_buffers_are_dense(on_cpu):
                 call()
     a = on_cpu.gated_scan_bwd_args(x, x, x, x, x, p, p, dense, workspace=dense[256:])
     assert (a.states_bytes, a.workspace_bytes) == (1 << 12, (1 << 12) - 256)
+
+
+def test_helpers_without_the_native_filler(on_cpu, monkeypatch):
+    """Where _marshal cannot be imported the helpers fill their structs in Python, with one warning."""
+    import sys
+    import torch
+    monkeypatch.setitem(sys.modules, on_cpu.__name__ + "._marshal", None)
+    monkeypatch.delattr(on_cpu, "_marshal", raising=False)
+    monkeypatch.setattr(on_cpu, "_native", None)
+    x, p = torch.zeros(2, 5, 8), torch.zeros(8)
+    with pytest.warns(RuntimeWarning, match="_marshal.so cannot be used"):
+        a = on_cpu.gated_scan_args(x, x, x, p)
+    assert (a.B, a.L, a.D, a.x) == (2, 5, 8, x.data_ptr())
+    # a buffer as before there was a filler: a dense allocation, its start moved to 256 bytes
+    empty = torch.empty
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch, "empty", lambda *s, device=None, **kw: empty(*s, **kw))
+    buf = on_cpu.alloc_workspace(1000)
+    assert buf.numel() >= 1000 and buf.data_ptr() % 256 == 0

@@ -84,3 +84,103 @@ def test_seam_forward_in_place(hm, io, n, D):
                 t = [s.clone() for s in src]
                 run(*t, t[i], t[j])
                 assert torch.equal(t[i], o) and torch.equal(t[j], x), (i, j)
+
+
+@pytest.fixture(params=["native", "python"])
+def filler(hm, monkeypatch, request):
+    """With the native filler, and with the helpers on their own."""
+    if request.param == "python":
+        monkeypatch.setattr(hm, "_native", hm._NoFiller())
+    else:
+        assert hm._filler().__name__.endswith("_marshal")
+    return hm
+
+
+def _buf(hm, n):
+    b = hm.alloc_workspace(n)
+    assert b.data_ptr() % 256 == 0 and b.numel() >= n
+    return b
+
+
+def test_recurrence_through_both_fillers(filler):
+    """Every argument a tensor of its own, so that none can stand for another.  fp32 against the
+    definition: a rounding, 2^-24, and 2^-19 of the magnitudes that the definition returns (gates
+    good to a few 2^-22, carried through the recurrence); all |z| here are below 32."""
+    import torch
+    B, L, D = 3, 40, 24
+    f = lambda n, *s: dev_tensor(_rand(n, s), "f32")                        # noqa: E731
+    x, dt, dy, A, bias, dh = f("x", B, L, D), f("dt", B, L, D), f("dy", B, L, D), f("A", D), f("b", D), f("dh", B, D)
+    h0 = f("h0", B, D)
+    e = lambda *s: torch.full(s, 7.0, device="cuda")                        # noqa: E731
+    y, h, dx, ddt, dA, db, dh0 = e(B, L, D), e(B, D), e(B, L, D), e(B, L, D), e(D), e(D), e(B, D)
+    lengths = torch.tensor([40, 0, 17], dtype=torch.int32, device="cuda")
+    a = filler.gated_scan_args(x, dt, y, A, dt_bias=bias, h0=h0, h_out=h, lengths=lengths, input_scale=1)
+    st = _buf(filler, filler.hm_gated_scan_states_size(a))
+    filler.hm_gated_scan_fwd(filler.gated_scan_args(x, dt, y, A, dt_bias=bias, h0=h0, h_out=h, lengths=lengths,
+                                                    input_scale=1, states=st))
+    kw = dict(dt_bias=bias, d_dt_bias=db, dh_out=dh, dh0=dh0, lengths=lengths, input_scale=1)
+    b = filler.gated_scan_bwd_args(x, dt, dy, dx, ddt, A, dA, st, **kw)
+    ws = _buf(filler, filler.hm_gated_scan_bwd_workspace_size(b))
+    filler.hm_gated_scan_bwd(filler.gated_scan_bwd_args(x, dt, dy, dx, ddt, A, dA, st, workspace=ws, **kw))
+    assert filler.hm_get_device_error() == filler.HM_OK
+
+    def near(got, want, mag):
+        assert np.all(np.abs(got - want) <= 2.0 ** -24 * np.abs(want) + 2.0 ** -19 * mag + 1e-37)
+    o = [to_np(t) for t in (x, dt, dy, A, bias)]
+    o = dict(x=o[0], dt=o[1], A_log=o[3], dt_bias=o[4], h0=to_np(h0), lengths=lengths.cpu().numpy(), scale=around.STEP)
+    wy, wh, mag = around.gated_scan(**o)
+    g = around.gated_scan_bwd(dy=to_np(dy), dh_out=to_np(dh), **o)
+    for s, n in enumerate((40, 0, 17)):
+        near(to_np(y[s, :n]), wy[s, :n], mag[s, :n])
+        near(to_np(h[s]), wh[s], mag[s, n - 1] if n else 0.0)
+        for got, k in ((dx, "dx"), (ddt, "ddt")):
+            near(to_np(got[s, :n]), g[k][0][s, :n], g[k][1][s, :n])
+    for got, k in ((dA, "dA_log"), (db, "d_dt_bias"), (dh0, "dh0")):
+        near(to_np(got), *g[k])
+    yt, ht = e(B, D), e(B, D)
+    filler.hm_gated_scan_step(filler.gated_step_args(x[:, 0], dt[:, 1], yt, h0, ht, A, dt_bias=bias, input_scale=2))
+    wy, wh, mag = around.gated_scan(o["x"][:, :1], o["dt"][:, 1:2], o["A_log"], o["dt_bias"], h0=o["h0"],
+                                    scale=around.UNIT)
+    near(to_np(yt), wy[:, 0], mag[:, 0])
+    near(to_np(ht), wh, mag[:, 0])
+
+
+def test_seam_through_both_fillers(filler):
+    """As above; a result is a sum of a few products whose errors are 2^-18 of their absolute sum.
+    The terms are products of up to eight values of order one (at most 4, most below 1) over a
+    row's deviation above 1/2, and the parameters' gradients sum 10 rows of them: below 2^8."""
+    import torch
+    n, D = 10, 48
+    f = lambda k, *s: dev_tensor(_rand(k, s), "f32")                        # noqa: E731
+    y, gate, r, dr_out, dxn = (f(k, n, D) for k in ("y", "gate", "r", "dr", "dxn"))
+    scale, post_w, post_b, pre_w, pre_b = (f(k, D) for k in ("sc", "w1", "b1", "w2", "b2"))
+    e = lambda *s: torch.full(s, 7.0, device="cuda")                        # noqa: E731
+    r_out, xn, dy, dgate, dr = (e(n, D) for _ in range(5))
+    d = {k: e(D) for k in ("dscale", "dpost_w", "dpost_b", "dpre_w", "dpre_b")}
+    kw = dict(norm=1, eps=1e-4, alpha=0.5, scale=scale, post_w=post_w, post_b=post_b, pre_w=pre_w)
+    filler.hm_norm_gate_fwd(filler.norm_gate_args(y, r, r_out, xn, gate=gate, pre_b=pre_b, **kw))
+    b = filler.norm_gate_bwd_args(y, r_out, dr_out, dxn, dy, dr, gate=gate, dgate=dgate, **d, **kw)
+    ws = _buf(filler, filler.hm_norm_gate_bwd_workspace_size(b))
+    filler.hm_norm_gate_bwd(filler.norm_gate_bwd_args(y, r_out, dr_out, dxn, dy, dr, gate=gate, dgate=dgate,
+                                                      workspace=ws, **d, **kw))
+    o = dict(layer=True, eps=1e-4, alpha=0.5, scale=to_np(scale), post_w=to_np(post_w), post_b=to_np(post_b),
+             pre_w=to_np(pre_w))
+    want = around.norm_gate(to_np(y), to_np(r), to_np(gate), pre_b=to_np(pre_b), **o)
+    back = around.norm_gate_bwd(to_np(y), to_np(r_out), to_np(dr_out), to_np(dxn), to_np(gate), **o)
+    got = dict(d, dy=dy, dr=dr, dgate=dgate)
+    for g, w in [(r_out, want[0]), (xn, want[1])] + [(got[k], back[k]) for k in got]:
+        assert np.abs(to_np(g) - w).max() < 2.0 ** -10
+
+
+def test_rotary_through_both_fillers(filler):
+    """As above; the stated error of an angle and a rounding: 2^-21 of (|u| + |v|) < 2^3 mscale."""
+    import torch
+    B, L = 2, 9
+    q, k = dev_tensor(_rand("q", (B, L, 4, 16)), "f32"), dev_tensor(_rand("k", (B, L, 2, 16)), "f32")
+    oq, ok = torch.full_like(q, 7.0), torch.full_like(k, 7.0)
+    pos = torch.tensor(np.random.default_rng(5).integers(0, 1000, (B, L)), device="cuda")
+    kw = dict(rot=12, base=5e5, factor=8.0, orig_len=100.0, beta_slow=0.5, beta_fast=20.0, mscale=1.25)
+    filler.hm_rotary(filler.rotary_args(q, k, oq, ok, layout=1, scaling=3, positions=pos, transpose=True, **kw))
+    for got, x in ((oq, q), (ok, k)):
+        want = around.rotary(to_np(x), pos.cpu().numpy(), interleaved=True, scaling="by_parts", transpose=True, **kw)
+        assert np.abs(to_np(got) - want).max() < 2.0 ** -17
