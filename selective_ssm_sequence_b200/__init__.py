@@ -266,6 +266,9 @@ def _filler():
         _need_torch()
         try:
             from . import _marshal as mod
+            from ._build import marshal_tag
+            if getattr(mod, "built_for", None) != marshal_tag():
+                raise ImportError("built for another torch or Python")
         except ImportError as e:
             import warnings
             warnings.warn("_marshal.so cannot be used (%s): calls of a few rows take some microseconds longer; run "

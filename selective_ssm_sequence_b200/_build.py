@@ -55,10 +55,19 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def marshal_tag() -> str:
+    """What a build of csrc/marshal.cpp is good for: it reads torch's and Python's objects at the
+    places that this torch and this Python have them."""
+    import sys
+    import torch
+    return "torch %s abi %d %s" % (torch.__version__, torch._C._GLIBCXX_USE_CXX11_ABI, sys.implementation.cache_tag)
+
+
 def build_marshal(force: bool = False) -> str:
     """Compile csrc/marshal.cpp into _marshal.so; returns its path."""
-    src = os.path.join(CSRC, "marshal.cpp")
-    if not force and not _stale(MARSHAL, [src, os.path.join(INCLUDE, "hm.h")]):
+    src, stamp, tag = os.path.join(CSRC, "marshal.cpp"), os.path.join(OBJDIR, "marshal.tag"), marshal_tag()
+    built = open(stamp).read() if os.path.exists(stamp) else ""
+    if not force and built == tag and not _stale(MARSHAL, [src, os.path.join(INCLUDE, "hm.h")]):
         return MARSHAL
     import sysconfig
     import torch
@@ -66,7 +75,7 @@ def build_marshal(force: bool = False) -> str:
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     tmp = MARSHAL + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE,
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, '-DHM_MARSHAL_TAG="%s"' % tag, "-I", INCLUDE,
            "-I", os.path.join(base, "include"), "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
            "-I", cuda, "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", os.path.join(base, "lib"),
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
@@ -74,6 +83,9 @@ def build_marshal(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("%s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
     os.replace(tmp, MARSHAL)
+    os.makedirs(OBJDIR, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(tag)
     return MARSHAL
 
 

@@ -289,4 +289,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal(void) { return PyModule_Create(&module); }
+// built_for: the torch and Python whose objects this build knows (the binding compares)
+PyMODINIT_FUNC PyInit__marshal(void) {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", HM_MARSHAL_TAG) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
