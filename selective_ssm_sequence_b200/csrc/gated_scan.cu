@@ -16,8 +16,10 @@
 // tokens once more out of registers.  So each input is read once from HBM in
 // one launch without scratch (but for the backward of long sequences of few
 // channels), and every sum has a fixed order.
+#include <mutex>
 #include <type_traits>
 
+#include "cluster_fit.h"
 #include "packed.cuh"
 #include "tc_common.cuh"
 
@@ -1222,26 +1224,68 @@ bool word_rows(const void *p, size_t es, int64_t B, int64_t L, int64_t sb, int64
     return es == 4 || (aligned_to(p, 4) && (L <= 1 || st % 2 == 0) && (B <= 1 || sb % 2 == 0));
 }
 
+struct ClusterLaunch {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at{};
+    ClusterLaunch(int64_t units, Split sp, size_t smem, cudaStream_t s) {
+        cfg.gridDim = dim3((unsigned)(units * sp.cluster));
+        cfg.blockDim = dim3(sp.warps * 32);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = sp.cluster;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+    }
+    ClusterLaunch(const ClusterLaunch &) = delete;
+};
+
+// Whether the current device has a place for one such cluster (of more blocks
+// than every device takes).  Asked once per kernel, device and launch shape.
+template <typename K>
+bool has_place(K kernel, Split sp, size_t smem) {
+    struct Entry {
+        const void *kernel;
+        int dev, cluster;
+        size_t smem;
+        bool fits;
+    };
+    static std::mutex mu;
+    static Entry known[64];
+    static int n_known = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const void *k = reinterpret_cast<const void *>(kernel);
+    std::lock_guard<std::mutex> g(mu);
+    for (int i = 0; i < n_known; ++i) {
+        const Entry &e = known[i];
+        if (e.kernel == k && e.dev == dev && e.cluster == sp.cluster && e.smem == smem) return e.fits;
+    }
+    const ClusterLaunch l(1, sp, smem, nullptr);
+    int n = 0;
+    const bool fits = tc::ensure_smem_limit(kernel, (int)smem) == cudaSuccess &&
+                      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                      cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) == cudaSuccess && n > 0;
+    if (!fits) cudaGetLastError();         // a question's error is no launch's
+    if (n_known < 64) known[n_known++] = {k, dev, sp.cluster, smem, fits};
+    return fits;
+}
+
+// sp with a cluster that has a place; smem_of(cluster): shared memory of a block
+template <typename K, typename S>
+Split placed(K kernel, Split sp, S smem_of) {
+    sp.cluster = placeable_cluster(
+        sp.cluster, [&](int n) { return has_place(kernel, Split{sp.warps, n}, smem_of(n)); });
+    return sp;
+}
+
 template <typename K, typename... A>
 cudaError_t launch_cluster(K kernel, int64_t units, Split sp, size_t smem, cudaStream_t s, A... args) {
     cudaError_t e = tc::ensure_smem_limit(kernel, (int)smem);
     if (e != cudaSuccess) return e;
-    if (sp.cluster > 8) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(units * sp.cluster));
-    cfg.blockDim = dim3(sp.warps * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = sp.cluster;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    const ClusterLaunch l(units, sp, smem, s);
+    e = cudaLaunchKernelEx(&l.cfg, kernel, args...);
     if (e == cudaSuccess) count_launches(1);
     return e;
 }
@@ -1275,9 +1319,12 @@ extern "C" hm_status hm_gated_scan_fwd(const hm_gated_scan_args *a, hm_stream_t 
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int S = decltype(sc)::value;
         auto go = [&](auto kernel, int tiles, int pitch = kCols) {
-            const size_t smem = (size_t)tiles * rows * pitch * sizeof(T) +
-                                (size_t)2 * (sp.warps + sp.cluster) * 32 * sizeof(Map2);
-            return launch_cluster(kernel, units, sp, smem, (cudaStream_t)stream, mdt, mx, my, f, sp.cluster, err);
+            auto smem_of = [&](int cluster) {
+                return (size_t)tiles * rows * pitch * sizeof(T) + (size_t)2 * (sp.warps + cluster) * 32 * sizeof(Map2);
+            };
+            const Split at = placed(kernel, sp, smem_of);
+            return launch_cluster(kernel, units, at, smem_of(at.cluster), (cudaStream_t)stream, mdt, mx, my, f,
+                                  at.cluster, err);
         };
         auto by_mode = [&](auto w) {
             constexpr int W = decltype(w)::value;
@@ -1316,8 +1363,7 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
         const Split sp{kWb, two ? 1 : splits};
         if (units * splits > 0x7fffffffLL)
             return fail_args(HM_ERR_UNSUPPORTED, "gated_scan_bwd: B * D / 64 is too large");
-        shares = a->B * splits;
-        if (two) f.maps = f.part + shares * 2 * a->D;
+        if (two) f.maps = f.part + a->B * splits * 2 * a->D;
         const size_t es = esize(a->io_dtype);
         struct {
             const void *p;
@@ -1340,8 +1386,10 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
             using T = std::remove_pointer_t<decltype(tp)>;
             constexpr int S = decltype(sc)::value;
             const int pitch = !wide && !words ? Lanes<__nv_bfloat16, kOdd>::kPitch : kCols;
-            const size_t smem = (size_t)kBwdStages * 3 * kChunk * pitch * sizeof(T) +
-                                (size_t)2 * (2 * kWb + sp.cluster) * 32 * sizeof(Map2);
+            auto smem_of = [&](int cluster) {
+                return (size_t)kBwdStages * 3 * kChunk * pitch * sizeof(T) +
+                       (size_t)2 * (2 * kWb + cluster) * 32 * sizeof(Map2);
+            };
             auto go = [&](auto kernel, auto adjoint) {
                 if (two) {
                     adjoint<<<(unsigned)((units * f.nchunk + 3) / 4), 128, 0, s>>>(f);
@@ -1350,8 +1398,11 @@ extern "C" hm_status hm_gated_scan_bwd(const hm_gated_scan_bwd_args *a, hm_strea
                     const cudaError_t e = cudaGetLastError();
                     if (e != cudaSuccess) return e;
                 }
-                return launch_cluster(kernel, units * (two ? splits : 1), sp, smem, s, t[0].map, t[1].map, t[2].map,
-                                      t[3].map, t[4].map, f, splits, err);
+                const Split at = placed(kernel, sp, smem_of);
+                const int blocks = two ? splits : at.cluster;      // of a unit; the workspace is for `splits` or fewer
+                shares = a->B * blocks;
+                return launch_cluster(kernel, units * (two ? splits : 1), at, smem_of(at.cluster), s, t[0].map,
+                                      t[1].map, t[2].map, t[3].map, t[4].map, f, blocks, err);
             };
             if (wide) return go(gated_bwd_kernel<T, S, kTma>, gated_adjoint_kernel<T, kTma>);
             if (words) return go(gated_bwd_kernel<T, S, kAsync>, gated_adjoint_kernel<T, kAsync>);

@@ -69,3 +69,40 @@ def test_one_token(hm, bias):
     h, y, A = torch.ones_like(x), torch.zeros_like(x), torch.zeros(40, device="cuda")
     hm.hm_gated_scan_step(hm.gated_step_args(x, x, y, h, h, A, dt_bias=torch.full_like(A, bias)))
     assert torch.equal(y, x) and torch.equal(h, x)
+
+
+FIRST_CALL = r"""
+import torch
+import selective_ssm_sequence_b200 as hm
+B, L, D = 1, 4096, 128       # few channels: clusters of 16
+g = torch.Generator(device="cuda").manual_seed(3)
+x, dt, dy = (torch.randn(B, L, D, generator=g, device="cuda").bfloat16() for _ in range(3))
+A, dA, y, dx, ddt = torch.zeros(D, device="cuda"), torch.zeros(D, device="cuda"), *(torch.zeros_like(x) for _ in range(3))
+a = hm.gated_scan_args(x, dt, y, A)
+st = hm.alloc_workspace(hm.hm_gated_scan_states_size(a))
+a = hm.gated_scan_args(x, dt, y, A, states=st)
+b = hm.gated_scan_bwd_args(x, dt, dy, dx, ddt, A, dA, st)
+ws = hm.alloc_workspace(hm.hm_gated_scan_bwd_workspace_size(b))
+b = hm.gated_scan_bwd_args(x, dt, dy, dx, ddt, A, dA, st, workspace=ws)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    hm.hm_gated_scan_fwd(a)
+    hm.hm_gated_scan_bwd(b)
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (y, dx, ddt, dA)]
+hm.hm_gated_scan_fwd(a)
+hm.hm_gated_scan_bwd(b)
+assert all(torch.equal(s, t) for s, t in zip(got, (y, dx, ddt, dA))) and dA.abs().sum() > 0
+assert hm.hm_get_device_error() == hm.HM_OK
+"""
+
+
+def test_a_process_whose_first_call_is_captured():
+    """What the library asks the device about clusters of 16 it may ask while a stream is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
