@@ -591,8 +591,10 @@ HM_API hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_t st
  * the output is the input).  transpose != 0 applies the transposed matrix
  * instead (angle -phi, same mscale): the gradient of the inputs from that of
  * the outputs.  Angles are reduced modulo a full turn in 64-bit integers, so
- * far positions keep their precision (any int64 position, negative ones too;
- * the angle is off by at most |pos| theta_i 2^-48 plus 2^-26 of a turn).
+ * far positions keep their precision: for any int64 position, negative ones too,
+ * and bases (NTK: with its factor) up to 2^20 the angle is off by at most |pos|
+ * (theta_i 2^-47 + 2^-62) plus 2^-26 of a turn; the first share is that of fp64
+ * frequencies, the second that of their 64-bit fractions of a turn.
  * q [B, L, Hq, d] and k [B, L, Hk, d] of io_dtype, heads' elements contiguous,
  * other strides in elements; Hk = 0 leaves k out.  positions: device int64,
  * that of (b, t) at positions[b * pos_stride_b + t * pos_stride_t]; NULL:
