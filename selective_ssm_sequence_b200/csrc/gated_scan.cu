@@ -50,8 +50,9 @@ __device__ __forceinline__ float sqrt_approx(float x) {
     return r;
 }
 
-// The issue slots and the special-function unit bound this pass as much as
-// HBM does, so the gates are formed in the log2 domain with two
+// Latency bounds this pass at the 16 warps that an SM holds of it (half of the
+// issue slots and a third of the special-function unit are used), so fewer
+// instructions are less time: the gates are formed in the log2 domain with two
 // special-function instructions per element (three with HM_INPUT_UNIT) and
 // packed fp32 arithmetic:
 //   e = 2^-|z'|, z' = z / ln 2;   softplus(z) / ln 2 = max(z', 0) + log2(1 + e)
@@ -107,7 +108,7 @@ __device__ __forceinline__ Gate2 gates2(F2 dt, const ChanParams &p) {
 }
 
 // beta^2 = 1 - a^2 = 1 - 2^w, w = 2 la.  Above -1/2 it is -w times a degree-4
-// polynomial fitted to (2^w - 1) / w (relative error 1.3e-8), since the
+// polynomial fitted to (2^w - 1) / w (relative error 3.2e-8), since the
 // difference would lose the bits of a step that hardly decays.
 __device__ __forceinline__ F2 unit_sq(const Gate2 &g) {
     const F2 w = g.la + g.la;
@@ -135,7 +136,6 @@ template <>
 struct Raw<__nv_bfloat16> {
     uint32_t w;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint32_t *>(p); }
-    __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint32_t *>(p) = w; }
     __device__ __forceinline__ void set(float x, float y) { w = tc::pack_bf16x2(x, y); }
     __device__ __forceinline__ F2 pair() const { return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
 };
@@ -143,7 +143,6 @@ template <>
 struct Raw<float> {
     float2 w;
     __device__ __forceinline__ void load(const float *p) { w = *reinterpret_cast<const float2 *>(p); }
-    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float2 *>(p) = w; }
     __device__ __forceinline__ void set(float x, float y) { w = make_float2(x, y); }
     __device__ __forceinline__ F2 pair() const { return pk(w.x, w.y); }
 };
@@ -216,8 +215,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// 16 bytes into block `rank`'s shared memory (at this block's address `dst`),
-// counted by that block's mbarrier `bar`
 // a run's (A, B), 16 bytes per lane
 struct __align__(16) Map2 {
     F2 A, B;
@@ -576,8 +573,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // the c that enters each chunk, and here every chunk stands for itself; dt and
 // dy are read twice.
 //
-// 4 x 2048 x 2048 bf16: 56 us, 108 instructions per channel pair and token, 45 %
-// of the issue slots: bound by latency at 16 warps per SM.
+// 4 x 2048 x 2048 bf16: 62 us with the sums below (8 x 4096 x 2048 without a
+// cluster 176, 1 x 32768 x 2048 in clusters of 8 264), 110 instructions per channel
+// pair and token in half of the issue slots, no pipe above 35 %: bound by latency
+// at 16 warps per SM.
 template <typename T, int SCALE, int MODE>
 __global__ void __launch_bounds__(kWb * 32, 2)
 gated_bwd_kernel(const __grid_constant__ CUtensorMap map_dt, const __grid_constant__ CUtensorMap map_x,

@@ -643,8 +643,8 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes
 // (from L1, 8 columns a thread, they cost 91 us in place of 77).  8192 x 2048
 // layer norms: 77 us against 95 with a row in registers, RMS 67 against 98, 4096 x
 // 4096 68 against 109, 32768 x 512 77 against 83; fp32 rows, with pieces of their
-// own half as wide, gained nothing.  What is left: issue slots and latency at
-// 16 warps per SM.
+// own half as wide, gained nothing.  What is left is latency at 16 warps per SM
+// (52 % of the issue slots, half of what L1 and shared memory can move).
 //
 // FAR: rows of 4096 to 8192 columns of either type, one at a time over 1024
 // threads, whose registers have no room for rows nor sums: the parameter
