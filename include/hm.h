@@ -545,9 +545,9 @@ HM_API hm_status hm_norm_gate_fwd(const hm_norm_gate_args *a, hm_stream_t stream
  * the forward stored (statistics are recomputed).  dxn NULL: xn was not used
  * (r_out is then not read and may be NULL); dr_out NULL: r_out was not used
  * after xn; not both.  Parameter gradients are fp32 [D], each nullable, summed
- * over the rows in a fixed order.  dr may alias dr_out or dxn, dy may alias y,
- * dgate may alias gate, with the same strides; an output that is another input's
- * or another output's array, or an input's with another stride, is refused.
+ * over the rows in a fixed order.  With the same strides dy may alias any input,
+ * dgate any but y, and dr may alias r_out, dr_out or dxn; other aliases among the
+ * row arrays, and those with other strides, are refused.
  */
 typedef struct {
     int64_t rows, D;

@@ -968,9 +968,9 @@ hm_status check_row(const char *who, const Row &r, int64_t rows, int64_t D, size
     return HM_OK;
 }
 
-// What an output may lie over.  A row is read whole before any of it is
-// written, so an input with the same row stride may be an output's array; with
-// other strides one row's output would fall on another's input.
+// What an output may lie over.  An input that a row's thread has read for the
+// last time before it writes the output may be the output's array, with the same
+// stride: with others one row's output would fall on another's input.
 hm_status check_over(const char *who, int64_t rows, const Row &out, const Row &in, bool allowed) {
     if (rows == 0 || !out.p || out.p != in.p) return HM_OK;
     if (!allowed) return fail_args(HM_ERR_INVALID_ARG, "%s: %s must not be %s", who, out.name, in.name);
@@ -1157,9 +1157,10 @@ extern "C" hm_status hm_norm_gate_bwd(const hm_norm_gate_bwd_args *a, hm_stream_
         vec = vec && wide(r, es);
     }
     for (int o = 5; o < 8; ++o) {
-        // dy over y; dgate over gate; dr over dr_out or dxn (wide rows are read again after other outputs)
+        // a row's outputs leave in the order dr, dgate, dy, and wide rows are read again in between:
+        // gate behind dr, y behind both
         for (int i = 0; i < 5; ++i)
-            HM_TRY(check_over(w, a->rows, rows[o], rows[i], o == 5 ? i == 0 : o == 6 ? i == 1 : i >= 3));
+            HM_TRY(check_over(w, a->rows, rows[o], rows[i], o == 5 || (o == 6 ? i > 0 : i > 1)));
         for (int i = 5; i < o; ++i) HM_TRY(check_over(w, a->rows, rows[o], rows[i], false));
     }
     const void *params[] = {a->scale, a->post_w, a->post_b, a->pre_w, a->dscale, a->dpost_w, a->dpost_b, a->dpre_w,

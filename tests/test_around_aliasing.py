@@ -34,7 +34,8 @@ def test_seam_forward(hm, out, inp):        # noqa: F811
     assert "misaligned parameter" in _detail(hm, "hm_norm_gate_fwd", one)
 
 
-ALLOWED = {("dy", "y"), ("dgate", "gate"), ("dr", "dr_out"), ("dr", "dxn")}
+ALLOWED = {("dy", n) for n in ("y", "gate", "r_out", "dr_out", "dxn")}
+ALLOWED |= {("dgate", n) for n in ("gate", "r_out", "dr_out", "dxn")} | {("dr", n) for n in ("r_out", "dr_out", "dxn")}
 
 
 @pytest.mark.parametrize("out", ["dy", "dgate", "dr"])

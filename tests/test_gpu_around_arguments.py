@@ -86,6 +86,32 @@ def test_seam_forward_in_place(hm, io, n, D):
                 assert torch.equal(t[i], o) and torch.equal(t[j], x), (i, j)
 
 
+@pytest.mark.parametrize("io,n,D", [("bf16", 37, 64), ("bf16", 301, 2048), ("bf16", 150, 6000), ("bf16", 9, 302),
+                                    ("f32", 7, 8192), ("f32", 11, 1001), ("bf16", 5, 16384)])
+def test_seam_backward_in_place(hm, io, n, D):
+    """Each output over each input that the header lets it lie over, in each form of the backward:
+    the same bits; and two or three of them at once."""
+    import torch
+    names = ("y", "gate", "r_out", "dr_out", "dxn")
+    src = {k: dev_tensor(_rand(k, (n, D)), io) for k in names}
+
+    def run(t, dy, dgate, dr):
+        d = {k: torch.empty(D, device="cuda") for k in ("dscale", "dpost_w", "dpre_b")}
+        kw = dict(gate=t["gate"], dgate=dgate, norm=hm.HM_NORM_LAYER, alpha=0.7, **d)
+        b = hm.norm_gate_bwd_args(t["y"], t["r_out"], t["dr_out"], t["dxn"], dy, dr, **kw)
+        ws = hm.alloc_workspace(hm.hm_norm_gate_bwd_workspace_size(b))
+        hm.hm_norm_gate_bwd(hm.norm_gate_bwd_args(t["y"], t["r_out"], t["dr_out"], t["dxn"], dy, dr, workspace=ws, **kw))
+        return [dy, dgate, dr, *d.values()]
+    want = run(src, *(torch.empty_like(src["y"]) for _ in range(3)))
+    may = {0: names, 1: names[1:], 2: names[2:]}
+    plans = [{o: k} for o in range(3) for k in may[o]]
+    plans += [{0: "y", 1: "gate", 2: "r_out"}, {0: "dxn", 1: "dr_out", 2: "r_out"}, {0: "gate", 1: "r_out", 2: "dxn"}]
+    for plan in plans:
+        t = {k: v.clone() for k, v in src.items()}
+        out = [t[plan[o]] if o in plan else torch.empty_like(src["y"]) for o in range(3)]
+        assert all(torch.equal(a, b) for a, b in zip(run(t, *out), want)), plan
+
+
 @pytest.fixture(params=["native", "python"])
 def filler(hm, monkeypatch, request):
     """With the native filler, and with the helpers on their own."""
